@@ -1,0 +1,482 @@
+"""The operators around the 4-bit KV cache as their users call them, for measurement and comparison.
+
+append   rotary positions on queries and keys, keys and values quantised to 4 bits and written to the cache
+attend   attention of the rotated queries over the cache (optionally accumulating every entry's softmax weight)
+evict    the prefix entries of largest accumulated weight, compacted into another cache row
+
+With `own` false the operators are computed in plain torch operations in 32 bits; with `own` true through the
+library's entry points.  `exact` gives the definition in 64 bits.
+"""
+import math
+
+import torch
+
+own = False
+
+DTYPES = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+DT_CODE = {"f32": 0, "f16": 1, "bf16": 2}
+GROUP = 32  # dimensions that share a scale and a minimum
+
+
+# ------------------------------------------------------------------ cases
+def _append(name, n, chunk, start, P, heads, dim, q_heads, dtype, layout, rope_dims, scaling, factor):
+    return dict(name=name, op="append", n=n, chunk=chunk, start=start, P=P, R=128, heads=heads, dim=dim, q_heads=q_heads,
+                dtype=dtype, layout=layout, rope_dims=rope_dims, scaling=scaling, factor=factor)
+
+
+def _attend(name, n, chunk, start, P, heads, dim, q_heads, sink, track, out):
+    return dict(name=name, op="attend", n=n, chunk=chunk, start=start, P=P, R=128, heads=heads, dim=dim, q_heads=q_heads,
+                sink=sink, track=track, out=out)
+
+
+def _evict(name, layers, rows, P, n, keep, protect, heads, dim):
+    return dict(name=name, op="evict", layers=layers, rows=rows, P=P, R=128, n=n, keep=keep, protect=protect, heads=heads,
+                dim=dim)
+
+
+def listed():
+    return [
+        # one token of one page: the latency of the smallest call (10 x 128 heads, 289 cached positions)
+        _append("append one token", 1, False, 300, 289, 10, 128, 10, "f16", "half", 128, "none", 1.0),
+        # the widest decode step, each row at its own position, interleaved pairs on half of the head
+        _append("append 64 rows", 64, False, 2048, 2048, 10, 128, 10, "bf16", "interleaved", 64, "none", 1.0),
+        # a page's prompt in one call
+        _append("append prompt", 2048, True, 0, 2048, 10, 128, 10, "f16", "half", 128, "none", 1.0),
+        # the tail of a long document, frequencies scaled for it, shared key/value heads, fp32 projections
+        _append("append long prompt", 4099, True, 28001, 32768, 2, 128, 16, "f32", "half", 128, "yarn", 8.0),
+        # one token over a short prompt: latency
+        _attend("attend one row", 1, False, 64, 64, 10, 128, 10, False, False, "f16"),
+        # the sink decoder's serving shape: 24 rows, 8 x 64 heads, 3000 cached positions
+        _attend("attend sink rows", 24, False, 3000, 3000, 8, 64, 8, True, False, "f16"),
+        # the 64-row decode step over 2048 cached positions and a full ring, weights accumulated for the eviction
+        _attend("attend 64 rows tracked", 64, False, 2300, 2048, 10, 128, 10, False, True, "f16"),
+        # few rows over a long document, shared key/value heads
+        _attend("attend long shared heads", 2, False, 60013, 60001, 4, 128, 32, False, False, "bf16"),
+        # causal attention of a page's prompt after its append
+        _attend("attend prompt", 2048, True, 0, 2048, 10, 128, 10, False, False, "f16"),
+        # one page, one layer, a short prefix
+        _evict("evict one row", 1, 1, 289, 289, 64, 4, 10, 128),
+        # a batch of pages, one layer
+        _evict("evict 32 rows", 1, 32, 2048, 2048, 512, 4, 10, 128),
+        # every layer of a decoder at once, an odd prefix
+        _evict("evict all layers", 12, 8, 3001, 3000, 701, 1, 10, 128),
+    ]
+
+
+def _log(rng, lo, hi):
+    return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+
+def draw(rng):
+    op = rng.choice(["append", "attend", "attend", "evict"])
+    dim = rng.choice([32, 64, 64, 128, 128, 256])
+    heads = max(1, min(_log(rng, 1, 16), 2048 // dim))
+    if heads * dim % 64:
+        heads += 1
+    if op == "append":
+        group = rng.choice([1, 1, 1, 2, 4, 8])
+        chunk = rng.random() < 0.5
+        P = _log(rng, 1, 20000)
+        n = _log(rng, 1, max(1, min(P, 8192 * 1024 // (heads * dim * (group + 2))))) if chunk else _log(rng, 1, 64)
+        start = rng.randrange(0, P + 128 - n + 1) if chunk else P + rng.randrange(0, 300)
+        scaling = rng.choice(["none", "linear", "yarn"])
+        return _pure(_append("", n, chunk, start, P, heads, dim, heads * group, rng.choice(list(DTYPES)),
+                             rng.choice(["half", "interleaved"]), 2 * rng.randrange(1, dim // 2 + 1), scaling,
+                             1.0 if scaling == "none" else rng.choice([2.0, 4.0, 8.0, 32.0])))
+    if op == "attend":
+        chunk = rng.random() < 0.4
+        group = rng.choice([1, 1, 2, 3, 4, 8])
+        if chunk:
+            P = _log(rng, 1, 2048)
+            n = _log(rng, 1, P)
+            while n * P * heads * dim * group > 2048 * 2048 * 1280:
+                n = max(1, n // 2)
+                P = max(n, P * 3 // 4)
+            start = rng.randrange(0, P + 128 - n + 1)
+        else:
+            n = _log(rng, 1, 64)
+            P = _log(rng, 1, max(1, min(60000, 64 * 2176 * 1280 // (n * heads * dim))))
+            start = max(0, P + rng.randrange(-(P // 2), 300))
+        return _pure(_attend("", n, chunk, start, P, heads, dim, heads * group, rng.random() < 0.4, rng.random() < 0.4,
+                             rng.choice(list(DTYPES))))
+    rows, layers = _log(rng, 1, 32), _log(rng, 1, 12)
+    P = max(2, min(_log(rng, 2, 6000), 12 * 8 * 3000 * 1280 // (rows * layers * heads * dim)))
+    n = rng.randrange(max(1, P // 2), P + 1)
+    keep = rng.randrange(1, max(1, n // 2) + 1)
+    return _pure(_evict("", layers, rows, P, n, keep, rng.randrange(0, min(keep, 8) + 1), heads, dim))
+
+
+def _pure(c):
+    del c["name"]
+    return c
+
+
+# ------------------------------------------------------------------ rotary frequencies
+def _inv_freq(c, device):
+    rd = c["rope_dims"]
+    i = torch.arange(rd // 2, dtype=torch.float64, device=device)
+    inv = 10000.0 ** (-2.0 * i / rd)
+    amp = 1.0
+    if c["scaling"] == "linear":
+        inv = inv / c["factor"]
+    elif c["scaling"] == "yarn":
+        turns = lambda b: rd * math.log(4096 / (2 * math.pi * b)) / (2 * math.log(10000.0))  # noqa: E731
+        lo = min(max(math.floor(turns(32.0)), 0), rd // 2 - 1)
+        hi = min(max(math.ceil(turns(1.0)), 0), rd // 2 - 1)
+        ramp = ((i - lo) / max(hi - lo, 1e-3)).clamp(0, 1)
+        inv = inv * ((1 - ramp) + ramp / c["factor"])
+        amp = 0.1 * math.log(c["factor"]) + 1.0
+    return inv, amp
+
+
+def _slots(pos, P, R):
+    return torch.where(pos < P, pos, P + (pos - P) % R)
+
+
+# ------------------------------------------------------------------ states
+def _codes(g, shape):
+    """A cache's entries as stored: codes, scale and minimum of every group (heavy and light channels among them)."""
+    code = torch.randint(0, 16, shape, generator=g, device="cuda", dtype=torch.uint8)
+    small = shape[:-1] + (shape[-1] // GROUP,)
+    s = (0.1 + 0.4 * torch.rand(small, generator=g, device="cuda")).half()
+    m = (-7.5 * s.float() + 0.3 * torch.randn(small, generator=g, device="cuda")).half()
+    return code, s, m
+
+
+def _context(c, layers, rows):
+    from quantized_moe_decode_gb300 import binding, synth
+
+    kw = dict(hidden=64, n_heads=c["heads"], head_dim=c["dim"], n_layers=layers, n_dense_layers=layers, dense_inter=64,
+              prefix_len=c["P"], ring_len=c["R"], max_rows=rows, kv_int4=1, kv_track=int(c.get("track", c["op"] == "evict")),
+              use_sink=int(c.get("sink", False)))
+    if c["op"] == "append":
+        kw |= dict(rope_layout=int(c["layout"] == "interleaved"), rope_dims=c["rope_dims"],
+                   rope_scaling={"none": 0, "linear": 1, "yarn": 2}[c["scaling"]], rope_factor=c["factor"], rope_orig_len=4096)
+    return binding.Context(synth.ModelConfig(**kw), max_rows=rows)
+
+
+def prepare(case, seed):
+    """What a serving program holds: the inputs of the call on the GPU and the cache (for `own`, a context that owns it)."""
+    c = dict(case)
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    st = dict(c=c)
+    h, D, P, R = c["heads"], c["dim"], c["P"], c["R"]
+    SL = P + R
+    if c["op"] == "append":
+        dt, n = DTYPES[c["dtype"]], c["n"]
+        gain = torch.exp(0.3 * torch.randn(h + c["q_heads"] + h, D, generator=g, device="cuda"))
+        x = torch.randn(n, c["q_heads"] + 2 * h, D, generator=g, device="cuda") * gain
+        st["qkv"] = x.to(dt)  # one fused projection output, sliced without a copy
+        if not c["chunk"]:
+            st["pos"] = (c["start"] + torch.randint(0, 64, (n,), generator=g, device="cuda")).int()
+        rows = 1 if c["chunk"] else n
+        if own:
+            st["ctx"] = _context(c, 1, rows)
+        else:
+            small = (rows, 2, h, SL, D // GROUP)
+            st["code"] = torch.zeros((rows, 2, h, SL, D), dtype=torch.uint8, device="cuda")
+            st["scale"], st["low"] = torch.zeros(small, device="cuda").half(), torch.zeros(small, device="cuda").half()
+        return st
+    if c["op"] == "attend":
+        n, rows = c["n"], 1 if c["chunk"] else c["n"]
+        st["q"] = torch.randn(n, c["q_heads"], D, generator=g, device="cuda")
+        if not c["chunk"]:
+            back = torch.randint(0, max(1, min(64, c["start"] + 1)), (n,), generator=g, device="cuda")
+            st["pos"] = (c["start"] - back).int()
+        code, s, m = _codes(g, (rows, 2, h, SL, D))
+        sink = torch.randn(1, h, generator=g, device="cuda") if c["sink"] else None
+        if own:
+            ctx = st["ctx"] = _context(c, 1, rows)
+            for r in range(rows):
+                ctx.uocr_kv_write_i4(r, 0, 0, code[r, 0], s[r, 0], m[r, 0], code[r, 1], s[r, 1], m[r, 1])
+            if c["sink"]:
+                ctx.uocr_set_sinks(sink.cpu().numpy())
+        else:
+            st |= dict(code=code, scale=s, low=m, sink=sink, weights=torch.zeros(rows, h, SL, device="cuda"))
+        return st
+    L, rows, n = c["layers"], c["rows"], c["n"]
+    w = torch.exp(2.0 * torch.randn(L, rows, h, n, generator=g, device="cuda"))
+    w = (w * 64).round() / 64  # accumulated weights with ties among the light entries
+    if own:
+        ctx = st["ctx"] = _context(c, L, 2 * rows)
+    else:
+        st |= dict(weights=w, code=[], scale=[], low=[])
+    for layer in range(L):
+        code, s, m = _codes(g, (rows, 2, h, n, D))
+        if own:
+            for r in range(rows):
+                ctx.uocr_kv_write_i4(r, layer, 0, code[r, 0], s[r, 0], m[r, 0], code[r, 1], s[r, 1], m[r, 1])
+        else:
+            st["code"].append(code), st["scale"].append(s), st["low"].append(m)
+    if own:
+        ctx.uocr_kv_weights_write(-1, 0, rows, 0, n, w.data_ptr())
+    else:
+        st |= {k: torch.stack(st[k]) for k in ("code", "scale", "low")}
+    return st
+
+
+# ------------------------------------------------------------------ plain forms
+def _rotate(x, cos, sin, c):
+    """x [n, heads, D] in fp32; cos, sin [n, rd/2]."""
+    rd = c["rope_dims"]
+    y = x.clone()
+    a, b = (x[..., 0:rd:2], x[..., 1:rd:2]) if c["layout"] == "interleaved" else (x[..., :rd // 2], x[..., rd // 2:rd])
+    cos, sin = cos[:, None, :], sin[:, None, :]
+    u, v = a * cos - b * sin, b * cos + a * sin
+    if c["layout"] == "interleaved":
+        y[..., 0:rd:2], y[..., 1:rd:2] = u, v
+    else:
+        y[..., :rd // 2], y[..., rd // 2:rd] = u, v
+    return y
+
+
+def _quantise(x):
+    """x [..., D] in fp32 -> codes, scale, minimum (fp16)."""
+    g = x.reshape(x.shape[:-1] + (-1, GROUP))
+    m = g.amin(-1).half()
+    t = ((g.amax(-1) - m.float()) / 15.0).clamp(min=0)
+    s = t.half()
+    s = (s.view(torch.int16) - (s.float() > t).to(torch.int16)).view(torch.float16)  # toward zero
+    sf = s.float()[..., None]
+    q = torch.where(sf > 0, ((g - m.float()[..., None]) / torch.where(sf > 0, sf, torch.ones_like(sf))).round().clamp(0, 15),
+                    torch.zeros_like(g))
+    return q.to(torch.uint8).reshape(x.shape), s, m
+
+
+def _value(code, s, m):
+    g = code.reshape(code.shape[:-1] + (-1, GROUP)).float()
+    return (s.float()[..., None] * g + m.float()[..., None]).half().reshape(code.shape)
+
+
+def _plain_append(st):
+    c = st["c"]
+    n, h, qh = c["n"], c["heads"], c["q_heads"]
+    pos = torch.arange(c["start"], c["start"] + n, device="cuda") if c["chunk"] else st["pos"].long()
+    inv, amp = _inv_freq(c, "cuda")
+    ang = pos.double()[:, None] * inv
+    cos, sin = (amp * torch.cos(ang)).float(), (amp * torch.sin(ang)).float()
+    x = st["qkv"].float()
+    q = _rotate(x[:, :qh], cos, sin, c)
+    kv = torch.stack([_rotate(x[:, qh:qh + h], cos, sin, c), x[:, qh + h:]], 1)  # [n, 2, h, D]
+    code, s, m = _quantise(kv)
+    slot = _slots(pos, c["P"], c["R"])
+    row = torch.zeros_like(slot) if c["chunk"] else torch.arange(n, device="cuda")
+    for name, t in (("code", code), ("scale", s), ("low", m)):
+        st[name][row, :, :, slot] = t
+    val = _value(code, s, m)
+    return dict(q=q, k=val[:, 0], v=val[:, 1])
+
+
+def _live(c, pos):
+    """[n, P + R]: the slots that a query at each position reads."""
+    P, R = c["P"], c["R"]
+    lim = torch.where(pos < P, pos + 1, P + (pos - P + 1).clamp(max=R))
+    return torch.arange(P + R, device=pos.device)[None, :] < lim[:, None]
+
+
+def _plain_attend(st):
+    c = st["c"]
+    n, h, D, G = c["n"], c["heads"], c["dim"], c["q_heads"] // c["heads"]
+    kv = _value(st["code"], st["scale"], st["low"]).float()  # [rows, 2, h, SL, D]
+    pos = torch.arange(c["start"], c["start"] + n, device="cuda") if c["chunk"] else st["pos"].long()
+    q = st["q"].reshape(n, h, G, D)
+    live = _live(c, pos)
+    if c["chunk"]:
+        q = q.permute(1, 0, 2, 3).reshape(1, h, n * G, D)
+        live = live[:, None, :].expand(n, G, -1).reshape(1, 1, n * G, -1)
+    else:
+        live = live[:, None, None, :]
+    score = torch.matmul(q, kv[:, 0].transpose(-1, -2)) * (1.0 / math.sqrt(D))
+    score = score.masked_fill(~live, -math.inf)
+    top = score.amax(-1, keepdim=True)
+    if c["sink"]:
+        sink = st["sink"].reshape(1, h, 1, 1)
+        top = torch.maximum(top, sink)
+    e = torch.exp(score - top)
+    z = e.sum(-1, keepdim=True)
+    if c["sink"]:
+        z = z + torch.exp(sink - top)
+    p = e / z
+    out = torch.matmul(p, kv[:, 1])
+    out = out.reshape(h, n, G, D).permute(1, 0, 2, 3) if c["chunk"] else out
+    out = out.reshape(n, h * G, D).to(DTYPES[c["out"]])
+    if not c["track"]:
+        return dict(out=out)
+    st["weights"] += p.sum(-2)
+    return dict(out=out, weights=st["weights"])
+
+
+def _plain_evict(st):
+    c = st["c"]
+    w = st["weights"].clone()
+    w[..., :c["protect"]] = math.inf
+    order = torch.sort(w, dim=-1, descending=True, stable=True).indices[..., :c["keep"]]
+    kept = order.sort(-1).values  # [L, rows, h, keep]
+    at = kept[:, :, None, :, :, None].expand(-1, -1, 2, -1, -1, -1)
+    code = st["code"].gather(4, at.expand(-1, -1, -1, -1, -1, c["dim"]))
+    s = st["scale"].gather(4, at.expand(-1, -1, -1, -1, -1, c["dim"] // GROUP))
+    m = st["low"].gather(4, at.expand(-1, -1, -1, -1, -1, c["dim"] // GROUP))
+    val = _value(code, s, m)
+    return dict(kept=kept.int(), k=val[:, :, 0], v=val[:, :, 1], weights=st["weights"].gather(3, kept))
+
+
+# ------------------------------------------------------------------ the framework's calls
+def _own_append(st):
+    c, ctx, x = st["c"], st["ctx"], st["qkv"]
+    n, h, qh, D = c["n"], c["heads"], c["q_heads"], c["dim"]
+    q = torch.empty(n, qh, D, device="cuda")
+    k, v = torch.empty(n, h, D, device="cuda", dtype=torch.float16), torch.empty(n, h, D, device="cuda", dtype=torch.float16)
+    ld = (qh + 2 * h) * D
+    base, e = x.data_ptr(), x.element_size()
+    kw = dict(dtype=DT_CODE[c["dtype"]], q_heads=qh, ld_q=ld, ld_k=ld, ld_v=ld, q_out=q.data_ptr(), k_val=k.data_ptr(),
+              v_val=v.data_ptr())
+    ptrs = (base, base + qh * D * e, base + (qh + h) * D * e)
+    if c["chunk"]:
+        ctx.uocr_kv_append_chunk(0, 0, c["start"], n, *ptrs, **kw)
+    else:
+        ctx.uocr_kv_append(0, n, st["pos"].data_ptr(), *ptrs, **kw)
+    return dict(q=q, k=k, v=v)
+
+
+def _own_attend(st):
+    c, ctx, q = st["c"], st["ctx"], st["q"]
+    n, h, qh = c["n"], c["heads"], c["q_heads"]
+    out = torch.empty(n, qh, c["dim"], device="cuda", dtype=DTYPES[c["out"]])
+    if c["chunk"]:
+        ctx.uocr_attend_chunk(0, 0, c["start"], n, qh, q.data_ptr(), out.data_ptr(), DT_CODE[c["out"]])
+    else:
+        ctx.uocr_attend(0, n, st["pos"].data_ptr(), qh, q.data_ptr(), out.data_ptr(), DT_CODE[c["out"]])
+    if not c["track"]:
+        return dict(out=out)
+    rows, SL = 1 if c["chunk"] else n, c["P"] + c["R"]
+    w = torch.empty(rows, h, SL, device="cuda")
+    ctx.uocr_kv_weights_read(0, 0, rows, 0, SL, w.data_ptr())
+    return dict(out=out, weights=w)
+
+
+def _own_evict(st):
+    c, ctx = st["c"], st["ctx"]
+    L, rows, h, D, keep = c["layers"], c["rows"], c["heads"], c["dim"], c["keep"]
+    kept = torch.empty(L, rows, h, keep, device="cuda", dtype=torch.int32)
+    k = torch.empty(L, rows, h, keep, D, device="cuda", dtype=torch.float16)
+    v = torch.empty(L, rows, h, keep, D, device="cuda", dtype=torch.float16)
+    w = torch.empty(L, rows, h, keep, device="cuda")
+    ctx.uocr_kv_evict(-1, range(rows), range(rows, 2 * rows), c["n"], keep, c["protect"], kept_ptr=kept.data_ptr(),
+                      k_val_ptr=k.data_ptr(), v_val_ptr=v.data_ptr())
+    ctx.uocr_kv_weights_read(-1, rows, rows, 0, keep, w.data_ptr())
+    return dict(kept=kept, k=k, v=v, weights=w)
+
+
+def run(state):
+    op = state["c"]["op"]
+    if own:
+        return {"append": _own_append, "attend": _own_attend, "evict": _own_evict}[op](state)
+    return {"append": _plain_append, "attend": _plain_attend, "evict": _plain_evict}[op](state)
+
+
+# ------------------------------------------------------------------ floors
+def work(case):
+    c = case
+    h, D, n = c["heads"], c["dim"], c["n"]
+    entry = D // 2 + D // GROUP * 4  # bytes of one key or value vector in the cache
+    if c["op"] == "append":
+        e = 4 if c["dtype"] == "f32" else 2
+        qh = c["q_heads"]
+        return dict(bytes=n * ((qh + 2 * h) * D * e + qh * D * 4 + 2 * h * (entry + 2 * D)), flops=n * (6 * qh + 20 * h) * D)
+    if c["op"] == "attend":
+        P, R, qh = c["P"], c["R"], c["q_heads"]
+        e = 4 if c["out"] == "f32" else 2
+        live = lambda p: p + 1 if p < P else P + min(p - P + 1, R)  # noqa: E731
+        if c["chunk"]:
+            slots, pairs, rows = live(c["start"] + n - 1), sum(live(c["start"] + t) for t in range(n)), 1
+        else:
+            slots = pairs = n * live(max(0, c["start"] - 32))
+            rows = n
+        weights = (slots * 8 + rows * (P + R) * 4) * h if c["track"] else 0
+        return dict(bytes=slots * h * 2 * entry + n * qh * D * (4 + e) + weights, flops=4.0 * pairs * qh * D)
+    vec = c["layers"] * c["rows"] * h
+    return dict(bytes=vec * (n * 4 + c["keep"] * (2 * 2 * entry + 4 + 3 * 4 + 2 * 2 * D)), flops=vec * (n + c["keep"] * 4 * D))
+
+
+# ------------------------------------------------------------------ the definition in 64 bits
+def _exact_append(st):
+    c = st["c"]
+    n, h, qh, rd = c["n"], c["heads"], c["q_heads"], c["rope_dims"]
+    pos = torch.arange(c["start"], c["start"] + n, device="cuda") if c["chunk"] else st["pos"].long()
+    x = st["qkv"].double()
+    inv, amp = _inv_freq(c, "cuda")
+    turn = torch.polar(torch.full((n, rd // 2), amp, dtype=torch.float64, device="cuda"), pos.double()[:, None] * inv)
+    head, tail = x[:, :qh + h, :rd], x[:, :qh + h, rd:]
+    if c["layout"] == "interleaved":
+        z = torch.view_as_complex(head.reshape(n, qh + h, rd // 2, 2).contiguous()) * turn[:, None]
+        head = torch.view_as_real(z).reshape(n, qh + h, rd)
+    else:
+        z = torch.complex(head[..., :rd // 2].contiguous(), head[..., rd // 2:].contiguous()) * turn[:, None]
+        head = torch.cat([z.real, z.imag], -1)
+    x = torch.cat([torch.cat([head, tail], -1), x[:, qh + h:]], 1)
+
+    def stored(y):
+        y = y.reshape(n, h, -1, GROUP)
+        low = y.min(-1, keepdim=True).values.half().double()
+        step = ((y.max(-1, keepdim=True).values - low) / 15).clamp(min=0)
+        near = step.half()
+        down = torch.where(near.double() > step, (near.view(torch.int16) - 1).view(torch.float16), near).double()
+        q = torch.where(down > 0, torch.round((y - low) / down.clamp(min=1e-30)).clamp(0, 15), torch.zeros_like(y))
+        return (down * q + low).reshape(n, h, -1)
+
+    return dict(q=x[:, :qh], k=stored(x[:, qh:qh + h]), v=stored(x[:, qh + h:]))
+
+
+def _exact_attend(st):
+    c = st["c"]
+    n, h, D, G = c["n"], c["heads"], c["dim"], c["q_heads"] // c["heads"]
+    P, R = c["P"], c["R"]
+    out = torch.empty(n, h, G, D, dtype=torch.float64, device="cuda")
+    weights = torch.zeros_like(st["weights"], dtype=torch.float64)
+    positions = range(c["start"], c["start"] + n) if c["chunk"] else st["pos"].tolist()
+    step = max(1, min(n, 2 ** 25 // ((P + R) * h * G))) if c["chunk"] else 1
+    entries = None
+    for i in range(0, n, step):
+        r = 0 if c["chunk"] else i
+        if entries is None or not c["chunk"]:
+            grouped = st["scale"][r].double()[..., None] * st["code"][r].double().unflatten(-1, (-1, GROUP))
+            entries = (grouped + st["low"][r].double()[..., None]).flatten(-2).half().double()
+        j = min(n, i + step)
+        last = [p + 1 if p < P else P + min(p - P + 1, R) for p in positions[i:j]]
+        top = max(last)
+        s = torch.einsum("thgd,hsd->htgs", st["q"][i:j].double().reshape(j - i, h, G, D), entries[0, :, :top]) / math.sqrt(D)
+        hidden = torch.arange(top, device="cuda")[None] >= torch.tensor(last, device="cuda")[:, None]
+        s.masked_fill_(hidden[None, :, None], -math.inf)
+        if c["sink"]:
+            s = torch.cat([s, st["sink"].double().reshape(h, 1, 1, 1).expand(h, j - i, G, 1)], -1)
+        p = torch.softmax(s, -1)[..., :top]
+        out[i:j] = torch.einsum("htgs,hsd->thgd", p, entries[1, :, :top])
+        weights[r, :, :top] += p.sum((1, 2))
+    got = dict(out=out.reshape(n, h * G, D))
+    return got | dict(weights=weights) if c["track"] else got
+
+
+def _exact_evict(st):
+    c = st["c"]
+    n, keep = c["n"], c["keep"]
+    w = st["weights"].double()
+    slot = torch.arange(n, device="cuda")
+    # one key per entry: heavier first, then the lower slot
+    rank = (-w * 64 * 2 ** 15).round() + slot.double()
+    rank[..., :c["protect"]] = -math.inf
+    kth = torch.kthvalue(rank, keep, -1, keepdim=True).values
+    chosen = rank <= kth
+    kept = slot.expand_as(rank)[chosen].reshape(w.shape[:-1] + (keep,))
+    both = chosen[:, :, None].expand(-1, -1, 2, -1, -1)
+    shape = both.shape[:-1] + (keep,)
+    code = st["code"][both].reshape(shape + (-1, GROUP))
+    s, m = st["scale"][both].reshape(shape + (-1, 1)), st["low"][both].reshape(shape + (-1, 1))
+    val = (s.double() * code + m.double()).flatten(-2)
+    return dict(kept=kept.int(), k=val[:, :, 0], v=val[:, :, 1], weights=w[chosen].reshape(kept.shape))
+
+
+def exact(case, seed):
+    st = prepare(case, seed)
+    if "code" not in st:
+        return None
+    return {"append": _exact_append, "attend": _exact_attend, "evict": _exact_evict}[case["op"]](st)
