@@ -41,9 +41,10 @@
  *    stream is made to wait for it, so the calls are asynchronous with respect
  *    to the host unless stated otherwise.
  *  - Kernels never trap.  Invalid device-side inputs (a token id outside
- *    [0, vocab), a negative position) set bits of a device status word that
- *    uocr_sync() reports as UOCR_E_TOKEN / UOCR_E_POSITION; the offending
- *    row uses id 0 / position 0 for that step.
+ *    [0, vocab), a negative position, a position inside an evicted prefix) set
+ *    bits of a device status word that uocr_sync() reports as UOCR_E_TOKEN /
+ *    UOCR_E_POSITION; the offending row uses id 0 / position 0 for that step
+ *    (inside an evicted prefix: its key and value are not written).
  */
 #ifndef UOCR_H
 #define UOCR_H
@@ -96,6 +97,10 @@ typedef enum {
                         j<32 = low nibble of qs[j], j>=32 = high nibble of qs[j-32]
                         ([Metal] "Quantizzazione": groups of 64 values)          */
 } uocr_format;
+
+/* Rotary pairs: rotate-half (i, i + rope_dims/2) or neighbours (2i, 2i + 1). */
+typedef enum { UOCR_ROPE_HALF = 0, UOCR_ROPE_INTERLEAVED = 1 } uocr_rope_layout;
+typedef enum { UOCR_ROPE_PLAIN = 0, UOCR_ROPE_LINEAR = 1, UOCR_ROPE_YARN = 2 } uocr_rope_scaling;
 
 /* Weight tensor kinds.  Source: [Metal] "Il decoder e il Mixture of Experts"
  * (attention, one dense MLP layer, MoE layers with a router, 64 routed and 2
@@ -174,7 +179,55 @@ typedef struct {
      8192 (else uocr_create returns UOCR_E_INVALID_ARG).  Router, experts, LM
      head and projector unchanged.  0 or 1. */
   int32_t act_int8;
+  /* rotary positions of queries and keys (every cache format).  All zero: the
+     whole head in rotate-half pairs at unscaled frequencies.  Pair i of the
+     rotated dimensions turns by position * inv_i, inv_i = rope_theta^(-2i/rope_dims),
+     with rope_scaling changing inv_i and the amplitude of the turned pair:
+       UOCR_ROPE_LINEAR  inv_i / rope_factor
+       UOCR_ROPE_YARN    inv_i ((1 - r_i) + r_i / rope_factor), where r_i rises
+         linearly from 0 at pair lo to 1 at pair hi (the pairs that turn
+         rope_beta_fast and rope_beta_slow times over rope_orig_len positions:
+         d(b) = rope_dims ln(rope_orig_len / (2 pi b)) / (2 ln rope_theta),
+         lo = floor d(beta_fast), hi = ceil d(beta_slow), both clamped to
+         [0, rope_dims/2 - 1]); cos and sin are multiplied by rope_mscale      */
+  int32_t rope_layout;     /* uocr_rope_layout                                   */
+  int32_t rope_dims;       /* rotated dimensions of a head, even (0 = head_dim); the
+                              others pass through                              */
+  int32_t rope_scaling;    /* uocr_rope_scaling                                  */
+  int32_t rope_orig_len;   /* YaRN: positions the frequencies were made for      */
+  float rope_factor;       /* >= 1 with a scaling                                */
+  float rope_beta_fast;    /* YaRN, 0 = 32                                       */
+  float rope_beta_slow;    /* YaRN, 0 = 1                                        */
+  float rope_mscale;       /* YaRN amplitude, 0 = 0.1 ln(rope_factor) + 1        */
+  /* 4-bit KV cache (excludes kv_int8; head_dim >= 32).  Per group of 32
+     dimensions of a key or value vector an fp16 minimum m and scale s and 32
+     codes: m = fp16(min), s = (max - m) fp32(1/15) rounded toward zero to fp16,
+     q = clamp(round((x - m) / s), 0, 15), all decided in fp32 (s = 0: q = 0); the
+     entry's value is fp16(s q + m).  A group that holds a NaN or a value beyond the
+     fp16 range reads as NaN.  5 bits per value.                               */
+  int32_t kv_int4;         /* 0 or 1                                             */
+  int32_t kv_track;        /* 1 (needs kv_int4): attention adds every softmax weight
+                              it gives to a fp32 sum per (layer, row, head, slot),
+                              by which uocr_kv_evict chooses                    */
 } uocr_config;
+
+/* Element types of device buffers. */
+typedef enum { UOCR_DT_F32 = 0, UOCR_DT_F16 = 1, UOCR_DT_BF16 = 2 } uocr_dtype;
+
+/* Queries, keys and values of n tokens before rotation (device pointers).
+ * Token i's head h starts at q + i*ld_q + h*head_dim elements (k, v alike), so
+ * slices of one fused projection output need no copy.                       */
+typedef struct {
+  const void* q;    /* [n][q_heads][head_dim], or NULL (then q_out is NULL too)   */
+  const void* k;    /* [n][n_heads][head_dim]                                     */
+  const void* v;    /* [n][n_heads][head_dim]                                     */
+  int64_t ld_q, ld_k, ld_v; /* elements between tokens, at least a token's; 0 = dense */
+  int32_t dtype;    /* uocr_dtype of q, k and v                                   */
+  int32_t q_heads;  /* a multiple of n_heads, at most 8 n_heads (0 without q)      */
+  float* q_out;     /* fp32 [n][q_heads][head_dim]: the rotated queries           */
+  uint16_t* k_val;  /* fp16 [n][n_heads][head_dim] or NULL: the values the stored  */
+  uint16_t* v_val;  /* entries stand for, e.g. for the caller's own attention      */
+} uocr_qkv;
 
 typedef struct {
   int32_t kind;     /* uocr_tensor_kind                                   */
@@ -260,6 +313,87 @@ UOCR_API uocr_status uocr_kv_read_i8(uocr_ctx* ctx, int32_t row, int32_t layer, 
 UOCR_API uocr_status uocr_kv_write_i8(uocr_ctx* ctx, int32_t row, int32_t layer, int32_t slot0, int32_t n,
                                       const int8_t* k_codes, const float* k_scales, const int8_t* v_codes,
                                       const float* v_scales);
+
+/* ------------------------------------------------------------ 4-bit KV cache
+ * The calls below need a context with kv_int4 = 1 (else UOCR_E_STATE); none
+ * needs weights to be loaded, so they also serve a decoder whose projections
+ * are the caller's.  A step or prefill of such a context runs the same
+ * kernels.  Device pointers are aligned to their element.  Asynchronous (see
+ * conventions) unless stated otherwise; they can be captured into a graph of
+ * the caller's stream.  uocr_kv_write_prefix / uocr_kv_write quantise the given
+ * fp16 vectors and uocr_kv_read returns the entries' values.               */
+
+/* Entries of slots [slot0, slot0+n) of one row and layer, exactly: codes one
+ * per byte [n_heads][n][head_dim] (the low four bits count), scales and minima fp16
+ * [n_heads][n][head_dim/32].  Host or device pointers.  Written entries start
+ * with weight 0.  Synchronous.                                              */
+UOCR_API uocr_status uocr_kv_write_i4(uocr_ctx* ctx, int32_t row, int32_t layer, int32_t slot0, int32_t n,
+                                      const uint8_t* k_codes, const uint16_t* k_scale, const uint16_t* k_min,
+                                      const uint8_t* v_codes, const uint16_t* v_scale, const uint16_t* v_min);
+UOCR_API uocr_status uocr_kv_read_i4(uocr_ctx* ctx, int32_t row, int32_t layer, int32_t slot0, int32_t n,
+                                     uint8_t* k_codes, uint16_t* k_scale, uint16_t* k_min, uint8_t* v_codes,
+                                     uint16_t* v_scale, uint16_t* v_min);
+
+/* Rotate q and k by their positions as the config says (angles formed in
+ * double, products and sums rounded to fp32), quantise k and v and write them
+ * to the slots of their positions, with weight 0.
+ *   uocr_kv_append        token i is row i's token at device int32 positions[i]
+ *                         (rows in [1, max_rows])
+ *   uocr_kv_append_chunk  n >= 1 consecutive positions of one row from
+ *                         start_pos; no ring wrap inside one call, as
+ *                         uocr_prefill, and not below the end of an evicted
+ *                         prefix (UOCR_E_STATE)
+ * A negative device position counts as 0, one inside an evicted prefix is not
+ * written; both are reported by uocr_sync as UOCR_E_POSITION.               */
+UOCR_API uocr_status uocr_kv_append(uocr_ctx* ctx, int32_t layer, int32_t rows, const int32_t* positions,
+                                    const uocr_qkv* x);
+UOCR_API uocr_status uocr_kv_append_chunk(uocr_ctx* ctx, int32_t layer, int32_t row, int32_t start_pos, int32_t n,
+                                          const uocr_qkv* x);
+
+/* Attention of rotated queries over a layer's entries: scale 1/sqrt(head_dim),
+ * the layer's sink if use_sink (query heads that share a cache head share its
+ * sink), the slots that a step at the position reads without the evicted ones.
+ * A query with nothing to read gives zeros.  With kv_track the weights are
+ * added to the entries' sums.
+ *   q    device fp32 [n][q_heads][head_dim]; query head h reads cache head
+ *        h / (q_heads / n_heads); q_heads a multiple of n_heads, at most 8 n_heads
+ *   out  device [n][q_heads][head_dim] of out_dtype
+ * uocr_attend: token i is row i at positions[i]; uocr_attend_chunk: tokens of
+ * one row at start_pos + i, causal (position p sees the slots of positions <= p). */
+UOCR_API uocr_status uocr_attend(uocr_ctx* ctx, int32_t layer, int32_t rows, const int32_t* positions,
+                                 int32_t q_heads, const float* q, int32_t out_dtype, void* out);
+UOCR_API uocr_status uocr_attend_chunk(uocr_ctx* ctx, int32_t layer, int32_t row, int32_t start_pos, int32_t n,
+                                       int32_t q_heads, const float* q, int32_t out_dtype, void* out);
+
+/* Evict from prefixes by accumulated weight (needs kv_track).  Of the entries
+ * that row src_rows[i] still holds among prefix slots [0, n), every head keeps
+ * `keep`: the first `protect` of them and then those of largest weight (ties:
+ * the lowest slot; a NaN counts as lowest).  The kept entries, with their
+ * weights, move to slots [0, keep) of row dst_rows[i] in slot order; slots
+ * [keep, n) of that row are then empty: attention skips them, and its
+ * positions go on from n.  Ring slots stay as they are.
+ *   layer     a layer, or -1: every layer
+ *   src_rows, dst_rows  host int32 [n_rows], n_rows in [1, max_rows]; the dst_rows
+ *             differ, and one is also a src row only in its own pair (in place)
+ *   n         in [1, prefix_len], not inside a src row's evicted slots
+ *   keep      in [0, entries held], protect in [0, keep]
+ *   kept      device int32 [layers][n_rows][n_heads][keep] or NULL: the source
+ *             slots, ascending
+ *   k_val, v_val  device fp16 [layers][n_rows][n_heads][keep][head_dim] or NULL:
+ *             the kept entries' values
+ * Until uocr_kv_reset(row, 0) a row refuses calls that write its evicted slots
+ * (UOCR_E_STATE).                                                           */
+UOCR_API uocr_status uocr_kv_evict(uocr_ctx* ctx, int32_t layer, int32_t n_rows, const int32_t* src_rows,
+                                   const int32_t* dst_rows, int32_t n, int32_t keep, int32_t protect,
+                                   int32_t* kept, uint16_t* k_val, uint16_t* v_val);
+
+/* The accumulated weights (needs kv_track) of slots [slot0, slot0+n) of rows
+ * [row0, row0+n_rows) of a layer (-1: every layer): device fp32
+ * [layers][n_rows][n_heads][n].                                             */
+UOCR_API uocr_status uocr_kv_weights_read(uocr_ctx* ctx, int32_t layer, int32_t row0, int32_t n_rows, int32_t slot0,
+                                          int32_t n, float* out);
+UOCR_API uocr_status uocr_kv_weights_write(uocr_ctx* ctx, int32_t layer, int32_t row0, int32_t n_rows, int32_t slot0,
+                                           int32_t n, const float* in);
 
 /* Source: [Falcon] intro (the sink is one more key whose logit is the sink and
  * whose value is zero; equivalent to rescaling by sigmoid(lse - sink)).
@@ -349,7 +483,8 @@ UOCR_API uocr_status uocr_generate(uocr_ctx* ctx, int32_t rows, const int32_t* t
 /* Source: [Metal] "Il decoder e il Mixture of Experts" (the ring bounds the
  * memory of generated tokens).
  * Zero the ring slots (and the prefix when keep_prefix == 0) of one row
- * (row = -1: all rows).  Attention never reads a slot not written for the
+ * (row = -1: all rows), with their accumulated weights; without the prefix
+ * nothing stays evicted.  Attention never reads a slot not written for the
  * current sequence, so this is hygiene, not a correctness requirement.      */
 UOCR_API uocr_status uocr_kv_reset(uocr_ctx* ctx, int32_t row, int32_t keep_prefix);
 

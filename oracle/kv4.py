@@ -1,0 +1,106 @@
+"""Oracle of the 4-bit KV cache: entries, attention over them, eviction; float64 NumPy.
+
+TEST INFRASTRUCTURE (see the package's docstring); shares no code with the CUDA library.
+
+An entry holds, per group of 32 dimensions, an fp16 minimum m and scale s and 32 codes in 0..15 and stands for
+fp16(s q + m).  The scale and the codes are integer decisions taken in floating point, so they are taken in fp32,
+the precision the kernels decide in.
+"""
+from __future__ import annotations
+
+import math
+
+import numpy as np
+
+from .model import ring_slot, rope_frequencies
+
+GROUP = 32
+
+
+def rotate_f32(x, pos, cfg):
+    """Keys or queries [..., D] at position pos, rotated as the kernels round: angle in double, its cosine and sine
+    times the amplitude rounded to fp32, then both products and their sum rounded to fp32."""
+    inv, amp = rope_frequencies(cfg)
+    rd = 2 * inv.size
+    ang = np.float64(pos) * inv
+    c, s = (amp * np.cos(ang)).astype(np.float32), (amp * np.sin(ang)).astype(np.float32)
+    x = np.asarray(x, np.float32)
+    out = x.copy()
+    if getattr(cfg, "rope_layout", 0) == 1:
+        a, b = x[..., 0:rd:2], x[..., 1:rd:2]
+        out[..., 0:rd:2], out[..., 1:rd:2] = a * c - b * s, b * c + a * s
+    else:
+        a, b = x[..., :rd // 2], x[..., rd // 2:rd]
+        out[..., :rd // 2], out[..., rd // 2:rd] = a * c - b * s, b * c + a * s
+    return out
+
+
+def half_toward_zero(x):
+    """fp32 x >= 0 rounded toward zero to fp16."""
+    h = x.astype(np.float16)
+    down = (h.view(np.uint16) - 1).astype(np.uint16).view(np.float16)
+    return np.where(h.astype(np.float32) > x, down, h)
+
+
+def kv4_quant(x):
+    """Entries of vectors x [..., D] (fp32): codes uint8 [..., D], scales and minima fp16 [..., D/32]."""
+    x = np.asarray(x, np.float32)
+    g = x.reshape(x.shape[:-1] + (-1, GROUP))
+    ok = np.all(np.abs(g) <= 65504, axis=-1)
+    safe = np.where(ok[..., None], g, np.float32(0))
+    m = safe.min(-1).astype(np.float16)
+    mf = m.astype(np.float32)
+    s = half_toward_zero(np.maximum((safe.max(-1) - mf) * (np.float32(1) / np.float32(15)), np.float32(0)).astype(np.float32))
+    sf = s.astype(np.float32)
+    div = np.where(sf > 0, sf, np.float32(1))
+    q = np.clip(np.rint(((safe - mf[..., None]).astype(np.float32) / div[..., None]).astype(np.float32)), 0, 15)
+    q = np.where((sf > 0)[..., None], q, 0).astype(np.uint8)
+    return q.reshape(x.shape), np.where(ok, s, np.float16(0)), np.where(ok, m, np.float16(np.nan))
+
+
+def kv4_value(codes, s, m):
+    """The values of entries, float64 (each one an fp16 number)."""
+    g = codes.reshape(codes.shape[:-1] + (-1, GROUP)).astype(np.float64)
+    v = s.astype(np.float64)[..., None] * g + m.astype(np.float64)[..., None]
+    return v.astype(np.float16).astype(np.float64).reshape(codes.shape)
+
+
+def live_slots(p, P, R, hole=(0, 0)):
+    """Slots a query at position p reads, ascending: as a decode step, without the evicted ones."""
+    p = max(int(p), 0)
+    n = p + 1 if p < P else P + min(p - P + 1, R)
+    return np.array([s for s in range(n) if not (hole[0] <= s < hole[1])], dtype=np.int64)
+
+
+def attend_kv4(q, K, V, positions, P, R, holes=None, sinks=None, causal_row=None):
+    """Attention of q [n, q_heads, D] over K, V [rows, nh, slots, D] (values): token i reads row i, or row
+    causal_row.  Returns (out [n, q_heads, D], weights [rows, nh, slots]): every softmax weight given, summed."""
+    n, qh, D = q.shape
+    rows, nh, SL, _ = K.shape
+    out = np.zeros((n, qh, D))
+    wts = np.zeros((rows, nh, SL))
+    for i in range(n):
+        r = i if causal_row is None else causal_row
+        at = live_slots(positions[i], P, R, (0, 0) if holes is None else holes[r])
+        for h in range(qh):
+            kh = h // (qh // nh)
+            if at.size == 0:
+                continue
+            s = K[r, kh, at] @ q[i, h].astype(np.float64) / math.sqrt(D)
+            top = s.max() if sinks is None else max(s.max(), sinks[kh])
+            e = np.exp(s - top)
+            z = e.sum() + (0.0 if sinks is None else math.exp(sinks[kh] - top))
+            out[i, h] = (e / z) @ V[r, kh, at]
+            wts[r, kh, at] += e / z
+    return out, wts
+
+
+def evict_choice(weights, n, keep, protect, hole=(0, 0)):
+    """Slots kept among the live ones of [0, n): the first `protect`, then by weight (NaN lowest, ties by slot)."""
+    live = [s for s in range(n) if not (hole[0] <= s < hole[1])]
+    rest = sorted(live[protect:], key=lambda s: (-weights[s] if weights[s] == weights[s] else math.inf, s))
+    return np.array(sorted(live[:protect] + rest[:keep - protect]), dtype=np.int64)
+
+
+def slot_of(p, P, R):
+    return ring_slot(max(int(p), 0), P, R)

@@ -100,6 +100,52 @@ def rope(v, pos, theta):
     return np.concatenate([a * c - b * s, b * c + a * s], axis=-1)
 
 
+def rope_frequencies(cfg):
+    """(frequency of every rotated pair, amplitude of cos and sin) of a config.
+
+    The first rope_dims dimensions of a head rotate (0: all); linear scaling
+    divides every frequency by rope_factor; YaRN divides the slow pairs only,
+    blending over the pairs that turn between rope_beta_fast and rope_beta_slow
+    times in rope_orig_len positions, and raises the amplitude.
+    """
+    rd = getattr(cfg, "rope_dims", 0) or cfg.head_dim
+    theta = float(cfg.rope_theta)
+    inv = np.array([theta ** (-2.0 * i / rd) for i in range(rd // 2)])
+    kind, f = getattr(cfg, "rope_scaling", 0), float(getattr(cfg, "rope_factor", 1.0))
+    if kind == 1:
+        return inv / f, 1.0
+    if kind == 2:
+        last = rd // 2 - 1
+
+        def pair(b):
+            return rd * math.log(cfg.rope_orig_len / (2.0 * math.pi * b)) / (2.0 * math.log(theta))
+
+        lo = min(max(math.floor(pair(float(cfg.rope_beta_fast) or 32.0)), 0), last)
+        hi = min(max(math.ceil(pair(float(cfg.rope_beta_slow) or 1.0)), 0), last)
+        out = []
+        for i, w in enumerate(inv):
+            r = min(max((i - lo) / max(hi - lo, 1e-3), 0.0), 1.0)
+            out.append(w * (1.0 - r) + w / f * r)
+        return np.array(out), float(cfg.rope_mscale) or 0.1 * math.log(f) + 1.0
+    return inv, 1.0
+
+
+def rope_cfg(v, pos, cfg):
+    """Rotary embedding of v[..., D] at position pos as the config says: layout
+    (rotate-half or neighbouring pairs), rotated dimensions, scaling."""
+    inv, amp = rope_frequencies(cfg)
+    rd = 2 * inv.size
+    z = amp * np.exp(1j * pos * inv)
+    out = np.array(v, dtype=np.float64, copy=True)
+    if getattr(cfg, "rope_layout", 0) == 1:
+        w = (v[..., 0:rd:2] + 1j * v[..., 1:rd:2]) * z
+        out[..., 0:rd:2], out[..., 1:rd:2] = w.real, w.imag
+    else:
+        w = (v[..., :rd // 2] + 1j * v[..., rd // 2:rd]) * z
+        out[..., :rd // 2], out[..., rd // 2:rd] = w.real, w.imag
+    return out
+
+
 def kv_quant(x):
     """INT8 KV cache entry of key or value vectors (last axis = one head's D values).
 
@@ -270,12 +316,13 @@ class OracleModel:
     sinks: optional fp32 [layers, heads].
     kv_int8: the KV cache holds INT8 entries (kv_quant) instead of fp16 values:
     every key and value vector is quantised when it is written (the cached
-    prefix included) and attention reads s * code.
+    prefix included) and attention reads s * code.  kv_int4: the same with 4-bit entries.
     """
 
     def __init__(self, cfg, tensors, rows, kv_prefix=None, sinks=None, cache="float64", kv_int8=False,
-                 act_int8=False):
+                 act_int8=False, kv_int4=False):
         self.cfg = cfg
+        self.kv_int4 = kv_int4
         self.rows = rows
         self.kv_int8 = kv_int8
         # dynamic int8 activations: the inputs of the dense projections (Q/K/V, O,
@@ -296,6 +343,8 @@ class OracleModel:
                 k, v = kv_prefix[l]
                 if kv_int8:
                     k, v = kv_dequant(*kv_quant(k)), kv_dequant(*kv_quant(v))
+                if kv_int4:
+                    k, v = self._int4(k), self._int4(v)
                 self.pk.append(k)
                 self.pv.append(v)
             else:
@@ -307,6 +356,13 @@ class OracleModel:
         self.slot_pos = np.full((rows, P + R), -1, dtype=np.int64)
         if kv_prefix is not None:
             self.slot_pos[:, :P] = np.arange(P)
+
+    @staticmethod
+    def _int4(x):
+        """The values of 4-bit entries of x (decided in fp32 on the fp32-rounded input)."""
+        from .kv4 import kv4_quant, kv4_value
+
+        return kv4_value(*kv4_quant(np.asarray(x, dtype=np.float64).astype(np.float32)))
 
     # ---------------------------------------------------------------- weights
     def w(self, kind, layer=0, expert=0):
@@ -382,16 +438,19 @@ class OracleModel:
             attn = np.zeros((rows, nh * D))
             for r in range(rows):
                 p = int(positions[r])
-                qh = rope(Q[r].reshape(nh, D), p, cfg.rope_theta)
+                qh = rope_cfg(Q[r].reshape(nh, D), p, cfg)
                 if self.kv_int8:  # the cache holds INT8 entries, one scale per head
-                    kq = kv_quant(rope(Kx[r].reshape(nh, D), p, cfg.rope_theta))
+                    kq = kv_quant(rope_cfg(Kx[r].reshape(nh, D), p, cfg))
                     vq = kv_quant(Vx[r].reshape(nh, D))
                     kh, vh = kv_dequant(*kq), kv_dequant(*vq)
                     if res.kv_entries is None:
                         res.kv_entries = {}
                     res.kv_entries.setdefault(l, []).append((kq[0], kq[1], vq[0], vq[1]))
+                elif self.kv_int4:  # ... or 4-bit entries
+                    kh = self._int4(rope_cfg(Kx[r].reshape(nh, D), p, cfg))
+                    vh = self._int4(Vx[r].reshape(nh, D))
                 else:  # the cache holds fp16
-                    kh = f16(rope(Kx[r].reshape(nh, D), p, cfg.rope_theta))
+                    kh = f16(rope_cfg(Kx[r].reshape(nh, D), p, cfg))
                     vh = f16(Vx[r].reshape(nh, D))
                 res.k_new[l, r], res.v_new[l, r] = kh, vh
                 s = int(res.slots[r])

@@ -18,6 +18,9 @@ LIB_PATH = os.environ.get("UOCR_LIB") or os.path.join(_PKG, "libuocr.so")
 
 UOCR_OK, UOCR_E_INVALID_ARG, UOCR_E_OOM, UOCR_E_BUDGET, UOCR_E_FORMAT = 0, 1, 2, 3, 4
 UOCR_E_STATE, UOCR_E_CUDA, UOCR_E_POSITION, UOCR_E_TOKEN, UOCR_E_TIMEOUT = 5, 6, 7, 8, 9
+ROPE_HALF, ROPE_INTERLEAVED = 0, 1
+ROPE_PLAIN, ROPE_LINEAR, ROPE_YARN = 0, 1, 2
+DT_F32, DT_F16, DT_BF16 = 0, 1, 2
 STATUS_NAMES = {0: "OK", 1: "E_INVALID_ARG", 2: "E_OOM", 3: "E_BUDGET", 4: "E_FORMAT", 5: "E_STATE",
                 6: "E_CUDA", 7: "E_POSITION", 8: "E_TOKEN", 9: "E_TIMEOUT"}
 
@@ -26,7 +29,9 @@ EXPORTED = ["uocr_create", "uocr_destroy", "uocr_load_weights", "uocr_kv_write_p
             "uocr_set_sinks", "uocr_decode_step", "uocr_decode_step_embeds", "uocr_decode_step_host",
             "uocr_prefill", "uocr_generate", "uocr_kv_reset", "uocr_sync", "uocr_last_error", "uocr_memory_report",
             "uocr_debug_hidden", "uocr_debug_router", "uocr_debug_router_logits", "uocr_profile",
-            "uocr_lm_head_argmax_noalloc", "uocr_debug_wait_probe", "uocr_kv_read_i8", "uocr_kv_write_i8", "uocr_project"]
+            "uocr_lm_head_argmax_noalloc", "uocr_debug_wait_probe", "uocr_kv_read_i8", "uocr_kv_write_i8", "uocr_project",
+            "uocr_kv_write_i4", "uocr_kv_read_i4", "uocr_kv_append", "uocr_kv_append_chunk", "uocr_attend",
+            "uocr_attend_chunk", "uocr_kv_evict", "uocr_kv_weights_read", "uocr_kv_weights_write"]
 
 
 class uocr_config(C.Structure):
@@ -36,12 +41,21 @@ class uocr_config(C.Structure):
         "prefix_len", "ring_len", "max_rows", "use_sink")] + [
         ("rms_eps", C.c_float), ("rope_theta", C.c_float), ("mem_budget", C.c_uint64),
         ("stream", C.c_void_p), ("device", C.c_int32), ("use_graphs", C.c_int32), ("kv_int8", C.c_int32),
-        ("proj_in", C.c_int32), ("fmt_proj", C.c_int32), ("act_int8", C.c_int32)]
+        ("proj_in", C.c_int32), ("fmt_proj", C.c_int32), ("act_int8", C.c_int32),
+        ("rope_layout", C.c_int32), ("rope_dims", C.c_int32), ("rope_scaling", C.c_int32),
+        ("rope_orig_len", C.c_int32), ("rope_factor", C.c_float), ("rope_beta_fast", C.c_float),
+        ("rope_beta_slow", C.c_float), ("rope_mscale", C.c_float), ("kv_int4", C.c_int32), ("kv_track", C.c_int32)]
 
 
 class uocr_tensor(C.Structure):
     _fields_ = [("kind", C.c_int32), ("layer", C.c_int32), ("expert", C.c_int32), ("format", C.c_int32),
                 ("rows", C.c_int32), ("cols", C.c_int32), ("data", C.c_void_p), ("bytes", C.c_uint64)]
+
+
+class uocr_qkv(C.Structure):
+    _fields_ = [("q", C.c_void_p), ("k", C.c_void_p), ("v", C.c_void_p), ("ld_q", C.c_int64), ("ld_k", C.c_int64),
+                ("ld_v", C.c_int64), ("dtype", C.c_int32), ("q_heads", C.c_int32), ("q_out", C.c_void_p),
+                ("k_val", C.c_void_p), ("v_val", C.c_void_p)]
 
 
 class uocr_mem_report(C.Structure):
@@ -86,6 +100,15 @@ def load(path: str = LIB_PATH):
         "uocr_kv_read_i8": ([P, I, I, I, I, P, P, P, P], I),
         "uocr_kv_write_i8": ([P, I, I, I, I, P, P, P, P], I),
         "uocr_project": ([P, I, P, P], I),
+        "uocr_kv_write_i4": ([P, I, I, I, I, P, P, P, P, P, P], I),
+        "uocr_kv_read_i4": ([P, I, I, I, I, P, P, P, P, P, P], I),
+        "uocr_kv_append": ([P, I, I, P, C.POINTER(uocr_qkv)], I),
+        "uocr_kv_append_chunk": ([P, I, I, I, I, C.POINTER(uocr_qkv)], I),
+        "uocr_attend": ([P, I, I, P, I, P, I, P], I),
+        "uocr_attend_chunk": ([P, I, I, I, I, I, P, I, P], I),
+        "uocr_kv_evict": ([P, I, I, P, P, I, I, I, P, P, P], I),
+        "uocr_kv_weights_read": ([P, I, I, I, I, I, P], I),
+        "uocr_kv_weights_write": ([P, I, I, I, I, I, P], I),
     }
     for name, (args, res) in sig.items():
         f = getattr(lib, name)
@@ -99,6 +122,16 @@ class UocrError(RuntimeError):
     def __init__(self, status, msg):
         super().__init__(f"{STATUS_NAMES.get(status, status)}: {msg}")
         self.status = status
+
+
+def _buffer(x, dtype):
+    """(address, owner) of a NumPy array or a contiguous torch tensor of the given element type."""
+    if hasattr(x, "data_ptr"):
+        if not x.is_contiguous() or str(x.dtype).split(".")[-1] != np.dtype(dtype).name:
+            raise ValueError(f"expected a contiguous {np.dtype(dtype).name} tensor, got {x.dtype}")
+        return x.data_ptr(), x
+    x = np.ascontiguousarray(x, dtype)
+    return x.ctypes.data, x
 
 
 def make_config(cfg, *, max_rows=None, mem_budget=0, stream=0, device=0, use_graphs=1) -> uocr_config:
@@ -120,6 +153,10 @@ def make_config(cfg, *, max_rows=None, mem_budget=0, stream=0, device=0, use_gra
     c.proj_in = int(getattr(cfg, "proj_in", 0))
     c.fmt_proj = int(getattr(cfg, "fmt_proj", 1))
     c.act_int8 = int(getattr(cfg, "act_int8", 0))
+    for n in ("rope_layout", "rope_dims", "rope_scaling", "rope_orig_len", "kv_int4", "kv_track"):
+        setattr(c, n, int(getattr(cfg, n, 0)))
+    for n in ("rope_factor", "rope_beta_fast", "rope_beta_slow", "rope_mscale"):
+        setattr(c, n, float(getattr(cfg, n, 0.0)))
     return c
 
 
@@ -199,6 +236,59 @@ class Context:
         vs = np.ascontiguousarray(vs, np.float32)
         self._ck(self.lib.uocr_kv_write_i8(self.h, row, layer, slot0, kc.shape[1], kc.ctypes.data, ks.ctypes.data,
                                            vc.ctypes.data, vs.ctypes.data))
+
+    # -- 4-bit cache
+    def uocr_kv_write_i4(self, row, layer, slot0, kc, ks, km, vc, vs, vm):
+        """Write 4-bit entries as given: codes uint8 [nh][n][D], scales and minima fp16 [nh][n][D/32]
+        (NumPy arrays, or contiguous torch tensors on the context's device)."""
+        b = [_buffer(x, d) for x, d in zip((kc, ks, km, vc, vs, vm), (np.uint8, np.float16, np.float16) * 2)]
+        self._ck(self.lib.uocr_kv_write_i4(self.h, row, layer, slot0, int(kc.shape[1]), *(p for p, _ in b)))
+
+    def uocr_kv_read_i4(self, row, layer, slot0, n):
+        """4-bit entries: (k codes uint8 [nh][n][D], k scales fp16 [nh][n][D/32], k minima, v codes, v scales,
+        v minima)."""
+        nh, D = self.cfg.n_heads, self.cfg.head_dim
+        out = []
+        for _ in range(2):
+            out += [np.empty((nh, n, D), np.uint8), np.empty((nh, n, D // 32), np.float16),
+                    np.empty((nh, n, D // 32), np.float16)]
+        self._ck(self.lib.uocr_kv_read_i4(self.h, row, layer, slot0, n, *(x.ctypes.data for x in out)))
+        return tuple(out)
+
+    def _qkv(self, q_ptr, k_ptr, v_ptr, dtype, q_heads, ld_q, ld_k, ld_v, q_out, k_val, v_val):
+        return uocr_qkv(q_ptr or None, k_ptr or None, v_ptr or None, ld_q, ld_k, ld_v, dtype, q_heads, q_out or None,
+                        k_val or None, v_val or None)
+
+    def uocr_kv_append(self, layer, rows, pos_ptr, q_ptr, k_ptr, v_ptr, *, dtype=DT_F16, q_heads=0, ld_q=0, ld_k=0,
+                       ld_v=0, q_out=0, k_val=0, v_val=0):
+        x = self._qkv(q_ptr, k_ptr, v_ptr, dtype, q_heads, ld_q, ld_k, ld_v, q_out, k_val, v_val)
+        self._ck(self.lib.uocr_kv_append(self.h, layer, rows, pos_ptr or None, C.byref(x)))
+
+    def uocr_kv_append_chunk(self, layer, row, start_pos, n, q_ptr, k_ptr, v_ptr, *, dtype=DT_F16, q_heads=0, ld_q=0,
+                             ld_k=0, ld_v=0, q_out=0, k_val=0, v_val=0):
+        x = self._qkv(q_ptr, k_ptr, v_ptr, dtype, q_heads, ld_q, ld_k, ld_v, q_out, k_val, v_val)
+        self._ck(self.lib.uocr_kv_append_chunk(self.h, layer, row, start_pos, n, C.byref(x)))
+
+    def uocr_attend(self, layer, rows, pos_ptr, q_heads, q_ptr, out_ptr, out_dtype=DT_F16):
+        self._ck(self.lib.uocr_attend(self.h, layer, rows, pos_ptr or None, q_heads, q_ptr or None, out_dtype,
+                                      out_ptr or None))
+
+    def uocr_attend_chunk(self, layer, row, start_pos, n, q_heads, q_ptr, out_ptr, out_dtype=DT_F16):
+        self._ck(self.lib.uocr_attend_chunk(self.h, layer, row, start_pos, n, q_heads, q_ptr or None, out_dtype,
+                                            out_ptr or None))
+
+    def uocr_kv_evict(self, layer, src_rows, dst_rows, n, keep, protect=0, *, kept_ptr=0, k_val_ptr=0, v_val_ptr=0):
+        src, dst = np.asarray(list(src_rows), np.int32), np.asarray(list(dst_rows), np.int32)
+        if src.shape != dst.shape:
+            raise ValueError("uocr_kv_evict: src_rows and dst_rows have different lengths")
+        self._ck(self.lib.uocr_kv_evict(self.h, layer, src.size, src.ctypes.data, dst.ctypes.data, n, keep, protect,
+                                        kept_ptr or None, k_val_ptr or None, v_val_ptr or None))
+
+    def uocr_kv_weights_read(self, layer, row0, n_rows, slot0, n, out_ptr):
+        self._ck(self.lib.uocr_kv_weights_read(self.h, layer, row0, n_rows, slot0, n, out_ptr or None))
+
+    def uocr_kv_weights_write(self, layer, row0, n_rows, slot0, n, in_ptr):
+        self._ck(self.lib.uocr_kv_weights_write(self.h, layer, row0, n_rows, slot0, n, in_ptr or None))
 
     def uocr_set_sinks(self, sinks):
         s = np.ascontiguousarray(sinks, dtype=np.float32)

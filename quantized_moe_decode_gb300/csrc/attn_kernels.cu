@@ -632,7 +632,7 @@ __global__ void k_embed(const EmbedArgs a) {
     a.out[(size_t)row * a.H + k] = f.x;
     a.out[(size_t)row * a.H + k + 1] = f.y;
   }
-  // rotary angles of this row's position (rotate-half RoPE): the angle is formed
+  // rotary angles of this row's position: the angle is formed
   // and reduced modulo 2 pi in double precision, then its cosine and sine in float
   const int pos = max(a.pos[row], 0);
   for (int j = threadIdx.x; j < a.half_d; j += blockDim.x) {
@@ -640,7 +640,7 @@ __global__ void k_embed(const EmbedArgs a) {
     ang -= 6.283185307179586 * rint(ang * 0.15915494309189535);
     float sn, cs;
     sincosf((float)ang, &sn, &cs);
-    a.rope[(size_t)row * a.half_d + j] = make_float2(cs, sn);
+    a.rope[(size_t)row * a.half_d + j] = make_float2(cs * a.amp, sn * a.amp);
   }
 }
 
@@ -652,8 +652,8 @@ cudaError_t launch_embed(const EmbedArgs& a, int rows, cudaStream_t st) {
 // ------------------------------------------------------------------ packer
 // Canonical blocks -> fragment-ordered device layout (see device_common.cuh).
 // One thread per (slab, unit, lane); packed row pr maps to (source, row) by
-// the matrix's row map: identity, Q/K/V sections with the rotary pairs (i,
-// i + D/2) placed in rows g and g + 8 of one slab, interleaved gate/up rows
+// the matrix's row map: identity, Q/K/V sections with the two dimensions of a
+// rotary pair placed in rows g and g + 8 of one slab, interleaved gate/up rows
 // (gate in rows 0..7 of a slab, up in 8..15) over one or more experts, or
 // column concatenation of several experts (shared down projections).
 struct PackSrcRef {
@@ -672,8 +672,9 @@ __device__ __forceinline__ PackSrcRef pack_row(const PackArgs& a, int pr) {
       const int sec = pr / a.S, w = pr - sec * a.S;
       const int head = w / a.D, wi = w - head * a.D;
       const int js = wi >> 4, j = wi & 15;
-      const int dim = j < 8 ? 8 * js + j : (a.D >> 1) + 8 * js + (j - 8);
-      if (sec < a.nsrc) r = {sec, head * a.D + dim};
+      int lo, hi;
+      rope_pair(a.rope_layout, a.rope_dims, 8 * js + (j & 7), lo, hi);
+      if (sec < a.nsrc) r = {sec, head * a.D + (j < 8 ? lo : hi)};
       break;
     }
     case MAP_SWIGLU: {

@@ -107,6 +107,19 @@ struct PMat {
   long long s_stride;
 };
 
+// Dimensions of pair j (0 <= j < D/2) of a head: the first rd/2 pairs rotate,
+// rotate-half (j, j + rd/2) or neighbours (2j, 2j + 1); the remaining
+// dimensions pair up as neighbours and pass through.
+__host__ __device__ __forceinline__ void rope_pair(int layout, int rd, int j, int& lo, int& hi) {
+  if (layout == 0 && j < rd / 2) {
+    lo = j;
+    hi = j + rd / 2;
+  } else {  // rd is even, so pair rd/2 starts at dimension rd in both layouts
+    lo = 2 * j;
+    hi = 2 * j + 1;
+  }
+}
+
 // Device status bits (reported by uocr_sync).
 constexpr int kStatusToken = 1;
 constexpr int kStatusPosition = 2;

@@ -19,6 +19,7 @@
 #include <string>
 #include <vector>
 
+#include "kv4_common.cuh"
 #include "launch.h"
 #include "uocr.h"
 
@@ -132,11 +133,19 @@ struct uocr_ctx {
   DMat proj;                 // projector [H][proj_in]
   __half* proj_b = nullptr;  // its bias [H]
   double* inv_freq = nullptr;
+  double rope_amp = 1.0;   // amplitude of cos and sin
   float2* rope = nullptr;  // [max_rows][head_dim/2] (cos, sin) of the step's positions
   __half* kv = nullptr;        // fp16 cache [L][MR][2][nh][SL][D]
   int8_t* kv8 = nullptr;       // INT8 cache codes, same shape
   float* kvs = nullptr;        // INT8 cache scales [L][MR][2][nh][SLp]
-  float* kv_new = nullptr;     // INT8 cache: the pass's new keys / values in fp32 [kTokCap][2][nh][D]
+  uint8_t* kv4 = nullptr;      // 4-bit cache [L][MR][2][nh][tiles] of kv4_tile_bytes
+  size_t kv4_layer = 0;        // bytes per layer
+  int tiles = 0;               // 16-slot tiles of a (row, K|V, head)
+  int2* hole = nullptr;        // 4-bit cache: evicted slots [x, y) of each [L][MR]
+  std::vector<int2> hole_h;    // ... the same on the host
+  float* wts = nullptr;        // accumulated weights [L][MR][nh][16 tiles] (kv_track)
+  float2* lse = nullptr;       // softmax statistics of one pass [kTokCap][8 nh] (kv_track)
+  float* kv_new = nullptr;     // quantised caches: the pass's new keys / values in fp32 [kTokCap][2][nh][D]
   size_t kv_layer = 0;         // entries (codes or fp16 values) per layer
   size_t kvs_layer = 0;        // scales per layer
   int SLp = 0;                 // scale slots per (row, K|V, head): SL rounded up to 16
@@ -264,7 +273,26 @@ static uocr_status check_config(uocr_ctx* ctx, const uocr_config& c) {
   if (c.use_sink != 0 && c.use_sink != 1) return bad("use_sink must be 0 or 1");
   if (!(c.rms_eps >= 0.f) || !(c.rope_theta > 0.f)) return bad("rms_eps >= 0 and rope_theta > 0 required");
   if (c.kv_int8 != 0 && c.kv_int8 != 1) return bad("kv_int8 must be 0 or 1");
+  if (c.kv_int4 != 0 && c.kv_int4 != 1) return bad("kv_int4 must be 0 or 1");
+  if (c.kv_int4 && c.kv_int8) return bad("kv_int4 and kv_int8 exclude each other");
+  if (c.kv_int4 && c.head_dim < 32) return bad("kv_int4 needs head_dim >= 32 (groups of 32 dimensions)");
+  if (c.kv_track != 0 && c.kv_track != 1) return bad("kv_track must be 0 or 1");
+  if (c.kv_track && !c.kv_int4) return bad("kv_track needs the 4-bit cache (kv_int4 = 1)");
   if (c.act_int8 != 0 && c.act_int8 != 1) return bad("act_int8 must be 0 or 1");
+  if (c.rope_layout != UOCR_ROPE_HALF && c.rope_layout != UOCR_ROPE_INTERLEAVED) return bad("unknown rope_layout");
+  if (c.rope_dims < 0 || c.rope_dims > c.head_dim || c.rope_dims % 2)
+    return bad("rope_dims must be even and in [0, head_dim]");
+  if (c.rope_scaling < UOCR_ROPE_PLAIN || c.rope_scaling > UOCR_ROPE_YARN) return bad("unknown rope_scaling");
+  if (c.rope_scaling != UOCR_ROPE_PLAIN && !(c.rope_factor >= 1.f && std::isfinite(c.rope_factor)))
+    return bad("a scaled rope needs a finite rope_factor >= 1");
+  if (c.rope_scaling == UOCR_ROPE_YARN) {
+    const float bf = c.rope_beta_fast != 0.f ? c.rope_beta_fast : 32.f;
+    const float bs = c.rope_beta_slow != 0.f ? c.rope_beta_slow : 1.f;
+    if (c.rope_orig_len < 1) return bad("YaRN needs rope_orig_len >= 1");
+    if (!(bs > 0.f) || !(bf >= bs) || !std::isfinite(bf)) return bad("YaRN needs rope_beta_fast >= rope_beta_slow > 0");
+    if (!(c.rope_theta > 1.f)) return bad("YaRN needs rope_theta > 1");
+    if (!(c.rope_mscale >= 0.f) || !std::isfinite(c.rope_mscale)) return bad("rope_mscale must be finite and >= 0");
+  }
   if (c.act_int8 && (!quant_fmt(c.fmt_attn) || (has_dense && !quant_fmt(c.fmt_dense))))
     return bad("act_int8 needs quantised fmt_attn and fmt_dense (int8 codes against int8 activations)");
   if (c.act_int8 && (c.hidden > kActMaxChunks * kActChunk || c.n_heads * c.head_dim > kActMaxChunks * kActChunk ||
@@ -276,6 +304,32 @@ static uocr_status check_config(uocr_ctx* ctx, const uocr_config& c) {
     if (plan_stream(2, kf(c.fmt_proj), c.proj_in).bytes > kSmemLimit) return bad("proj_in too large");
   }
   return UOCR_OK;
+}
+
+// Rotary frequencies of the config, one per pair of a head (pairs that pass
+// through hold 0), and the amplitude of cos and sin.
+static std::vector<double> rope_frequencies(const uocr_config& c, double* amp) {
+  const int rd = c.rope_dims, pairs = rd / 2;
+  std::vector<double> inv(c.head_dim / 2, 0.0);
+  for (int i = 0; i < pairs; ++i) inv[i] = std::pow((double)c.rope_theta, -2.0 * i / rd);
+  *amp = 1.0;
+  if (c.rope_scaling == UOCR_ROPE_LINEAR)
+    for (int i = 0; i < pairs; ++i) inv[i] /= (double)c.rope_factor;
+  if (c.rope_scaling == UOCR_ROPE_YARN) {
+    const double pi = 3.14159265358979323846, f = c.rope_factor;
+    auto pair_of = [&](double turns) {  // the pair that turns this often over rope_orig_len positions
+      return rd * std::log(c.rope_orig_len / (2.0 * pi * turns)) / (2.0 * std::log((double)c.rope_theta));
+    };
+    auto clamp = [&](double x) { return std::fmin(std::fmax(x, 0.0), (double)(pairs - 1)); };
+    const double lo = clamp(std::floor(pair_of(c.rope_beta_fast != 0.f ? c.rope_beta_fast : 32.0)));
+    const double hi = clamp(std::ceil(pair_of(c.rope_beta_slow != 0.f ? c.rope_beta_slow : 1.0)));
+    for (int i = 0; i < pairs; ++i) {
+      const double r = std::fmin(std::fmax((i - lo) / std::fmax(hi - lo, 1e-3), 0.0), 1.0);
+      inv[i] *= (1.0 - r) + r / f;
+    }
+    *amp = c.rope_mscale != 0.f ? (double)c.rope_mscale : 0.1 * std::log(f) + 1.0;
+  }
+  return inv;
 }
 
 // ------------------------------------------------------------------ memory plan
@@ -345,6 +399,16 @@ static void carve(uocr_ctx* ctx, Carver& cv) {
     ctx->kvs_layer = (size_t)MR * 2 * c.n_heads * ctx->SLp;
     ctx->kv8 = cv.take<int8_t>(ctx->kv_layer * Lc, r.kv_cache);
     ctx->kvs = cv.take<float>(ctx->kvs_layer * Lc, r.kv_cache);
+    ctx->kv_new = cv.take<float>((size_t)TC * 2 * S, r.activations);
+  } else if (c.kv_int4) {
+    ctx->tiles = (ctx->SL + kKv4Slots - 1) / kKv4Slots;
+    ctx->kv4_layer = (size_t)MR * 2 * c.n_heads * ctx->tiles * kv4_tile_bytes(c.head_dim);
+    ctx->kv4 = cv.take<uint8_t>(ctx->kv4_layer * Lc, r.kv_cache);
+    ctx->hole = cv.take<int2>((size_t)Lc * MR, r.kv_cache);
+    if (c.kv_track) {
+      ctx->wts = cv.take<float>((size_t)Lc * MR * c.n_heads * ctx->tiles * kKv4Slots, r.kv_cache);
+      ctx->lse = cv.take<float2>((size_t)TC * 8 * c.n_heads, r.activations);
+    }
     ctx->kv_new = cv.take<float>((size_t)TC * 2 * S, r.activations);
   } else {
     ctx->kv = cv.take<__half>(ctx->kv_layer * Lc, r.kv_cache);
@@ -423,6 +487,43 @@ struct StepShape {
 
 }  // namespace
 
+// The fields of the 4-bit cache's kernels that a layer fixes.
+static Kv4AppendArgs kv4_append_args(uocr_ctx* ctx, int layer) {
+  const uocr_config& c = ctx->cfg;
+  Kv4AppendArgs a{};
+  a.inv_freq = ctx->inv_freq;
+  a.amp = ctx->rope_amp;
+  a.rope_layout = c.rope_layout;
+  a.rope_dims = c.rope_dims;
+  a.nh = c.n_heads;
+  a.D = c.head_dim;
+  a.kv4 = ctx->kv4 + ctx->kv4_layer * layer;
+  a.wts = ctx->wts ? ctx->wts + (size_t)layer * c.max_rows * c.n_heads * ctx->tiles * kKv4Slots : nullptr;
+  a.hole = ctx->hole + (size_t)layer * c.max_rows;
+  a.P = c.prefix_len;
+  a.R = c.ring_len;
+  a.tiles = ctx->tiles;
+  a.status = ctx->status;
+  return a;
+}
+static Kv4AttnArgs kv4_attn_args(uocr_ctx* ctx, int layer) {
+  const uocr_config& c = ctx->cfg;
+  Kv4AttnArgs a{};
+  a.kv4 = ctx->kv4 + ctx->kv4_layer * layer;
+  a.sink = c.use_sink ? ctx->sinks + (size_t)layer * c.n_heads : nullptr;
+  a.hole = ctx->hole + (size_t)layer * c.max_rows;
+  a.wts = ctx->wts ? ctx->wts + (size_t)layer * c.max_rows * c.n_heads * ctx->tiles * kKv4Slots : nullptr;
+  a.lse = ctx->lse;
+  a.nh = c.n_heads;
+  a.D = c.head_dim;
+  a.P = c.prefix_len;
+  a.R = c.ring_len;
+  a.tiles = ctx->tiles;
+  a.scale = 1.0f / sqrtf((float)c.head_dim);
+  a.status = ctx->status;
+  return a;
+}
+
 static uocr_status enqueue_step(uocr_ctx* ctx, const StepShape& sh, Prof* prof) {
   const uocr_config& c = ctx->cfg;
   cudaStream_t st = ctx->st;
@@ -460,6 +561,7 @@ static uocr_status enqueue_step(uocr_ctx* ctx, const StepShape& sh, Prof* prof) 
   ea.inv_freq = ctx->inv_freq;
   ea.rope = ctx->rope;
   ea.half_d = c.head_dim / 2;
+  ea.amp = (float)ctx->rope_amp;
   ea.status = ctx->status;
   if (want("embed")) {
     CK(launch_embed(ea, rows, st), "embed launch");
@@ -487,6 +589,8 @@ static uocr_status enqueue_step(uocr_ctx* ctx, const StepShape& sh, Prof* prof) 
     qa.q_out = ctx->q;
     qa.kv = kvl;
     qa.rope = ctx->rope;
+    qa.rope_layout = c.rope_layout;
+    qa.rope_dims = c.rope_dims;
     qa.nh = c.n_heads;
     qa.D = c.head_dim;
     qa.S = S;
@@ -495,7 +599,7 @@ static uocr_status enqueue_step(uocr_ctx* ctx, const StepShape& sh, Prof* prof) 
     qa.SL = ctx->SL;
     qa.kv_row0 = kv_row0;
     qa.kv_rstep = kv_rstep;
-    qa.kv_new = kv8l ? ctx->kv_new : nullptr;
+    qa.kv_new = kv8l || ctx->kv4 ? ctx->kv_new : nullptr;
     qa.status = ctx->status;
     if (want("qkv")) {
       if (a8g) {
@@ -520,6 +624,31 @@ static uocr_status enqueue_step(uocr_ctx* ctx, const StepShape& sh, Prof* prof) 
       ka.kv_rstep = kv_rstep;
       if (want("kv_quant")) {
         CK(launch_kv_quant(ka, rows, st, pdl), "kv quant launch");
+      }
+    }
+    if (ctx->kv4) {  // 4-bit cache: the same, and its own attention
+      Kv4AppendArgs ka = kv4_append_args(ctx, l);
+      ka.k = ctx->kv_new;
+      ka.v = ctx->kv_new + S;
+      ka.ldk = ka.ldv = 2 * S;
+      ka.lhk = c.head_dim;
+      ka.dtype = UOCR_DT_F32;
+      ka.pos = ctx->pos_buf;
+      ka.kv_row0 = kv_row0;
+      ka.kv_rstep = kv_rstep;
+      if (want("kv_quant")) {
+        CK(launch_kv4_append(ka, rows, st, pdl), "kv append launch");
+      }
+      Kv4AttnArgs xa = kv4_attn_args(ctx, l);
+      xa.q = ctx->q;
+      xa.q_heads = c.n_heads;
+      xa.out = ctx->attn_out;
+      xa.out_dtype = UOCR_DT_F16;
+      xa.pos = ctx->pos_buf;
+      xa.kv_row0 = kv_row0;
+      xa.kv_rstep = kv_rstep;
+      if (want("attention")) {
+        CK(launch_kv4_attn(xa, rows, st, pdl), "attention launch");
       }
     }
     // attention
@@ -565,7 +694,7 @@ static uocr_status enqueue_step(uocr_ctx* ctx, const StepShape& sh, Prof* prof) 
       if (kv8l) aa.chunk = (aa.chunk + 15) / 16 * 16;  // scale runs start on 16-byte boundaries
     }
     aa.scale = 1.0f / sqrtf((float)c.head_dim);
-    if (want("attention")) {
+    if (!ctx->kv4 && want("attention")) {
       CK(launch_attn(aa, rows, st, pdl), "attention launch");
     }
     // O projection + residual
@@ -943,6 +1072,8 @@ static uocr_status pack_into(uocr_ctx* ctx, const DMat& dst, size_t expert_off_q
   pa.src_cols = src_cols;
   pa.S = ctx->S;
   pa.D = ctx->cfg.head_dim;
+  pa.rope_layout = ctx->cfg.rope_layout;
+  pa.rope_dims = ctx->cfg.rope_dims;
   pa.I = I;
   CK(launch_pack(pa, ctx->st), "pack launch");
   CK(cudaStreamSynchronize(ctx->st), "pack");
@@ -1116,6 +1247,7 @@ static cudaError_t noalloc_scratch(int device, unsigned long long** out) {
 
 static uocr_status noalloc_launch(uocr_ctx* ctx, int rows, const float* hidden, int32_t* next_ids, float* logits,
                                   unsigned long long* scratch, cudaStream_t st);
+static uocr_status kv4_reset(uocr_ctx* ctx, int r0, int r1, int from);
 
 // ------------------------------------------------------------------ C ABI
 extern "C" {
@@ -1132,6 +1264,7 @@ uocr_status uocr_create(const uocr_config* cfg, uocr_ctx** out) {
     delete ctx;
     return s;
   }
+  if (ctx->cfg.rope_dims == 0) ctx->cfg.rope_dims = ctx->cfg.head_dim;
   // measuring pass for the budget check
   Carver m;
   carve(ctx, m);
@@ -1206,9 +1339,7 @@ uocr_status uocr_create(const uocr_config* cfg, uocr_ctx** out) {
   // zero everything (KV cache, counters, argmax keys, status)
   if (e == cudaSuccess) e = cudaMemsetAsync(ctx->arena, 0, m.off, ctx->st);
   if (e == cudaSuccess) {
-    std::vector<double> inv(cfg->head_dim / 2);
-    for (int i = 0; i < cfg->head_dim / 2; ++i)
-      inv[i] = std::pow((double)cfg->rope_theta, -2.0 * i / cfg->head_dim);
+    const std::vector<double> inv = rope_frequencies(ctx->cfg, &ctx->rope_amp);
     e = cudaMemcpyAsync(ctx->inv_freq, inv.data(), inv.size() * sizeof(double), cudaMemcpyHostToDevice, ctx->st);
   }
   if (e == cudaSuccess) e = cudaStreamSynchronize(ctx->st);
@@ -1217,6 +1348,7 @@ uocr_status uocr_create(const uocr_config* cfg, uocr_ctx** out) {
     uocr_destroy(ctx);
     return UOCR_E_CUDA;
   }
+  if (ctx->kv4) ctx->hole_h.assign((size_t)cfg->n_layers * cfg->max_rows, int2{0, 0});
   g_create_err.clear();
   *out = ctx;
   return UOCR_OK;
@@ -1252,13 +1384,25 @@ uocr_status uocr_load_weights(uocr_ctx* ctx, const uocr_tensor* t, size_t n) {
 
 }  // extern "C"
 
+// Whether slots [slot0, slot0 + n) of a (row, layer) meet its evicted ones, and
+// whether positions from `pos` on would.
+static bool in_hole(uocr_ctx* ctx, int row, int layer, int slot0, int n) {
+  if (!ctx->kv4) return false;
+  const int2 h = ctx->hole_h[(size_t)layer * ctx->cfg.max_rows + row];
+  return n > 0 && slot0 < h.y && slot0 + n > h.x && h.y > h.x;
+}
+static bool below_hole(uocr_ctx* ctx, int row, int layer, int pos) {
+  const int2 h = ctx->hole_h[(size_t)layer * ctx->cfg.max_rows + row];
+  return h.y > h.x && pos < h.y;
+}
+
 // Slots [slot0, slot0 + n) of one (row, layer) from host fp16 [nh][n][D]
 // keys and values; the INT8 cache quantises them on the device.
 static uocr_status kv_put(uocr_ctx* ctx, int row, int layer, int slot0, int n, const uint16_t* k, const uint16_t* v) {
   const uocr_config& c = ctx->cfg;
   const size_t D = c.head_dim, nh = c.n_heads;
   if (n == 0) return UOCR_OK;
-  if (!ctx->kv8) {
+  if (!ctx->kv8 && !ctx->kv4) {
     for (int kv = 0; kv < 2; ++kv) {
       const uint16_t* src = kv ? v : k;
       for (size_t h = 0; h < nh; ++h) {
@@ -1275,7 +1419,18 @@ static uocr_status kv_put(uocr_ctx* ctx, int row, int layer, int slot0, int n, c
   uint8_t* st8 = reinterpret_cast<uint8_t*>(stage);
   cudaError_t e = cudaMemcpyAsync(st8, k, bytes, cudaMemcpyHostToDevice, ctx->st);
   if (e == cudaSuccess) e = cudaMemcpyAsync(st8 + bytes, v, bytes, cudaMemcpyHostToDevice, ctx->st);
-  if (e == cudaSuccess) {
+  if (e == cudaSuccess && ctx->kv4) {
+    Kv4AppendArgs ka = kv4_append_args(ctx, layer);
+    ka.k = st8;
+    ka.v = st8 + bytes;
+    ka.ldk = ka.ldv = (long long)D;
+    ka.lhk = (long long)n * (long long)D;
+    ka.dtype = UOCR_DT_F16;
+    ka.slots = 1;
+    ka.pos0 = slot0;
+    ka.kv_row0 = row;
+    e = launch_kv4_append(ka, n, ctx->st, false);
+  } else if (e == cudaSuccess) {
     KvQuantArgs ka{};
     ka.src16k = reinterpret_cast<const __half*>(st8);
     ka.src16v = reinterpret_cast<const __half*>(st8 + bytes);
@@ -1304,7 +1459,7 @@ static uocr_status kv_get(uocr_ctx* ctx, int row, int layer, int slot0, int n, u
   const size_t D = c.head_dim, nh = c.n_heads;
   CK(cudaStreamSynchronize(ctx->st), "kv read");
   if (n == 0) return UOCR_OK;
-  if (!ctx->kv8) {
+  if (!ctx->kv8 && !ctx->kv4) {
     for (int kv = 0; kv < 2; ++kv) {
       uint16_t* dst = kv ? v : k;
       for (size_t h = 0; h < nh; ++h) {
@@ -1319,9 +1474,23 @@ static uocr_status kv_get(uocr_ctx* ctx, int row, int layer, int slot0, int n, u
   CK(cudaMalloc(&stage, 2 * bytes), "kv staging allocation");
   __half* sk = reinterpret_cast<__half*>(stage);
   __half* sv = sk + nh * n * D;
-  cudaError_t e = launch_kv_dequant(ctx->kv8 + ctx->kv_layer * layer + (size_t)row * 2 * nh * ctx->SL * D,
-                                    ctx->kvs + ctx->kvs_layer * layer + (size_t)row * 2 * nh * ctx->SLp, c.n_heads,
-                                    c.head_dim, ctx->SL, ctx->SLp, slot0, n, sk, sv, ctx->st);
+  cudaError_t e;
+  if (ctx->kv4) {
+    Kv4IoArgs ia{};
+    ia.kv4 = ctx->kv4 + ctx->kv4_layer * layer + (size_t)row * 2 * nh * ctx->tiles * kv4_tile_bytes(c.head_dim);
+    ia.val[0] = sk;
+    ia.val[1] = sv;
+    ia.nh = c.n_heads;
+    ia.D = c.head_dim;
+    ia.tiles = ctx->tiles;
+    ia.slot0 = slot0;
+    ia.n = n;
+    e = launch_kv4_io(ia, ctx->st);
+  } else {
+    e = launch_kv_dequant(ctx->kv8 + ctx->kv_layer * layer + (size_t)row * 2 * nh * ctx->SL * D,
+                          ctx->kvs + ctx->kvs_layer * layer + (size_t)row * 2 * nh * ctx->SLp, c.n_heads,
+                          c.head_dim, ctx->SL, ctx->SLp, slot0, n, sk, sv, ctx->st);
+  }
   if (e == cudaSuccess) e = cudaStreamSynchronize(ctx->st);
   if (e == cudaSuccess) e = cudaMemcpy(k, sk, bytes, cudaMemcpyDeviceToHost);
   if (e == cudaSuccess) e = cudaMemcpy(v, sv, bytes, cudaMemcpyDeviceToHost);
@@ -1365,6 +1534,7 @@ uocr_status uocr_kv_write_prefix(uocr_ctx* ctx, int32_t row, int32_t layer, cons
   if (!k || !v || row < 0 || row >= c.max_rows || layer < 0 || layer >= c.n_layers || start < 0 || n < 0 ||
       start + n > c.prefix_len)
     return ctx->fail(UOCR_E_INVALID_ARG, "kv_write_prefix: bad row/layer/range");
+  if (in_hole(ctx, row, layer, start, n)) return ctx->fail(UOCR_E_STATE, "kv_write_prefix: the slots are evicted");
   return kv_put(ctx, row, layer, start, n, k, v);
 }
 
@@ -1376,6 +1546,7 @@ uocr_status uocr_kv_write(uocr_ctx* ctx, int32_t row, int32_t layer, int32_t slo
   if (!k || !v || row < 0 || row >= c.max_rows || layer < 0 || layer >= c.n_layers || slot0 < 0 || n < 0 ||
       slot0 + n > ctx->SL)
     return ctx->fail(UOCR_E_INVALID_ARG, "kv_write: bad row/layer/slot range");
+  if (in_hole(ctx, row, layer, slot0, n)) return ctx->fail(UOCR_E_STATE, "kv_write: the slots are evicted");
   return kv_put(ctx, row, layer, slot0, n, k, v);
 }
 
@@ -1519,6 +1690,10 @@ uocr_status uocr_prefill(uocr_ctx* ctx, int32_t row, const int32_t* token_ids, c
     return ctx->fail(UOCR_E_INVALID_ARG,
                      "prefill: positions [%d, %d) must lie in [0, prefix_len + ring_len = %d) (no ring wrap)",
                      start_pos, start_pos + n, ctx->SL);
+  for (int l = 0; ctx->kv4 && l < c.n_layers; ++l)
+    if (below_hole(ctx, row, l, start_pos))
+      return ctx->fail(UOCR_E_STATE, "prefill: position %d of row %d lies in an evicted prefix (layer %d)", start_pos, row,
+                       l);
   uocr_status s = check_complete(ctx);
   if (s != UOCR_OK) return s;
   CK(cudaEventRecord(ctx->ev_in, ctx->ust), "event record");
@@ -1613,6 +1788,7 @@ uocr_status uocr_kv_reset(uocr_ctx* ctx, int32_t row, int32_t keep_prefix) {
   if (row < -1 || row >= c.max_rows) return ctx->fail(UOCR_E_INVALID_ARG, "row out of range");
   const int r0 = row < 0 ? 0 : row, r1 = row < 0 ? c.max_rows : row + 1;
   const int from = keep_prefix ? c.prefix_len : 0;
+  if (ctx->kv4) return kv4_reset(ctx, r0, r1, from);
   for (int l = 0; l < c.n_layers; ++l)
     for (int r = r0; r < r1; ++r) {
       if (!ctx->kv8) {
@@ -1644,7 +1820,8 @@ uocr_status uocr_sync(uocr_ctx* ctx) {
     if (st & kStatusTimeout)
       return ctx->fail(UOCR_E_TIMEOUT, "a kernel's bounded wait for its asynchronous copies ran out");
     if (st & kStatusToken) return ctx->fail(UOCR_E_TOKEN, "a token id was outside [0, vocab)");
-    return ctx->fail(UOCR_E_POSITION, "a position was negative");
+    return ctx->fail(UOCR_E_POSITION, ctx->kv4 ? "a position was negative or inside an evicted prefix"
+                                               : "a position was negative");
   }
   return UOCR_OK;
 }
@@ -1800,6 +1977,398 @@ uocr_status uocr_lm_head_argmax_noalloc(uocr_ctx* ctx, int32_t rows, const float
   const uocr_status ls = noalloc_launch(ctx, rows, hidden, next_ids, logits, scratch, st);
   if (prev != c.device) CK(cudaSetDevice(prev), "restore device");
   return ls;
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------------ 4-bit cache
+// The context's device is current while one of these calls runs, whatever the
+// caller's thread has current.
+namespace {
+struct OnDevice {
+  int prev = -1;
+  cudaError_t e;
+  explicit OnDevice(int device) {
+    e = cudaGetDevice(&prev);
+    if (e == cudaSuccess && prev != device) {
+      e = cudaSetDevice(device);
+    } else {
+      prev = -1;
+    }
+  }
+  ~OnDevice() {
+    if (prev >= 0) cudaSetDevice(prev);
+  }
+};
+}  // namespace
+
+static uocr_status kv4_begin(uocr_ctx* ctx) {
+  CK(cudaEventRecord(ctx->ev_in, ctx->ust), "event record");
+  CK(cudaStreamWaitEvent(ctx->st, ctx->ev_in, 0), "stream wait");
+  return UOCR_OK;
+}
+
+static uocr_status kv4_reset(uocr_ctx* ctx, int r0, int r1, int from) {
+  const uocr_config& c = ctx->cfg;
+  const size_t tb = kv4_tile_bytes(c.head_dim), SLt = (size_t)ctx->tiles * kKv4Slots;
+  if (from == 0) {  // whole rows, and nothing stays evicted
+    for (int l = 0; l < c.n_layers; ++l) {
+      const size_t row_bytes = (size_t)2 * c.n_heads * ctx->tiles * tb;
+      CK(cudaMemsetAsync(ctx->kv4 + ctx->kv4_layer * l + r0 * row_bytes, 0, (r1 - r0) * row_bytes, ctx->st), "kv reset");
+      CK(cudaMemsetAsync(ctx->hole + (size_t)l * c.max_rows + r0, 0, (r1 - r0) * sizeof(int2), ctx->st), "kv reset");
+      if (ctx->wts)
+        CK(cudaMemsetAsync(ctx->wts + ((size_t)l * c.max_rows + r0) * c.n_heads * SLt, 0,
+                           (r1 - r0) * c.n_heads * SLt * sizeof(float), ctx->st),
+           "kv reset");
+      for (int r = r0; r < r1; ++r) ctx->hole_h[(size_t)l * c.max_rows + r] = int2{0, 0};
+    }
+    return UOCR_OK;
+  }
+  for (int l = 0; l < c.n_layers; ++l)
+    for (int r = r0; r < r1; ++r) CK(launch_kv4_zero(kv4_append_args(ctx, l), r, from, ctx->SL - from, ctx->st), "kv reset");
+  return UOCR_OK;
+}
+
+static uocr_status kv4_io(uocr_ctx* ctx, int row, int layer, int slot0, int n, uint8_t* const codes[2],
+                          uint16_t* const scale[2], uint16_t* const low[2], bool put) {
+  const uocr_config& c = ctx->cfg;
+  if (n == 0) return UOCR_OK;
+  const size_t vecs = (size_t)c.n_heads * n, cb = vecs * c.head_dim, gb = vecs * (c.head_dim / kKv4Group) * 2;
+  void* stage = nullptr;
+  CK(cudaMalloc(&stage, 2 * (cb + 2 * gb)), "kv staging allocation");
+  Kv4IoArgs a{};
+  a.kv4 = ctx->kv4 + ctx->kv4_layer * layer + (size_t)row * 2 * c.n_heads * ctx->tiles * kv4_tile_bytes(c.head_dim);
+  a.wts = ctx->wts ? ctx->wts + ((size_t)layer * c.max_rows + row) * c.n_heads * ctx->tiles * kKv4Slots : nullptr;
+  uint8_t* p = reinterpret_cast<uint8_t*>(stage);
+  for (int kv = 0; kv < 2; ++kv) {
+    a.codes[kv] = p;
+    a.scale[kv] = reinterpret_cast<__half*>(p + cb);
+    a.low[kv] = reinterpret_cast<__half*>(p + cb + gb);
+    p += cb + 2 * gb;
+  }
+  a.nh = c.n_heads;
+  a.D = c.head_dim;
+  a.tiles = ctx->tiles;
+  a.slot0 = slot0;
+  a.n = n;
+  a.put = put;
+  cudaError_t e = cudaSuccess;
+  auto copies = [&]() {  // host or device buffers of the caller
+    for (int kv = 0; kv < 2 && e == cudaSuccess; ++kv) {
+      void* mine[3] = {a.codes[kv], a.scale[kv], a.low[kv]};
+      void* theirs[3] = {codes[kv], scale[kv], low[kv]};
+      const size_t bytes[3] = {cb, gb, gb};
+      for (int i = 0; i < 3 && e == cudaSuccess; ++i)
+        e = put ? cudaMemcpyAsync(mine[i], theirs[i], bytes[i], cudaMemcpyDefault, ctx->st)
+                : cudaMemcpyAsync(theirs[i], mine[i], bytes[i], cudaMemcpyDefault, ctx->st);
+    }
+  };
+  if (put) copies();
+  if (e == cudaSuccess) e = launch_kv4_io(a, ctx->st);
+  if (!put) copies();
+  if (e == cudaSuccess) e = cudaStreamSynchronize(ctx->st);
+  cudaFree(stage);
+  return ctx->cuda(e, "kv entries");
+}
+
+static uocr_status kv4_check(uocr_ctx* ctx, const char* what, int layer) {
+  if (!ctx->kv4) return ctx->fail(UOCR_E_STATE, "%s: the context has no 4-bit cache (kv_int4 = 0)", what);
+  if (layer < 0 || layer >= ctx->cfg.n_layers)
+    return ctx->fail(UOCR_E_INVALID_ARG, "%s: layer %d outside [0, %d)", what, layer, ctx->cfg.n_layers);
+  return UOCR_OK;
+}
+
+static uocr_status kv4_check_chunk(uocr_ctx* ctx, const char* what, int layer, int row, int start_pos, int n) {
+  uocr_status s = kv4_check(ctx, what, layer);
+  if (s != UOCR_OK) return s;
+  if (row < 0 || row >= ctx->cfg.max_rows)
+    return ctx->fail(UOCR_E_INVALID_ARG, "%s: row %d outside [0, %d)", what, row, ctx->cfg.max_rows);
+  if (n < 1 || start_pos < 0 || (long long)start_pos + n > (long long)ctx->SL)
+    return ctx->fail(UOCR_E_INVALID_ARG,
+                     "%s: %d positions from %d must be at least one and lie in [0, prefix_len + ring_len = %d) (no ring wrap)",
+                     what, n, start_pos, ctx->SL);
+  if (below_hole(ctx, row, layer, start_pos))
+    return ctx->fail(UOCR_E_STATE, "%s: position %d of row %d lies in an evicted prefix", what, start_pos, row);
+  return UOCR_OK;
+}
+
+static uocr_status kv4_check_q_heads(uocr_ctx* ctx, const char* what, int q_heads) {
+  const int nh = ctx->cfg.n_heads;
+  if (q_heads < nh || q_heads % nh || q_heads / nh > 8)
+    return ctx->fail(UOCR_E_INVALID_ARG, "%s: q_heads %d is not one to eight times n_heads = %d", what, q_heads, nh);
+  return UOCR_OK;
+}
+
+// Fill the operator form of the append from the caller's struct.
+static uocr_status kv4_append_from(uocr_ctx* ctx, const char* what, const uocr_qkv* x, Kv4AppendArgs& a) {
+  const uocr_config& c = ctx->cfg;
+  if (!x || !x->k || !x->v) return ctx->fail(UOCR_E_INVALID_ARG, "%s: NULL pointer", what);
+  if ((x->q == nullptr) != (x->q_out == nullptr) || (!x->q && x->q_heads != 0))
+    return ctx->fail(UOCR_E_INVALID_ARG, "%s: q, q_heads and q_out come together", what);
+  if (x->dtype < UOCR_DT_F32 || x->dtype > UOCR_DT_BF16) return ctx->fail(UOCR_E_INVALID_ARG, "%s: unknown dtype", what);
+  if (x->q) {
+    uocr_status s = kv4_check_q_heads(ctx, what, x->q_heads);
+    if (s != UOCR_OK) return s;
+  }
+  const long long kw = ctx->S, qw = (long long)x->q_heads * c.head_dim;
+  if ((x->ld_q && x->ld_q < qw) || (x->ld_k && x->ld_k < kw) || (x->ld_v && x->ld_v < kw))
+    return ctx->fail(UOCR_E_INVALID_ARG, "%s: a token stride is shorter than a token", what);
+  a.q = x->q;
+  a.k = x->k;
+  a.v = x->v;
+  a.ldq = x->ld_q ? x->ld_q : qw;
+  a.ldk = x->ld_k ? x->ld_k : kw;
+  a.ldv = x->ld_v ? x->ld_v : kw;
+  a.lhk = c.head_dim;
+  a.dtype = x->dtype;
+  a.rotate = 1;
+  a.q_heads = x->q_heads;
+  a.q_out = x->q_out;
+  a.k_val = reinterpret_cast<__half*>(x->k_val);
+  a.v_val = reinterpret_cast<__half*>(x->v_val);
+  return UOCR_OK;
+}
+
+static uocr_status kv4_weights(uocr_ctx* ctx, const char* what, int layer, int row0, int n_rows, int slot0, int n,
+                               float* dense, bool put) {
+  const uocr_config& c = ctx->cfg;
+  if (!ctx->wts) return ctx->fail(UOCR_E_STATE, "%s: the context accumulates no weights (kv_track = 0)", what);
+  if (!dense || layer < -1 || layer >= c.n_layers || row0 < 0 || n_rows < 1 || n_rows > c.max_rows - row0 || slot0 < 0 ||
+      n < 0 || n > ctx->SL - slot0)
+    return ctx->fail(UOCR_E_INVALID_ARG, "%s: NULL pointer or bad layer/row/slot range", what);
+  OnDevice dev(c.device);
+  CK(dev.e, "set device");
+  uocr_status s = kv4_begin(ctx);
+  if (s != UOCR_OK) return s;
+  Kv4WeightsArgs a{};
+  a.wts = ctx->wts;
+  a.dense = dense;
+  a.MR = c.max_rows;
+  a.nh = c.n_heads;
+  a.tiles = ctx->tiles;
+  a.layer0 = layer < 0 ? 0 : layer;
+  a.layers = layer < 0 ? c.n_layers : 1;
+  a.row0 = row0;
+  a.rows = n_rows;
+  a.slot0 = slot0;
+  a.n = n;
+  a.put = put;
+  CK(launch_kv4_weights(a, ctx->st), "weights launch");
+  return step_epilogue(ctx);
+}
+
+extern "C" {
+
+uocr_status uocr_kv_write_i4(uocr_ctx* ctx, int32_t row, int32_t layer, int32_t slot0, int32_t n,
+                             const uint8_t* k_codes, const uint16_t* k_scale, const uint16_t* k_min,
+                             const uint8_t* v_codes, const uint16_t* v_scale, const uint16_t* v_min) {
+  if (!ctx) return UOCR_E_INVALID_ARG;
+  std::lock_guard<std::mutex> lk(ctx->mu);
+  uocr_status s = kv4_check(ctx, "kv_write_i4", layer);
+  if (s != UOCR_OK) return s;
+  if (!k_codes || !k_scale || !k_min || !v_codes || !v_scale || !v_min || row < 0 || row >= ctx->cfg.max_rows ||
+      slot0 < 0 || n < 0 || n > ctx->SL - slot0)
+    return ctx->fail(UOCR_E_INVALID_ARG, "kv_write_i4: NULL pointer or bad row/slot range");
+  if (in_hole(ctx, row, layer, slot0, n)) return ctx->fail(UOCR_E_STATE, "kv_write_i4: the slots are evicted");
+  OnDevice dev(ctx->cfg.device);
+  CK(dev.e, "set device");
+  s = kv4_begin(ctx);  // device buffers of the caller's stream
+  if (s != UOCR_OK) return s;
+  uint8_t* const codes[2] = {const_cast<uint8_t*>(k_codes), const_cast<uint8_t*>(v_codes)};
+  uint16_t* const scale[2] = {const_cast<uint16_t*>(k_scale), const_cast<uint16_t*>(v_scale)};
+  uint16_t* const low[2] = {const_cast<uint16_t*>(k_min), const_cast<uint16_t*>(v_min)};
+  return kv4_io(ctx, row, layer, slot0, n, codes, scale, low, true);
+}
+
+uocr_status uocr_kv_read_i4(uocr_ctx* ctx, int32_t row, int32_t layer, int32_t slot0, int32_t n, uint8_t* k_codes,
+                            uint16_t* k_scale, uint16_t* k_min, uint8_t* v_codes, uint16_t* v_scale, uint16_t* v_min) {
+  if (!ctx) return UOCR_E_INVALID_ARG;
+  std::lock_guard<std::mutex> lk(ctx->mu);
+  uocr_status s = kv4_check(ctx, "kv_read_i4", layer);
+  if (s != UOCR_OK) return s;
+  if (!k_codes || !k_scale || !k_min || !v_codes || !v_scale || !v_min || row < 0 || row >= ctx->cfg.max_rows ||
+      slot0 < 0 || n < 0 || n > ctx->SL - slot0)
+    return ctx->fail(UOCR_E_INVALID_ARG, "kv_read_i4: NULL pointer or bad row/slot range");
+  OnDevice dev(ctx->cfg.device);
+  CK(dev.e, "set device");
+  s = kv4_begin(ctx);
+  if (s != UOCR_OK) return s;
+  uint8_t* const codes[2] = {k_codes, v_codes};
+  uint16_t* const scale[2] = {k_scale, v_scale};
+  uint16_t* const low[2] = {k_min, v_min};
+  return kv4_io(ctx, row, layer, slot0, n, codes, scale, low, false);
+}
+
+uocr_status uocr_kv_append(uocr_ctx* ctx, int32_t layer, int32_t rows, const int32_t* positions, const uocr_qkv* x) {
+  if (!ctx) return UOCR_E_INVALID_ARG;
+  std::lock_guard<std::mutex> lk(ctx->mu);
+  uocr_status s = kv4_check(ctx, "kv_append", layer);
+  if (s != UOCR_OK) return s;
+  if (rows < 1 || rows > ctx->cfg.max_rows || !positions)
+    return ctx->fail(UOCR_E_INVALID_ARG, "kv_append: NULL positions or rows %d outside [1, max_rows = %d]", rows,
+                     ctx->cfg.max_rows);
+  Kv4AppendArgs a = kv4_append_args(ctx, layer);
+  s = kv4_append_from(ctx, "kv_append", x, a);
+  if (s != UOCR_OK) return s;
+  a.pos = positions;
+  a.kv_rstep = 1;
+  OnDevice dev(ctx->cfg.device);
+  CK(dev.e, "set device");
+  s = kv4_begin(ctx);
+  if (s != UOCR_OK) return s;
+  CK(launch_kv4_append(a, rows, ctx->st, false), "kv append launch");
+  return step_epilogue(ctx);
+}
+
+uocr_status uocr_kv_append_chunk(uocr_ctx* ctx, int32_t layer, int32_t row, int32_t start_pos, int32_t n,
+                                 const uocr_qkv* x) {
+  if (!ctx) return UOCR_E_INVALID_ARG;
+  std::lock_guard<std::mutex> lk(ctx->mu);
+  uocr_status s = kv4_check_chunk(ctx, "kv_append_chunk", layer, row, start_pos, n);
+  if (s != UOCR_OK) return s;
+  Kv4AppendArgs a = kv4_append_args(ctx, layer);
+  s = kv4_append_from(ctx, "kv_append_chunk", x, a);
+  if (s != UOCR_OK) return s;
+  a.pos0 = start_pos;
+  a.kv_row0 = row;
+  OnDevice dev(ctx->cfg.device);
+  CK(dev.e, "set device");
+  s = kv4_begin(ctx);
+  if (s != UOCR_OK) return s;
+  CK(launch_kv4_append(a, n, ctx->st, false), "kv append launch");
+  return step_epilogue(ctx);
+}
+
+uocr_status uocr_attend(uocr_ctx* ctx, int32_t layer, int32_t rows, const int32_t* positions, int32_t q_heads,
+                        const float* q, int32_t out_dtype, void* out) {
+  if (!ctx) return UOCR_E_INVALID_ARG;
+  std::lock_guard<std::mutex> lk(ctx->mu);
+  uocr_status s = kv4_check(ctx, "attend", layer);
+  if (s == UOCR_OK) s = kv4_check_q_heads(ctx, "attend", q_heads);
+  if (s != UOCR_OK) return s;
+  if (rows < 1 || rows > ctx->cfg.max_rows || !positions || !q || !out || out_dtype < UOCR_DT_F32 ||
+      out_dtype > UOCR_DT_BF16)
+    return ctx->fail(UOCR_E_INVALID_ARG, "attend: NULL pointer, unknown dtype or rows %d outside [1, max_rows = %d]", rows,
+                     ctx->cfg.max_rows);
+  if (ctx->cfg.use_sink && !ctx->sinks_set) return ctx->fail(UOCR_E_STATE, "use_sink = 1 but uocr_set_sinks was not called");
+  Kv4AttnArgs a = kv4_attn_args(ctx, layer);
+  a.q = q;
+  a.q_heads = q_heads;
+  a.out = out;
+  a.out_dtype = out_dtype;
+  a.pos = positions;
+  a.kv_rstep = 1;
+  OnDevice dev(ctx->cfg.device);
+  CK(dev.e, "set device");
+  s = kv4_begin(ctx);
+  if (s != UOCR_OK) return s;
+  CK(launch_kv4_attn(a, rows, ctx->st, false), "attention launch");
+  return step_epilogue(ctx);
+}
+
+uocr_status uocr_attend_chunk(uocr_ctx* ctx, int32_t layer, int32_t row, int32_t start_pos, int32_t n, int32_t q_heads,
+                              const float* q, int32_t out_dtype, void* out) {
+  if (!ctx) return UOCR_E_INVALID_ARG;
+  std::lock_guard<std::mutex> lk(ctx->mu);
+  uocr_status s = kv4_check_chunk(ctx, "attend_chunk", layer, row, start_pos, n);
+  if (s == UOCR_OK) s = kv4_check_q_heads(ctx, "attend_chunk", q_heads);
+  if (s != UOCR_OK) return s;
+  if (!q || !out || out_dtype < UOCR_DT_F32 || out_dtype > UOCR_DT_BF16)
+    return ctx->fail(UOCR_E_INVALID_ARG, "attend_chunk: NULL pointer or unknown dtype");
+  if (ctx->cfg.use_sink && !ctx->sinks_set) return ctx->fail(UOCR_E_STATE, "use_sink = 1 but uocr_set_sinks was not called");
+  OnDevice dev(ctx->cfg.device);
+  CK(dev.e, "set device");
+  s = kv4_begin(ctx);
+  if (s != UOCR_OK) return s;
+  // the softmax statistics of the weights' accumulation hold kTokCap tokens
+  const int step = ctx->wts ? kTokCap : n;
+  const int D = ctx->cfg.head_dim, esz = out_dtype == UOCR_DT_F32 ? 4 : 2;
+  for (int off = 0; off < n; off += step) {
+    Kv4AttnArgs a = kv4_attn_args(ctx, layer);
+    a.q = q + (size_t)off * q_heads * D;
+    a.q_heads = q_heads;
+    a.out = reinterpret_cast<uint8_t*>(out) + (size_t)off * q_heads * D * esz;
+    a.out_dtype = out_dtype;
+    a.pos0 = start_pos + off;
+    a.kv_row0 = row;
+    CK(launch_kv4_attn(a, n - off < step ? n - off : step, ctx->st, false), "attention launch");
+  }
+  return step_epilogue(ctx);
+}
+
+uocr_status uocr_kv_evict(uocr_ctx* ctx, int32_t layer, int32_t n_rows, const int32_t* src_rows, const int32_t* dst_rows,
+                          int32_t n, int32_t keep, int32_t protect, int32_t* kept, uint16_t* k_val, uint16_t* v_val) {
+  if (!ctx) return UOCR_E_INVALID_ARG;
+  std::lock_guard<std::mutex> lk(ctx->mu);
+  const uocr_config& c = ctx->cfg;
+  uocr_status s = kv4_check(ctx, "kv_evict", layer == -1 ? 0 : layer);
+  if (s != UOCR_OK) return s;
+  if (!ctx->wts) return ctx->fail(UOCR_E_STATE, "kv_evict: the context accumulates no weights (kv_track = 0)");
+  if (!src_rows || !dst_rows || n_rows < 1 || n_rows > c.max_rows)
+    return ctx->fail(UOCR_E_INVALID_ARG, "kv_evict: NULL rows or n_rows %d outside [1, max_rows = %d]", n_rows, c.max_rows);
+  if (n < 1 || n > c.prefix_len || keep < 0 || protect < 0 || protect > keep)
+    return ctx->fail(UOCR_E_INVALID_ARG, "kv_evict: n in [1, prefix_len], keep >= 0 and protect in [0, keep] required");
+  Kv4EvictArgs a{};
+  for (int i = 0; i < n_rows; ++i) {
+    const int rs = src_rows[i], rd = dst_rows[i];
+    if (rs < 0 || rs >= c.max_rows || rd < 0 || rd >= c.max_rows)
+      return ctx->fail(UOCR_E_INVALID_ARG, "kv_evict: row pair (%d, %d) outside [0, %d)", rs, rd, c.max_rows);
+    for (int j = 0; j < n_rows; ++j)
+      if (j != i && (dst_rows[j] == rd || src_rows[j] == rd))
+        return ctx->fail(UOCR_E_INVALID_ARG, "kv_evict: row %d is written and used twice", rd);
+    a.src[i] = (unsigned char)rs;
+    a.dst[i] = (unsigned char)rd;
+  }
+  a.layer0 = layer < 0 ? 0 : layer;
+  a.layers = layer < 0 ? c.n_layers : 1;
+  for (int l = a.layer0; l < a.layer0 + a.layers; ++l)
+    for (int i = 0; i < n_rows; ++i) {
+      const int2 h = ctx->hole_h[(size_t)l * c.max_rows + src_rows[i]];
+      const int gap = h.y - h.x;
+      if (gap > 0 && n < h.y)
+        return ctx->fail(UOCR_E_INVALID_ARG, "kv_evict: n = %d lies in row %d's evicted slots [%d, %d)", n, src_rows[i], h.x,
+                         h.y);
+      if (keep > n - gap)
+        return ctx->fail(UOCR_E_INVALID_ARG, "kv_evict: keep = %d of the %d entries that row %d holds", keep, n - gap,
+                         src_rows[i]);
+    }
+  a.kv4 = ctx->kv4;
+  a.wts = ctx->wts;
+  a.hole = ctx->hole;
+  a.kept = kept;
+  a.k_val = reinterpret_cast<__half*>(k_val);
+  a.v_val = reinterpret_cast<__half*>(v_val);
+  a.MR = c.max_rows;
+  a.nh = c.n_heads;
+  a.D = c.head_dim;
+  a.tiles = ctx->tiles;
+  a.rows = n_rows;
+  a.n = n;
+  a.keep = keep;
+  a.protect = protect;
+  OnDevice dev(c.device);
+  CK(dev.e, "set device");
+  s = kv4_begin(ctx);
+  if (s != UOCR_OK) return s;
+  CK(launch_kv4_evict(a, ctx->st), "eviction launch");
+  for (int l = a.layer0; l < a.layer0 + a.layers; ++l)
+    for (int i = 0; i < n_rows; ++i)
+      ctx->hole_h[(size_t)l * c.max_rows + dst_rows[i]] = keep < n ? int2{keep, n} : int2{0, 0};
+  return step_epilogue(ctx);
+}
+
+uocr_status uocr_kv_weights_read(uocr_ctx* ctx, int32_t layer, int32_t row0, int32_t n_rows, int32_t slot0, int32_t n,
+                                 float* out) {
+  if (!ctx) return UOCR_E_INVALID_ARG;
+  std::lock_guard<std::mutex> lk(ctx->mu);
+  return kv4_weights(ctx, "kv_weights_read", layer, row0, n_rows, slot0, n, out, false);
+}
+
+uocr_status uocr_kv_weights_write(uocr_ctx* ctx, int32_t layer, int32_t row0, int32_t n_rows, int32_t slot0, int32_t n,
+                                  const float* in) {
+  if (!ctx) return UOCR_E_INVALID_ARG;
+  std::lock_guard<std::mutex> lk(ctx->mu);
+  return kv4_weights(ctx, "kv_weights_write", layer, row0, n_rows, slot0, n, const_cast<float*>(in), true);
 }
 
 }  // extern "C"

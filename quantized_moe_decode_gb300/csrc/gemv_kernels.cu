@@ -143,10 +143,12 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) k_gemv(const GemvArgs a)
         const int wi = pr - sec * a.S;
         const int head = wi / a.D;
         const int js = (wi - head * a.D) >> 4;
-        const int dlo = 8 * js + pg, dhi = (a.D >> 1) + dlo;
+        const int pair = 8 * js + pg;
+        int dlo, dhi;
+        rope_pair(a.rope_layout, a.rope_dims, pair, dlo, dhi);
         float vlo = lo, vhi = hi;
-        if (sec < 2) {
-          const float2 r = s_rope[tok * (a.D / 2) + dlo];  // (cos, sin) of this position's angle
+        if (sec < 2 && pair < (a.rope_dims >> 1)) {
+          const float2 r = s_rope[tok * (a.D / 2) + pair];  // (cos, sin) of this position's angle
           vlo = lo * r.x - hi * r.y;
           vhi = hi * r.x + lo * r.y;
         }

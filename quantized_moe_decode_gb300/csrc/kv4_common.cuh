@@ -1,0 +1,175 @@
+// Layout of the 4-bit KV cache and the arithmetic of its entries.
+//
+// Entry (one head's key or value vector): per group of 32 dimensions an fp16
+// scale s and minimum m and 32 codes q in 0..15; its value is the fp16 number
+// nearest to s q + m (one fused multiply-add in fp16).
+//
+// A (row, K|V, head) holds tiles of 16 slots, 10 D bytes each: 8 D bytes of
+// codes, 2 D bytes of scales and minima.  The order inside a tile is that of
+// the m16n8k16 tensor-core A fragment, so that lane L = 4 g + t of a warp
+// finds everything it feeds the products with in bytes that it alone reads:
+//   keys    the fragment's rows are slots, its columns dimensions: lane (g, t)
+//           holds dimensions [t D/4, (t+1) D/4) of slots g and g + 8;
+//   values  rows are dimensions, columns slots: lane (g, t) holds dimensions
+//           [g D/8, (g+1) D/8) of slots 2t, 2t+1, 2t+8, 2t+9, the two slots of
+//           a pair side by side in the halves of a word.
+// A lane's D/4 bytes are stored 16 at a time, lanes side by side (head_dim 32:
+// 8 bytes per lane), so a warp's loads are whole contiguous 512-byte pieces.
+#pragma once
+#include <cuda_fp16.h>
+
+#include "device_common.cuh"
+
+namespace uocr {
+
+constexpr int kKv4Slots = 16;  // slots of a tile
+constexpr int kKv4Group = 32;  // dimensions that share a scale and a minimum
+
+__host__ __device__ constexpr int kv4_tile_bytes(int D) { return 10 * D; }
+
+// byte o of lane's stream of D/4 bytes
+__device__ __forceinline__ int kv4_stream(int D, int lane, int o) {
+  return D >= 64 ? (o >> 4) * 512 + lane * 16 + (o & 15) : lane * 8 + o;
+}
+// key word i (32 bits: dimensions 8i .. 8i+7) of slot s; dimension 8i + j is
+// nibble (j >> 1) + 4 (j & 1): a word's halves hold neighbouring dimensions
+__device__ __forceinline__ int kv4_k_word(int D, int s, int i) {
+  const int wpc = D / 32;
+  return kv4_stream(D, (s & 7) * 4 + i / wpc, (s >> 3) * (D / 8) + (i % wpc) * 4);
+}
+// value quad i (16 bits: dimensions 4i .. 4i+3, one nibble each) of slot s
+__device__ __forceinline__ int kv4_v_quad(int D, int s, int i) {
+  const int qpc = D / 32;
+  return kv4_stream(D, (i / qpc) * 4 + ((s & 7) >> 1), (((s >> 3) * qpc + i % qpc) * 2 + (s & 1)) * 2);
+}
+// (s, m) pair of slot s, group grp of the keys
+__device__ __forceinline__ int kv4_k_param(int D, int s, int grp) {
+  return 8 * D + (((s & 7) * (D / 32) + grp) * 2 + (s >> 3)) * 4;
+}
+// scale (which = 0) or minimum (1) of slot s, group grp of the values: the two
+// slots of a pair side by side
+__device__ __forceinline__ int kv4_v_param(int D, int s, int grp, int which) {
+  return 8 * D + (grp * 4 + ((s & 7) >> 1)) * 16 + (s >> 3) * 8 + which * 4 + (s & 1) * 2;
+}
+
+// Scale and minimum of a group from its extremes (fp32 decisions): m is the
+// minimum rounded to fp16, s = (max - m) times fp32(1/15), rounded toward
+// zero, so that no value of the group leaves the fp16 range.  A group that holds a NaN or a
+// value beyond the fp16 range (ok = false) reads as NaN.
+__device__ __forceinline__ void kv4_params(float mn, float mx, bool ok, __half& s, __half& m) {
+  m = ok ? __float2half_rn(mn) : __ushort_as_half((unsigned short)0x7FFF);
+  s = ok ? __float2half_rz(fmaxf((mx - __half2float(m)) * (1.0f / 15.0f), 0.f)) : __ushort_as_half((unsigned short)0);
+}
+__device__ __forceinline__ uint32_t kv4_code(float x, float s, float m) {
+  if (!(s > 0.f)) return 0u;
+  return (uint32_t)fminf(fmaxf(rintf((x - m) / s), 0.f), 15.f);
+}
+__device__ __forceinline__ __half kv4_value(uint32_t code, __half s, __half m) {
+  return __hfma(s, __ushort2half_rn((unsigned short)code), m);
+}
+
+// Slot of a position, and how many slots (a prefix of the slot order) a query
+// at that position may read.
+__device__ __forceinline__ int kv_slot(int p, int P, int R) { return p < P ? p : P + (p - P) % R; }
+__device__ __forceinline__ int kv_limit(int p, int P, int R) { return p < P ? p + 1 : P + min(p - P + 1, R); }
+
+// element i of an fp32 / fp16 / bf16 array (uocr_dtype)
+__device__ __forceinline__ float load_elem(const void* p, int dtype, long long i) {
+  if (dtype == 0) return reinterpret_cast<const float*>(p)[i];
+  const unsigned short u = reinterpret_cast<const unsigned short*>(p)[i];
+  return dtype == 1 ? __half2float(__ushort_as_half(u)) : __uint_as_float((uint32_t)u << 16);
+}
+__device__ __forceinline__ void store_elem(void* p, int dtype, long long i, float v) {
+  if (dtype == 0) {
+    reinterpret_cast<float*>(p)[i] = v;
+  } else if (dtype == 1) {
+    reinterpret_cast<__half*>(p)[i] = __float2half_rn(v);
+  } else {  // bf16, round to nearest even; a NaN stays one
+    const uint32_t u = __float_as_uint(v);
+    const uint32_t r = (v != v) ? 0x7FFFu : (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
+    reinterpret_cast<unsigned short*>(p)[i] = (unsigned short)r;
+  }
+}
+
+// ---- launch arguments
+// Rotate (operator form) and append key / value vectors.
+struct Kv4AppendArgs {
+  const void *q, *k, *v;       // element (token t, head h, dim d) at t ld + h lh + d
+  long long ldq, ldk, ldv;
+  long long lhk;               // head stride of k and v (q heads are D apart)
+  int dtype;                   // uocr_dtype of q, k, v
+  int rotate;                  // 1: rotate q and k by their position
+  const double* inv_freq;      // [D/2]
+  double amp;
+  int rope_layout, rope_dims;
+  int q_heads, nh, D;
+  float* q_out;                // [tokens][q_heads][D] or nullptr
+  __half *k_val, *v_val;       // [tokens][nh][D] or nullptr: the stored entries' values
+  uint8_t* kv4;                // layer base of the cache
+  float* wts;                  // layer base of the accumulated weights, or nullptr
+  const int2* hole;            // [rows] evicted slots [x, y) of the layer
+  const int* pos;              // [tokens], or nullptr: pos0 + t
+  int pos0;
+  int slots;                   // 1: pos0 counts slots, not positions
+  int P, R, tiles;
+  int kv_row0, kv_rstep;
+  int* status;
+};
+cudaError_t launch_kv4_append(const Kv4AppendArgs& a, int tokens, cudaStream_t st, bool pdl);
+// Zero the entries and weights of slots [slot0, slot0 + n) of a row.
+cudaError_t launch_kv4_zero(const Kv4AppendArgs& a, int row, int slot0, int n, cudaStream_t st);
+
+struct Kv4AttnArgs {
+  const float* q;              // [tokens][q_heads][D]
+  const uint8_t* kv4;          // layer base
+  void* out;                   // [tokens][q_heads][D]
+  int out_dtype;
+  const float* sink;           // [nh] or nullptr
+  const int2* hole;            // [rows]
+  const int* pos;              // [tokens], or nullptr: pos0 + t
+  int pos0;
+  float* wts;                  // layer base of the accumulated weights, or nullptr
+  float2* lse;                 // [tokens][q_heads] (maximum, 1 / sum) when wts is given
+  int q_heads, nh, D, P, R, tiles;
+  int kv_row0, kv_rstep;       // kv_rstep 0: every token belongs to cache row kv_row0
+  float scale;
+  int* status;
+};
+cudaError_t launch_kv4_attn(const Kv4AttnArgs& a, int tokens, cudaStream_t st, bool pdl);
+
+// Host-visible entries: codes one per byte [nh][n][D], scales and minima
+// [nh][n][D/32], for K and V of one (layer, row).
+struct Kv4IoArgs {
+  uint8_t* kv4;                // of the (layer, row)
+  float* wts;                  // of the (layer, row), or nullptr: zeroed where entries are written
+  uint8_t* codes[2];
+  __half* scale[2];
+  __half* low[2];
+  __half* val[2];              // values instead of entries (read only), or nullptr
+  int nh, D, tiles, slot0, n, put;
+};
+cudaError_t launch_kv4_io(const Kv4IoArgs& a, cudaStream_t st);
+
+// Accumulated weights of slots [slot0, slot0 + n) of rows [row0, row0 + rows)
+// in layers [layer0, layer0 + layers): dense [layers][rows][nh][n].
+struct Kv4WeightsArgs {
+  float* wts;                  // [L][MR][nh][16 tiles]
+  float* dense;
+  int MR, nh, tiles, layer0, layers, row0, rows, slot0, n, put;
+};
+cudaError_t launch_kv4_weights(const Kv4WeightsArgs& a, cudaStream_t st);
+
+constexpr int kKv4MaxRows = 64;
+struct Kv4EvictArgs {
+  uint8_t* kv4;                // [L][MR][2][nh][tiles]
+  float* wts;                  // [L][MR][nh][16 tiles]
+  int2* hole;                  // [L][MR]
+  int* kept;                   // [layers][rows][nh][keep] or nullptr
+  __half *k_val, *v_val;       // [layers][rows][nh][keep][D] or nullptr
+  int MR, nh, D, tiles, layer0, layers, rows, n, keep, protect;
+  unsigned char src[kKv4MaxRows], dst[kKv4MaxRows];
+};
+cudaError_t launch_kv4_evict(const Kv4EvictArgs& a, cudaStream_t st);
+cudaError_t init_kv4_attributes();
+
+}  // namespace uocr

@@ -54,6 +54,7 @@ struct GemvArgs {
   float* q_out;             // [rows][nh][D]
   __half* kv;               // layer base [rows][2][nh][SL][D]
   const float2* rope;       // [rows][D/2] (cos, sin) of the step's positions
+  int rope_layout, rope_dims;
   int nh, D, S, P, R, SL;
   int kv_row0, kv_rstep;    // token t writes cache row kv_row0 + t * kv_rstep (decode: 0, 1; prefill: row, 0)
   float* kv_new;            // INT8 cache: rotated k and v go here in fp32 [tokens][2][nh][D] (k_kv_quant
@@ -161,6 +162,7 @@ struct EmbedArgs {
   const double* inv_freq;   // [half_d]
   float2* rope;             // [rows][half_d]
   int half_d;
+  float amp;                // amplitude of cos and sin (1 unless the frequencies are scaled)
   int* status;
 };
 
@@ -174,6 +176,7 @@ struct PackArgs {
   int src_rows, src_cols;   // shape of each source
   int nsrc;
   int S, D;                 // MAP_QKV: section rows, head dim
+  int rope_layout, rope_dims;  // MAP_QKV: which dimensions form pair j (rope_pair)
   int I;                    // MAP_SWIGLU: rows per source expert; MAP_KCAT: cols per source
 };
 enum PackMap : int { MAP_IDENT = 0, MAP_QKV = 1, MAP_SWIGLU = 2, MAP_KCAT = 3 };

@@ -78,6 +78,17 @@ class ModelConfig:
     act_int8: int = 0  # dynamic int8 activations (groups of 32) on the dense projections
     proj_in: int = 0  # projector input width (visual features; 0 = no projector)
     fmt_proj: int = Q8_0
+    # rotary positions (the defaults: the whole head in rotate-half pairs, unscaled)
+    kv_int4: int = 0       # 4-bit KV cache (scale and minimum per 32 dimensions)
+    kv_track: int = 0      # accumulate every entry's attention weight (for the eviction)
+    rope_layout: int = 0   # 0 rotate-half pairs, 1 neighbouring pairs
+    rope_dims: int = 0     # rotated dimensions of a head (0 = all)
+    rope_scaling: int = 0  # 0 none, 1 linear, 2 YaRN
+    rope_orig_len: int = 0
+    rope_factor: float = 1.0
+    rope_beta_fast: float = 0.0
+    rope_beta_slow: float = 0.0
+    rope_mscale: float = 0.0
 
     @property
     def moe(self) -> bool:
