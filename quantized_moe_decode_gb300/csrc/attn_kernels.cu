@@ -863,6 +863,7 @@ cudaError_t init_gemv_attributes();
 cudaError_t init_moe_attributes();
 cudaError_t init_tc_attributes();
 cudaError_t init_tc_expert_attributes();
+cudaError_t init_kv4_attributes();
 
 cudaError_t init_kernel_attributes() {
   cudaError_t e = init_gemv_attributes();
@@ -870,6 +871,7 @@ cudaError_t init_kernel_attributes() {
   if (e == cudaSuccess) e = init_attn_attributes();
   if (e == cudaSuccess) e = init_tc_attributes();
   if (e == cudaSuccess) e = init_tc_expert_attributes();
+  if (e == cudaSuccess) e = init_kv4_attributes();
   return e;
 }
 

@@ -144,7 +144,11 @@ struct uocr_ctx {
   int2* hole = nullptr;        // 4-bit cache: evicted slots [x, y) of each [L][MR]
   std::vector<int2> hole_h;    // ... the same on the host
   float* wts = nullptr;        // accumulated weights [L][MR][nh][16 tiles] (kv_track)
-  float2* lse = nullptr;       // softmax statistics of one pass [kTokCap][8 nh] (kv_track)
+  float* scores = nullptr;     // kv_track: scores of one pass [track_q][nh][16 tiles]
+  float2* lse = nullptr;       // ... and softmax statistics [track_q][nh]
+  // queries per cache head of one tracked pass: a step's rows with eight heads
+  // on each cache head, or a prefill chunk
+  int track_q() const { return cfg.max_rows * 8 > kTokCap ? cfg.max_rows * 8 : kTokCap; }
   float* kv_new = nullptr;     // quantised caches: the pass's new keys / values in fp32 [kTokCap][2][nh][D]
   size_t kv_layer = 0;         // entries (codes or fp16 values) per layer
   size_t kvs_layer = 0;        // scales per layer
@@ -407,7 +411,8 @@ static void carve(uocr_ctx* ctx, Carver& cv) {
     ctx->hole = cv.take<int2>((size_t)Lc * MR, r.kv_cache);
     if (c.kv_track) {
       ctx->wts = cv.take<float>((size_t)Lc * MR * c.n_heads * ctx->tiles * kKv4Slots, r.kv_cache);
-      ctx->lse = cv.take<float2>((size_t)TC * 8 * c.n_heads, r.activations);
+      ctx->scores = cv.take<float>((size_t)ctx->track_q() * c.n_heads * ctx->tiles * kKv4Slots, r.activations);
+      ctx->lse = cv.take<float2>((size_t)ctx->track_q() * c.n_heads, r.activations);
     }
     ctx->kv_new = cv.take<float>((size_t)TC * 2 * S, r.activations);
   } else {
@@ -513,7 +518,9 @@ static Kv4AttnArgs kv4_attn_args(uocr_ctx* ctx, int layer) {
   a.sink = c.use_sink ? ctx->sinks + (size_t)layer * c.n_heads : nullptr;
   a.hole = ctx->hole + (size_t)layer * c.max_rows;
   a.wts = ctx->wts ? ctx->wts + (size_t)layer * c.max_rows * c.n_heads * ctx->tiles * kKv4Slots : nullptr;
+  a.scores = ctx->scores;
   a.lse = ctx->lse;
+  a.n_sm = ctx->n_sm;
   a.nh = c.n_heads;
   a.D = c.head_dim;
   a.P = c.prefix_len;
@@ -2280,8 +2287,8 @@ uocr_status uocr_attend_chunk(uocr_ctx* ctx, int32_t layer, int32_t row, int32_t
   CK(dev.e, "set device");
   s = kv4_begin(ctx);
   if (s != UOCR_OK) return s;
-  // the softmax statistics of the weights' accumulation hold kTokCap tokens
-  const int step = ctx->wts ? kTokCap : n;
+  // the accumulation's scratch holds track_q() queries per cache head
+  const int step = ctx->wts ? ctx->track_q() / (q_heads / ctx->cfg.n_heads) : n;
   const int D = ctx->cfg.head_dim, esz = out_dtype == UOCR_DT_F32 ? 4 : 2;
   for (int off = 0; off < n; off += step) {
     Kv4AttnArgs a = kv4_attn_args(ctx, layer);

@@ -129,9 +129,11 @@ struct Kv4AttnArgs {
   const int* pos;              // [tokens], or nullptr: pos0 + t
   int pos0;
   float* wts;                  // layer base of the accumulated weights, or nullptr
-  float2* lse;                 // [tokens][q_heads] (maximum, 1 / sum) when wts is given
+  float* scores;               // scratch when wts is given: [tokens][q_heads][16 tiles], log2 units
+  float2* lse;                 // scratch: [tokens][q_heads] (maximum, 1 / sum)
   int q_heads, nh, D, P, R, tiles;
   int kv_row0, kv_rstep;       // kv_rstep 0: every token belongs to cache row kv_row0
+  int n_sm;
   float scale;
   int* status;
 };

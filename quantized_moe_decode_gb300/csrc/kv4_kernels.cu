@@ -1,5 +1,7 @@
 // The 4-bit KV cache: rotary positions and the append, attention over the
 // entries, and the eviction of the entries that attention uses least.
+#include <cooperative_groups.h>
+#include <limits.h>
 #include <math.h>
 
 #include "kv4_common.cuh"
@@ -299,119 +301,552 @@ cudaError_t launch_kv4_weights(const Kv4WeightsArgs& a, cudaStream_t st) {
 }
 
 // ------------------------------------------------------------------ attention
-// One CTA per (query head, token): every warp takes slots in turn, a lane
-// eight dimensions, and keeps an online softmax; the warps merge at the end.
-__global__ void __launch_bounds__(128) k_kv4_attn(const Kv4AttnArgs a) {
-  constexpr int NW = 4;
-  __shared__ float s_m[NW], s_l[NW], s_acc[NW][256];
-  pdl_launch_dependents();
-  pdl_wait();
-  const int qh = blockIdx.x, t = blockIdx.y, D = a.D, W = D / 8;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int head = qh / (a.q_heads / a.nh), row = a.kv_row0 + t * a.kv_rstep;
-  int p = a.pos ? a.pos[t] : a.pos0 + t;
-  const int2 hole = a.hole[row];
-  if (p < 0 || (hole.y > hole.x && p < hole.y)) {
-    if (threadIdx.x == 0) atomicOr(a.status, kStatusPosition);
-    p = max(p, 0);
+// softmax(q k / sqrt D) v over the live slots, split over a cluster of CTAs.
+//
+// A CTA holds the queries that read one (row, head): the heads that share it,
+// or a tile of a chunk's tokens.  A warp takes 16-slot tiles in turn and keeps
+// an online softmax per query.  Both products run on the tensor cores with the
+// cache as the A operand (m16n8k16): scores = K q with slots as rows, then
+// out = V^T p with dimensions as rows.  The cache's layout puts the A fragments
+// into a lane's own bytes, so a lane copies them with cp.async into its own
+// ring slots (no barrier guards them), turns a word of eight codes into four
+// fp16 pairs with three masks and a shift, and applies scale and minimum with
+// one fused multiply-add each, which gives the entry's value exactly.
+//
+// The eight B columns are four queries, each as an fp16 number and the fp16
+// remainder of its fp32 value (queries scaled by a power of two to [1, 2)), and
+// likewise the four weight vectors: the products then carry about 22 bits at
+// no cost, since a decode step would leave the columns empty.  Scores, sums and
+// outputs accumulate in fp32.  The running maximum of a query moves only when
+// a score exceeds it by 2^8 (weights up to 256 are held), so that almost no tile
+// rescales the accumulators.
+constexpr int kAttn4Warps = 8;
+constexpr int kAttn4Stages = 4;  // tiles of a warp's ring
+
+template <int D>
+struct Attn4 {
+  static constexpr int NG = D / 32;
+  static constexpr int CB = D / 4;                // code bytes of a lane in a K or V tile
+  static constexpr int KPB = D == 256 ? 16 : 8;   // its key parameter bytes
+  static constexpr int STAGE = 32 * (2 * CB + KPB + 16);
+  static constexpr int RING = kAttn4Stages * STAGE;
+};
+
+// One exponential; the argument is in units of log2.
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t hfma2u(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+__device__ __forceinline__ uint32_t hsub2u(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+
+// Four pairs of codes of a word (nibbles 0|4, 1|5, 2|6, 3|7) as fp16 values
+// s q + m: the code is or'ed into the mantissa of 1024 (bits 0-3) or 64 (bits
+// 4-7), which is subtracted again, exactly.
+__device__ __forceinline__ void dequant8(uint32_t w, uint32_t s, uint32_t m, uint32_t (&x)[4]) {
+  const uint32_t h = w >> 8;
+  x[0] = hfma2u(s, hsub2u(lop_and_or(w, 0x000F000Fu, 0x64006400u), 0x64006400u), m);
+  x[1] = hfma2u(s, hsub2u(lop_and_or(w, 0x00F000F0u, 0x54005400u), 0x54005400u), m);
+  x[2] = hfma2u(s, hsub2u(lop_and_or(h, 0x000F000Fu, 0x64006400u), 0x64006400u), m);
+  x[3] = hfma2u(s, hsub2u(lop_and_or(h, 0x00F000F0u, 0x54005400u), 0x54005400u), m);
+}
+
+// The slots a CTA reads, as whole tiles: those of [0, x) and of [y, lim).
+struct TileList {
+  int ta, tb, count;
+  __device__ TileList(int lim, int2 hole) {
+    const int x = min(hole.x, lim);
+    const bool gap = hole.y > hole.x && lim > hole.x;
+    ta = ((gap ? x : lim) + 15) >> 4;
+    tb = gap ? max(ta, hole.y >> 4) : ta;
+    count = ta + (gap && lim > hole.y ? max(((lim + 15) >> 4) - tb, 0) : 0);
   }
-  const int lim = kv_limit(p, a.P, a.R);
-  const uint8_t* kt = a.kv4 + (size_t)(row * 2 * a.nh + head) * a.tiles * kv4_tile_bytes(D);
-  const uint8_t* vt = kt + (size_t)a.nh * a.tiles * kv4_tile_bytes(D);
-  float q[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) q[j] = lane < W ? a.q[((size_t)t * a.q_heads + qh) * D + 8 * lane + j] * a.scale : 0.f;
-  float m = -INFINITY, l = 0.f, acc[8] = {};
-  for (int slot = warp; slot < lim; slot += NW) {
-    if (slot >= hole.x && slot < hole.y) continue;
-    const int s = slot & 15;
-    const size_t off = (size_t)(slot >> 4) * kv4_tile_bytes(D);
-    float d = 0.f;
-    if (lane < W) {
-      __half x[8];
-      key_values(kt + off, D, s, lane, x);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) d = fmaf(q[j], __half2float(x[j]), d);
+  __device__ int operator()(int j) const { return j < ta ? j : tb + (j - ta); }
+};
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kAttn4Warps * 32, D * NT <= 128 ? 2 : 1) k_kv4_attn(const Kv4AttnArgs a, int n_queries) {
+  using C = Attn4<D>;
+  constexpr int NW = kAttn4Warps, ST = kAttn4Stages, NQ = 4 * NT;
+  constexpr bool QREG = D * NT <= 256;  // query fragments in registers, else in shared memory
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ float s_m[NW][NQ], s_l[NW][NQ];
+  __shared__ float s_part[NQ][D + 2];
+  __shared__ float s_c[NQ];     // score factor of each query: scale log2(e) 2^e
+  __shared__ float2 s_fin[NQ];  // final maximum and 1 / sum
+  __shared__ int s_lim[NQ];
+  __shared__ uint2 s_q[QREG ? 1 : NT * (D / 16) * 32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int split = blockIdx.x, head = blockIdx.y, G = a.q_heads / a.nh;
+  // queries of this CTA: u = token * G + head in the group
+  const int u0 = a.kv_rstep ? blockIdx.z * G : blockIdx.z * NQ;
+  const int nq = a.kv_rstep ? G : min(NQ, n_queries - u0);
+  const int row = a.kv_row0 + (a.kv_rstep ? blockIdx.z : 0);
+  auto token = [&](int i) { return (u0 + i) / G; };
+  auto q_index = [&](int i) { return (size_t)token(i) * a.q_heads + head * G + (u0 + i) % G; };
+
+  pdl_launch_dependents();
+  pdl_wait();  // queries and new entries come from the previous kernels
+  const int2 hole = a.hole[row];
+  if (threadIdx.x < NQ) {
+    int lim = 0;
+    if (threadIdx.x < nq) {
+      const int tok = token(threadIdx.x);
+      int p = a.pos ? a.pos[tok] : a.pos0 + tok;
+      if (p < 0 || (hole.y > hole.x && p < hole.y)) {
+        atomicOr(a.status, kStatusPosition);
+        p = max(p, 0);
+      }
+      lim = kv_limit(p, a.P, a.R);
+    }
+    s_lim[threadIdx.x] = lim;
+  }
+  // queries to fp16 pairs (value, remainder): a warp per query
+  float* sq = reinterpret_cast<float*>(smem);  // [NQ][D], before the ring is used
+  for (int i = warp; i < NQ; i += NW) {
+    float mx = 0.f;
+    for (int d = lane; d < D; d += 32) {
+      const float x = i < nq ? a.q[q_index(i) * D + d] : 0.f;
+      sq[i * D + d] = x;
+      mx = fmaxf(mx, fabsf(x));
     }
 #pragma unroll
-    for (int o = 16; o; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-    const float mn = fmaxf(m, d);
-    const float corr = m == -INFINITY ? 0.f : __expf(m - mn);
-    const float w = mn == -INFINITY ? 0.f : __expf(d - mn);
-    l = l * corr + w;
-    m = mn;
-    if (lane < W) {
+    for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    // 2^-e with e the exponent of the largest magnitude (0 and infinities stay)
+    const int e = mx > 0.f && mx < INFINITY ? min(max(ilogbf(mx), -100), 100) : 0;
+    const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+    for (int d = lane; d < D; d += 32) sq[i * D + d] *= down;
+    if (lane == 0) s_c[i] = a.scale * 1.4426950408889634f * __uint_as_float((uint32_t)(127 + e) << 23);
+  }
+  __syncthreads();
+  uint2 qf[QREG ? NT * (D / 16) : 1];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        __half x[4];
-        value_values(vt + off, D, s, 2 * lane + h, x);
+  for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[4 * h + j] = fmaf(w, __half2float(x[j]), acc[4 * h + j] * corr);
+    for (int k = 0; k < D / 16; ++k) {
+      // step k covers dimensions 8 (k/2) + 4 (k%2) .. + 3 of every lane's quarter
+      const float* s = sq + (4 * nt + (g >> 1)) * D + t * (D / 4) + 4 * k;
+      float v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float hi = __half2float(__float2half_rn(s[j]));
+        v[j] = (g & 1) ? s[j] - hi : s[j];
+      }
+      const uint2 f = make_uint2(pack2(v[0], v[1]), pack2(v[2], v[3]));
+      if constexpr (QREG)
+        qf[nt * (D / 16) + k] = f;
+      else if (warp == 0)
+        s_q[(nt * (D / 16) + k) * 32 + lane] = f;
+    }
+  int lim_lo = INT_MAX, lim_hi = 0;
+  for (int i = 0; i < nq; ++i) {
+    lim_lo = min(lim_lo, s_lim[i]);
+    lim_hi = max(lim_hi, s_lim[i]);
+  }
+  int lim_q[NT];
+  float cq[NT];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    lim_q[nt] = s_lim[4 * nt + t];
+    cq[nt] = s_c[4 * nt + t];
+  }
+  __syncthreads();  // the ring overwrites sq
+
+  const TileList tiles(lim_hi, hole);
+  const int per = (tiles.count + gridDim.x - 1) / gridDim.x;
+  const int j0 = split * per, j1 = min(tiles.count, j0 + per);
+  const uint8_t* kt = a.kv4 + ((size_t)row * 2 * a.nh + head) * a.tiles * kv4_tile_bytes(D);
+  const uint8_t* vt = kt + (size_t)a.nh * a.tiles * kv4_tile_bytes(D);
+  unsigned char* ring = smem + warp * C::RING;
+  const int kp_off = 8 * D + (D == 256 ? g * 64 + t * 16 : (g * C::NG + t * C::NG / 4) * 8);
+  const int vp_off = 8 * D + ((g * D / 256) * 4 + t) * 16;
+  auto issue = [&](int j, int stage) {
+    if (j < j1) {
+      const size_t off = (size_t)tiles(j) * kv4_tile_bytes(D);
+      unsigned char* d = ring + stage * C::STAGE;
+      if constexpr (D == 32) {
+        cp_async8(d + lane * 8, kt + off + lane * 8);
+        cp_async8(d + 32 * C::CB + lane * 8, vt + off + lane * 8);
+      } else {
+#pragma unroll
+        for (int p = 0; p < C::CB / 16; ++p) {
+          cp_async16(d + p * 512 + lane * 16, kt + off + p * 512 + lane * 16);
+          cp_async16(d + 32 * C::CB + p * 512 + lane * 16, vt + off + p * 512 + lane * 16);
+        }
+      }
+      if constexpr (C::KPB == 16)
+        cp_async16(d + 64 * C::CB + lane * 16, kt + off + kp_off);
+      else
+        cp_async8(d + 64 * C::CB + lane * 8, kt + off + kp_off);
+      cp_async16(d + 64 * C::CB + 32 * C::KPB + lane * 16, vt + off + vp_off);
+    }
+    cp_commit();
+  };
+
+  float m_ref[NT], l[NT], acc[NT][D / 16][4];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    m_ref[nt] = -INFINITY;
+    l[nt] = 0.f;
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[nt][i][j] = 0.f;
+  }
+#pragma unroll
+  for (int s = 0; s < ST - 1; ++s) issue(j0 + warp + s * NW, s);
+
+  int stage = 0;
+  for (int j = j0 + warp; j < j1; j += NW) {
+    cp_wait<ST - 2>();
+    const unsigned char* d = ring + stage * C::STAGE;
+    issue(j + (ST - 1) * NW, stage == 0 ? ST - 1 : stage - 1);  // the slot that the last tile left
+    stage = stage == ST - 1 ? 0 : stage + 1;
+    const int slot0 = tiles(j) * 16;
+    const bool gap = hole.y > hole.x;
+    const bool full = slot0 + 16 <= lim_lo && (!gap || slot0 + 16 <= hole.x || slot0 >= hole.y);
+
+    // ---- scores
+    float sc[NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sc[nt][i] = 0.f;
+    {
+      constexpr int W = D / 32;  // words per slot
+      uint32_t w[2 * W];
+      if constexpr (D == 32) {
+        const uint2 u = *reinterpret_cast<const uint2*>(d + lane * 8);
+        w[0] = u.x;
+        w[1] = u.y;
+      } else {
+#pragma unroll
+        for (int p = 0; p < W / 2; ++p) {
+          const uint4 u = lds128(d + p * 512 + lane * 16);
+          w[4 * p] = u.x;
+          w[4 * p + 1] = u.y;
+          w[4 * p + 2] = u.z;
+          w[4 * p + 3] = u.w;
+        }
+      }
+      // (s, m) of slots g and g + 8, one or two groups
+      uint32_t par[4];
+      if constexpr (C::KPB == 16) {
+        const uint4 u = lds128(d + 64 * C::CB + lane * 16);
+        par[0] = u.x, par[1] = u.y, par[2] = u.z, par[3] = u.w;
+      } else {
+        const uint2 u = *reinterpret_cast<const uint2*>(d + 64 * C::CB + lane * 8);
+        par[0] = u.x, par[1] = u.y, par[2] = u.x, par[3] = u.y;
+      }
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+        const uint32_t p0 = par[i >= 4 ? 2 : 0], p1 = par[i >= 4 ? 3 : 1];
+        uint32_t e[4], f[4];
+        dequant8(w[i], __byte_perm(p0, 0, 0x1010), __byte_perm(p0, 0, 0x3232), e);
+        dequant8(w[W + i], __byte_perm(p1, 0, 0x1010), __byte_perm(p1, 0, 0x3232), f);
+        const uint32_t a0[4] = {e[0], f[0], e[1], f[1]}, a1[4] = {e[2], f[2], e[3], f[3]};
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          uint2 b0, b1;
+          if constexpr (QREG) {
+            b0 = qf[nt * (D / 16) + 2 * i];
+            b1 = qf[nt * (D / 16) + 2 * i + 1];
+          } else {
+            b0 = s_q[(nt * (D / 16) + 2 * i) * 32 + lane];
+            b1 = s_q[(nt * (D / 16) + 2 * i + 1) * 32 + lane];
+          }
+          mma_16816(sc[nt], a0, b0.x, b0.y);
+          mma_16816(sc[nt], a1, b1.x, b1.y);
+        }
+      }
+    }
+    // ---- softmax: lane (g, t) holds slots g and g + 8 of query t
+    float p0[NT], p1[NT];
+    bool raise = false;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      p0[nt] = (sc[nt][0] + sc[nt][1]) * cq[nt];
+      p1[nt] = (sc[nt][2] + sc[nt][3]) * cq[nt];
+      if (!full) {
+        const int s0 = slot0 + g, s1 = s0 + 8;
+        if (s0 >= lim_q[nt] || (s0 >= hole.x && s0 < hole.y)) p0[nt] = -INFINITY;
+        if (s1 >= lim_q[nt] || (s1 >= hole.x && s1 < hole.y)) p1[nt] = -INFINITY;
+      }
+      if (a.scores && 4 * nt + t < nq) {
+        float* so = a.scores + q_index(4 * nt + t) * (size_t)a.tiles * kKv4Slots + slot0 + g;
+        so[0] = p0[nt];
+        so[8] = p1[nt];
+      }
+      raise = raise || fmaxf(p0[nt], p1[nt]) > m_ref[nt] + 8.f;
+    }
+    if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float mx = fmaxf(p0[nt], p1[nt]);
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        const float m_new = fmaxf(m_ref[nt], mx);
+        const float corr = m_ref[nt] == m_new ? 1.f : ex2(m_ref[nt] - m_new);
+        m_ref[nt] = m_new;
+        l[nt] *= corr;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) acc[nt][i][k] *= corr;
+      }
+    }
+    uint32_t pb[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const float m = m_ref[nt] == -INFINITY ? 0.f : m_ref[nt];
+      p0[nt] = ex2(p0[nt] - m);
+      p1[nt] = ex2(p1[nt] - m);
+      l[nt] += p0[nt] + p1[nt];
+      // column g of the B fragment: query g / 2, its weight or the remainder
+      const int src = 8 * t + (g >> 1);
+      const float v0 = __shfl_sync(0xffffffffu, p0[nt], src), v1 = __shfl_sync(0xffffffffu, p0[nt], src + 4);
+      const float v2 = __shfl_sync(0xffffffffu, p1[nt], src), v3 = __shfl_sync(0xffffffffu, p1[nt], src + 4);
+      const uint32_t h0 = pack2(v0, v1), h1 = pack2(v2, v3);
+      if (g & 1) {
+        const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&h0));
+        const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&h1));
+        pb[nt][0] = pack2(v0 - f0.x, v1 - f0.y);
+        pb[nt][1] = pack2(v2 - f1.x, v3 - f1.y);
+      } else {
+        pb[nt][0] = h0;
+        pb[nt][1] = h1;
+      }
+    }
+    // ---- values: slots 2t, 2t+1 (par.x, par.y) and 2t+8, 2t+9 (par.z, par.w)
+    uint4 par = lds128(d + 64 * C::CB + 32 * C::KPB + lane * 16);
+    auto accumulate = [&](const uint4& vp) {
+      constexpr int Q = D / 32;  // words per slot pair
+      uint32_t w[2 * Q];
+      if constexpr (D == 32) {
+        const uint2 u = *reinterpret_cast<const uint2*>(d + 32 * C::CB + lane * 8);
+        w[0] = u.x;
+        w[1] = u.y;
+      } else {
+#pragma unroll
+        for (int p = 0; p < Q / 2; ++p) {
+          const uint4 u = lds128(d + 32 * C::CB + p * 512 + lane * 16);
+          w[4 * p] = u.x;
+          w[4 * p + 1] = u.y;
+          w[4 * p + 2] = u.z;
+          w[4 * p + 3] = u.w;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < Q; ++i) {
+        uint32_t e[4], f[4];
+        dequant8(w[i], vp.x, vp.y, e);
+        dequant8(w[Q + i], vp.z, vp.w, f);
+        const uint32_t a0[4] = {e[0], e[1], f[0], f[1]}, a1[4] = {e[2], e[3], f[2], f[3]};
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          mma_16816(acc[nt][2 * i], a0, pb[nt][0], pb[nt][1]);
+          mma_16816(acc[nt][2 * i + 1], a1, pb[nt][0], pb[nt][1]);
+        }
+      }
+    };
+    // slots that no query reads become zeros: their weight is zero, but an unread
+    // NaN or infinity times zero would not be
+    if (!full) {
+      const int s = slot0 + 2 * t;
+      auto live = [&](int x) { return x < lim_hi && !(x >= hole.x && x < hole.y); };
+      const uint32_t k0 = (live(s) ? 0xFFFFu : 0u) | (live(s + 1) ? 0xFFFF0000u : 0u);
+      const uint32_t k1 = (live(s + 8) ? 0xFFFFu : 0u) | (live(s + 9) ? 0xFFFF0000u : 0u);
+      par.x &= k0, par.y &= k0, par.z &= k1, par.w &= k1;
+    }
+    if (!full && lim_lo != lim_hi) {
+      // a slot that only some of the tile's queries read: where its group is not
+      // finite it is left out of the products, and the queries that do read it
+      // get NaN there (a lane's values of a slot all belong to one group)
+      auto odd = [](uint32_t s, uint32_t m) {
+        return (((s & 0x7C00u) == 0x7C00u || (m & 0x7C00u) == 0x7C00u) ? 1u : 0u) |
+               (((s & 0x7C000000u) == 0x7C000000u || (m & 0x7C000000u) == 0x7C000000u) ? 2u : 0u);
+      };
+      const uint32_t b0 = odd(par.x, par.y), b1 = odd(par.z, par.w);
+      uint32_t bad = (b0 << (2 * t)) | (b1 << (2 * t + 8));
+      if (__any_sync(0xffffffffu, bad != 0u)) {
+        const uint32_t k0 = (b0 & 1 ? 0u : 0xFFFFu) | (b0 & 2 ? 0u : 0xFFFF0000u);
+        const uint32_t k1 = (b1 & 1 ? 0u : 0xFFFFu) | (b1 & 2 ? 0u : 0xFFFF0000u);
+        par.x &= k0, par.y &= k0, par.z &= k1, par.w &= k1;
+        bad |= __shfl_xor_sync(0xffffffffu, bad, 1);
+        bad |= __shfl_xor_sync(0xffffffffu, bad, 2);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const int n = min(max(lim_q[nt] - slot0, 0), 16);  // the query reads the tile's first n slots
+          if (bad & ((1u << n) - 1u))
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) acc[nt][i][0] = acc[nt][i][2] = __int_as_float(0x7FFFFFFF);
+        }
+      }
+    }
+    accumulate(par);
+  }
+  cp_wait<0>();
+  __syncthreads();  // the rings are free: they take the warps' partials
+
+  float* s_acc = reinterpret_cast<float*>(smem);  // [NW][NQ][D]
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int i = 4 * nt + t;
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) l[nt] += __shfl_xor_sync(0xffffffffu, l[nt], o);
+    if (g == 0) {
+      s_m[warp][i] = m_ref[nt];
+      s_l[warp][i] = l[nt];
+    }
+    if (i < nq) {
+      float* o = s_acc + ((size_t)warp * NQ + i) * D + g * (D / 8);
+#pragma unroll
+      for (int x = 0; x < D / 16; ++x) {
+        o[2 * x] = acc[nt][x][0] + acc[nt][x][1];
+        o[2 * x + 1] = acc[nt][x][2] + acc[nt][x][3];
       }
     }
   }
-  if (lane == 0) {
-    s_m[warp] = m;
-    s_l[warp] = l;
-  }
-  if (lane < W)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) s_acc[warp][8 * lane + j] = acc[j];
   __syncthreads();
-  float M = a.sink ? a.sink[head] : -INFINITY;
-  for (int w = 0; w < NW; ++w) M = fmaxf(M, s_m[w]);
-  float L = a.sink ? __expf(a.sink[head] - M) : 0.f;
-  for (int w = 0; w < NW; ++w)
-    if (s_l[w] != 0.f) L += s_l[w] * __expf(s_m[w] - M);
-  const float inv = L != 0.f ? 1.f / L : 0.f;  // nothing to read: the output is zero
-  for (int d = threadIdx.x; d < D; d += blockDim.x) {
-    float v = 0.f;
-    for (int w = 0; w < NW; ++w)
-      if (s_l[w] != 0.f) v += s_acc[w][d] * __expf(s_m[w] - M);
-    store_elem(a.out, a.out_dtype, ((long long)t * a.q_heads + qh) * D + d, v * inv);
+  // the CTA's partial of each query: maximum, sum, weighted values
+  for (int i = warp; i < nq; i += NW) {
+    float M = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) M = fmaxf(M, s_m[w][i]);
+    float f[NW], L = 0.f;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {  // a warp without a finite maximum has summed nothing, or NaN
+      f[w] = s_m[w][i] == -INFINITY ? (s_l[w][i] == 0.f ? 0.f : 1.f) : ex2(s_m[w][i] - M);
+      L += s_l[w][i] * f[w];
+    }
+    for (int d = lane; d < D; d += 32) {
+      float v = 0.f;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) v += s_acc[((size_t)w * NQ + i) * D + d] * f[w];
+      s_part[i][2 + d] = v;
+    }
+    if (lane == 0) {
+      s_part[i][0] = M;
+      s_part[i][1] = L;
+    }
   }
-  if (a.lse && threadIdx.x == 0) a.lse[(size_t)t * a.q_heads + qh] = make_float2(M, inv);
+  // the splits' partials meet through the cluster's shared memory; every CTA
+  // writes a slice of the output
+  namespace cg = cooperative_groups;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int ns = gridDim.x;
+  if (ns > 1) {
+    cluster.sync();
+  } else {
+    __syncthreads();
+  }
+  auto part = [&](int sp, int i) { return ns > 1 ? cluster.map_shared_rank(&s_part[i][0], sp) : &s_part[i][0]; };
+  const float sink = a.sink ? a.sink[head] * 1.4426950408889634f : -INFINITY;
+  for (int i = warp; i < nq; i += NW) {
+    float M = sink;
+    for (int sp = 0; sp < ns; ++sp) M = fmaxf(M, part(sp, i)[0]);
+    float L = a.sink ? ex2(sink - M) : 0.f;
+    auto factor = [&](const float* pp) {
+      return pp[0] == -INFINITY ? (pp[1] == 0.f ? 0.f : 1.f) : ex2(pp[0] - M);
+    };
+    for (int sp = 0; sp < ns; ++sp) L += part(sp, i)[1] * factor(part(sp, i));
+    const float inv = L == 0.f ? 0.f : 1.f / L;  // nothing to read: zeros
+    const int d1 = (split + 1) * D / ns;
+    for (int d = split * D / ns + lane; d < d1; d += 32) {
+      float v = 0.f;
+      for (int sp = 0; sp < ns; ++sp) v += part(sp, i)[2 + d] * factor(part(sp, i));
+      store_elem(a.out, a.out_dtype, (long long)q_index(i) * D + d, v * inv);
+    }
+    if (lane == 0) {
+      s_fin[i] = make_float2(M, inv);
+      if (a.lse && split == 0) a.lse[q_index(i)] = s_fin[i];
+    }
+  }
+  if (ns > 1) cluster.sync();  // a CTA keeps its partial until all slices are merged
+  if (a.wts && a.kv_rstep) {
+    // this CTA alone has these slots of the row: add its queries' weights in order
+    __syncthreads();
+    float* wt = a.wts + ((size_t)row * a.nh + head) * a.tiles * kKv4Slots;
+    for (int x = threadIdx.x; x < (j1 - j0) * 16; x += NW * 32) {
+      const int slot = tiles(j0 + (x >> 4)) * 16 + (x & 15);
+      float add = 0.f;
+      for (int i = 0; i < nq; ++i)
+        add += ex2(a.scores[q_index(i) * (size_t)a.tiles * kKv4Slots + slot] - s_fin[i].x) * s_fin[i].y;
+      if (add != 0.f) wt[slot] += add;
+    }
+  }
 }
 
-// Accumulate the softmax weights that the attention gave: one warp per (slot,
-// head, row) adds the weights of every query of the row in order.
+// The weights of a chunk's queries, which several CTAs hold: one thread per
+// slot adds them in the tokens' order.
 __global__ void k_kv4_track(const Kv4AttnArgs a, int tokens) {
   pdl_launch_dependents();
   pdl_wait();
-  const int slot = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  const int head = blockIdx.y, D = a.D, W = D / 8, G = a.q_heads / a.nh;
-  const int row = a.kv_row0 + blockIdx.z * a.kv_rstep;
-  const int t0 = a.kv_rstep ? blockIdx.z : 0, t1 = a.kv_rstep ? t0 + 1 : tokens;
+  const int slot = blockIdx.x * blockDim.x + threadIdx.x, head = blockIdx.y, G = a.q_heads / a.nh;
+  const int row = a.kv_row0;
   const int2 hole = a.hole[row];
   if (slot >= a.P + a.R || (slot >= hole.x && slot < hole.y)) return;
-  const uint8_t* kt = a.kv4 + ((size_t)(row * 2 * a.nh + head) * a.tiles + (slot >> 4)) * kv4_tile_bytes(D);
-  __half x[8];
-  if (lane < W) key_values(kt, D, slot & 15, lane, x);
   float add = 0.f;
-  for (int t = t0; t < t1; ++t) {
+  for (int t = 0; t < tokens; ++t) {
     const int p = max(a.pos ? a.pos[t] : a.pos0 + t, 0);
     if (slot >= kv_limit(p, a.P, a.R)) continue;
     for (int g = 0; g < G; ++g) {
       const size_t qi = (size_t)t * a.q_heads + head * G + g;
-      float d = 0.f;
-      if (lane < W)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) d = fmaf(a.q[qi * D + 8 * lane + j] * a.scale, __half2float(x[j]), d);
-#pragma unroll
-      for (int o = 16; o; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
       const float2 n = a.lse[qi];
-      add += __expf(d - n.x) * n.y;
+      add += ex2(a.scores[qi * a.tiles * kKv4Slots + slot] - n.x) * n.y;
     }
   }
-  if (lane == 0 && add != 0.f) a.wts[((size_t)row * a.nh + head) * a.tiles * kKv4Slots + slot] += add;
+  if (add != 0.f) a.wts[((size_t)row * a.nh + head) * a.tiles * kKv4Slots + slot] += add;
+}
+
+template <int D, int NT>
+static cudaError_t launch_attn4(const Kv4AttnArgs& a, int tokens, int nsplit, cudaStream_t st, bool pdl) {
+  constexpr int part = kAttn4Warps * 4 * NT * D * 4, ring = kAttn4Warps * Attn4<D>::RING;
+  const int queries = tokens * (a.q_heads / a.nh);
+  const int z = a.kv_rstep ? tokens : (queries + 4 * NT - 1) / (4 * NT);
+  return launch_kernel_cluster(k_kv4_attn<D, NT>, dim3(nsplit, a.nh, z), dim3(kAttn4Warps * 32),
+                               (size_t)(part > ring ? part : ring), st, pdl, nsplit, a, queries);
+}
+
+template <int NT>
+static cudaError_t launch_attn4(const Kv4AttnArgs& a, int tokens, int nsplit, cudaStream_t st, bool pdl) {
+  switch (a.D) {
+    case 32: return launch_attn4<32, NT>(a, tokens, nsplit, st, pdl);
+    case 64: return launch_attn4<64, NT>(a, tokens, nsplit, st, pdl);
+    case 128: return launch_attn4<128, NT>(a, tokens, nsplit, st, pdl);
+    case 256: return launch_attn4<256, NT>(a, tokens, nsplit, st, pdl);
+  }
+  return cudaErrorInvalidValue;
 }
 
 cudaError_t launch_kv4_attn(const Kv4AttnArgs& a, int tokens, cudaStream_t st, bool pdl) {
   if (tokens <= 0) return cudaSuccess;
-  cudaError_t e = launch_kernel(k_kv4_attn, dim3(a.q_heads, tokens), dim3(128), 0, st, pdl, a);
-  if (e == cudaSuccess && a.wts)
-    e = launch_kernel(k_kv4_track, dim3((a.P + a.R + 7) / 8, a.nh, a.kv_rstep ? tokens : 1), dim3(256), 0, st, pdl, a,
-                      tokens);
+  const int G = a.q_heads / a.nh;
+  // a second group of four queries costs registers: only where they exist
+  const int nt = (a.kv_rstep ? G : tokens * G) > 4 ? 2 : 1;
+  // splits: enough CTAs for two on every SM, each with a tile for every warp
+  const int ctas = a.nh * (a.kv_rstep ? tokens : (tokens * G + 4 * nt - 1) / (4 * nt));
+  int ns = (2 * a.n_sm + ctas - 1) / ctas;
+  const int cap = (a.tiles + kAttn4Warps - 1) / kAttn4Warps;
+  ns = ns > cap ? cap : ns;
+  ns = ns > 8 ? 8 : ns < 1 ? 1 : ns;
+  cudaError_t e = nt == 1 ? launch_attn4<1>(a, tokens, ns, st, pdl) : launch_attn4<2>(a, tokens, ns, st, pdl);
+  if (e == cudaSuccess && a.wts && !a.kv_rstep)
+    e = launch_kernel(k_kv4_track, dim3((a.P + a.R + 127) / 128, a.nh), dim3(128), 0, st, pdl, a, tokens);
   return e;
 }
 
@@ -581,6 +1016,14 @@ cudaError_t launch_kv4_evict(const Kv4EvictArgs& a, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-cudaError_t init_kv4_attributes() { return cudaSuccess; }
+cudaError_t init_kv4_attributes() {
+  cudaError_t e = cudaSuccess;
+#define UOCR_A(D_)                                              \
+  if (e == cudaSuccess) e = allow_max_dyn_smem(k_kv4_attn<D_, 1>); \
+  if (e == cudaSuccess) e = allow_max_dyn_smem(k_kv4_attn<D_, 2>);
+  UOCR_A(32) UOCR_A(64) UOCR_A(128) UOCR_A(256)
+#undef UOCR_A
+  return e;
+}
 
 }  // namespace uocr
