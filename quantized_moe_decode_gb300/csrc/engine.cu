@@ -134,6 +134,7 @@ struct uocr_ctx {
   __half* proj_b = nullptr;  // its bias [H]
   double* inv_freq = nullptr;
   double rope_amp = 1.0;   // amplitude of cos and sin
+  double2* turns = nullptr;  // 4-bit cache: (cos, sin) of 0..255 and of 256 (0..255) turns of each pair
   float2* rope = nullptr;  // [max_rows][head_dim/2] (cos, sin) of the step's positions
   __half* kv = nullptr;        // fp16 cache [L][MR][2][nh][SL][D]
   int8_t* kv8 = nullptr;       // INT8 cache codes, same shape
@@ -409,6 +410,7 @@ static void carve(uocr_ctx* ctx, Carver& cv) {
     ctx->kv4_layer = (size_t)MR * 2 * c.n_heads * ctx->tiles * kv4_tile_bytes(c.head_dim);
     ctx->kv4 = cv.take<uint8_t>(ctx->kv4_layer * Lc, r.kv_cache);
     ctx->hole = cv.take<int2>((size_t)Lc * MR, r.kv_cache);
+    ctx->turns = cv.take<double2>((size_t)512 * (c.head_dim / 2), r.weights);
     if (c.kv_track) {
       ctx->wts = cv.take<float>((size_t)Lc * MR * c.n_heads * ctx->tiles * kKv4Slots, r.kv_cache);
       ctx->scores = cv.take<float>((size_t)ctx->track_q() * c.n_heads * ctx->tiles * kKv4Slots, r.activations);
@@ -497,6 +499,8 @@ static Kv4AppendArgs kv4_append_args(uocr_ctx* ctx, int layer) {
   const uocr_config& c = ctx->cfg;
   Kv4AppendArgs a{};
   a.inv_freq = ctx->inv_freq;
+  a.turns = ctx->turns;
+  a.n_sm = ctx->n_sm;
   a.amp = ctx->rope_amp;
   a.rope_layout = c.rope_layout;
   a.rope_dims = c.rope_dims;
@@ -1348,6 +1352,7 @@ uocr_status uocr_create(const uocr_config* cfg, uocr_ctx** out) {
   if (e == cudaSuccess) {
     const std::vector<double> inv = rope_frequencies(ctx->cfg, &ctx->rope_amp);
     e = cudaMemcpyAsync(ctx->inv_freq, inv.data(), inv.size() * sizeof(double), cudaMemcpyHostToDevice, ctx->st);
+    if (e == cudaSuccess && ctx->turns) e = launch_kv4_turns(ctx->inv_freq, ctx->turns, cfg->head_dim / 2, ctx->st);
   }
   if (e == cudaSuccess) e = cudaStreamSynchronize(ctx->st);
   if (e != cudaSuccess) {

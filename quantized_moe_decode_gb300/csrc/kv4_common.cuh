@@ -100,6 +100,7 @@ struct Kv4AppendArgs {
   int dtype;                   // uocr_dtype of q, k, v
   int rotate;                  // 1: rotate q and k by their position
   const double* inv_freq;      // [D/2]
+  const double2* turns;        // [2][256][D/2] (cos, sin) of b inv_j and of 256 b inv_j
   double amp;
   int rope_layout, rope_dims;
   int q_heads, nh, D;
@@ -113,8 +114,10 @@ struct Kv4AppendArgs {
   int slots;                   // 1: pos0 counts slots, not positions
   int P, R, tiles;
   int kv_row0, kv_rstep;
+  int n_sm;
   int* status;
 };
+cudaError_t launch_kv4_turns(const double* inv_freq, double2* turns, int pairs, cudaStream_t st);
 cudaError_t launch_kv4_append(const Kv4AppendArgs& a, int tokens, cudaStream_t st, bool pdl);
 // Zero the entries and weights of slots [slot0, slot0 + n) of a row.
 cudaError_t launch_kv4_zero(const Kv4AppendArgs& a, int row, int slot0, int n, cudaStream_t st);

@@ -41,33 +41,106 @@ __device__ __forceinline__ void sincos_taylor(double a, double& sn, double& cs) 
   cs = (k == 1 || k == 2) ? -w : w;
 }
 
-// Element d of a rotated vector: (x, y) -> (x c - y s, y c + x s), the products
-// and the sum each rounded to fp32.
-__device__ __forceinline__ float rotated(const void* p, int dtype, long long base, int d, const Kv4AppendArgs& a,
-                                         const float2* cs) {
-  const float x = load_elem(p, dtype, base + d);
-  if (!a.rotate || d >= a.rope_dims) return x;
-  const int half = a.rope_dims >> 1;
-  int j, other;
-  bool lo;
-  if (a.rope_layout == 0) {
-    lo = d < half;
-    j = lo ? d : d - half;
-    other = lo ? d + half : d - half;
-  } else {
-    lo = !(d & 1);
-    j = d >> 1;
-    other = d ^ 1;
-  }
-  const float y = load_elem(p, dtype, base + other);
-  const float2 r = cs[j];
-  return lo ? __fsub_rn(__fmul_rn(x, r.x), __fmul_rn(y, r.y)) : __fadd_rn(__fmul_rn(x, r.x), __fmul_rn(y, r.y));
+// cos and sin of b inv_j (first table) and 256 b inv_j (second), b < 256: what a
+// chunk's positions are composed from.  The product's rounding error e enters
+// as cos(x + e) = cos x - e sin x.
+__global__ void k_kv4_turns(const double* inv_freq, double2* turns, int pairs) {
+  const double f = inv_freq[threadIdx.x], b = (double)(blockIdx.x & 255) * (blockIdx.x >> 8 ? 256.0 : 1.0);
+  const double x = b * f, e = fma(b, f, -x);
+  double sn, cs;
+  sincos_taylor(x, sn, cs);
+  turns[(size_t)blockIdx.x * pairs + threadIdx.x] = make_double2(fma(-e, sn, cs), fma(e, cs, sn));
 }
 
-// One CTA per token.  A thread takes eight dimensions of a key or value
-// vector, four neighbouring lanes a group of 32.
-__global__ void __launch_bounds__(256) k_kv4_append(const Kv4AppendArgs a) {
-  __shared__ float2 s_cs[128];
+cudaError_t launch_kv4_turns(const double* inv_freq, double2* turns, int pairs, cudaStream_t st) {
+  k_kv4_turns<<<512, pairs, 0, st>>>(inv_freq, turns, pairs);
+  return cudaGetLastError();
+}
+
+// Eight neighbouring elements in fp32.
+template <int DT, bool VEC>
+__device__ __forceinline__ void load8(const void* p, long long at, float (&x)[8]) {
+  if constexpr (!VEC) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = load_elem(p, DT, at + j);
+  } else if constexpr (DT == 0) {
+    const float4* q = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(p) + at);
+    const float4 u = __ldg(q), v = __ldg(q + 1);
+    x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w, x[4] = v.x, x[5] = v.y, x[6] = v.z, x[7] = v.w;
+  } else {
+    const uint4 u = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const unsigned short*>(p) + at));
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (DT == 1) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+        x[2 * j] = f.x;
+        x[2 * j + 1] = f.y;
+      } else {
+        x[2 * j] = __uint_as_float(w[j] << 16);
+        x[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+      }
+    }
+  }
+}
+
+// Place of pair j's (cos, sin) in shared memory: lanes that take pairs 8 apart
+// read neighbouring entries.
+__device__ __forceinline__ int turn_at(int j) { return (j & 7) * 17 + (j >> 3); }
+
+// Dimensions d .. d+7 of a vector at `base`, rotated: (x, y) -> (x c - y s,
+// y c + x s), the products and the sum each rounded to fp32.
+template <int DT, bool VEC>
+__device__ __forceinline__ void load8_rotated(const void* p, long long base, int d, const Kv4AppendArgs& a,
+                                              const float2* cs, float (&x)[8]) {
+  load8<DT, VEC>(p, base + d, x);
+  const int rd = a.rope_dims, half = rd >> 1;
+  if (d >= rd) return;
+  if (a.rope_layout == 1) {
+#pragma unroll
+    for (int j = 0; j < 8; j += 2)
+      if (d + j < rd) {
+        const float2 r = cs[turn_at((d + j) >> 1)];
+        const float u = x[j], v = x[j + 1];
+        x[j] = __fsub_rn(__fmul_rn(u, r.x), __fmul_rn(v, r.y));
+        x[j + 1] = __fadd_rn(__fmul_rn(v, r.x), __fmul_rn(u, r.y));
+      }
+    return;
+  }
+  if ((half & 7) == 0) {  // the partners are eight neighbours too
+    const bool lo = d < half;
+    const int o = lo ? d + half : d - half, c = lo ? d : d - half;
+    float y[8];
+    load8<DT, VEC>(p, base + o, y);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float2 r = cs[turn_at(c + j)];
+      const float u = __fmul_rn(x[j], r.x), v = __fmul_rn(y[j], r.y);
+      x[j] = lo ? __fsub_rn(u, v) : __fadd_rn(u, v);
+    }
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int i = d + j;
+    if (i >= rd) break;
+    const bool lo = i < half;
+    const float2 r = cs[turn_at(lo ? i : i - half)];
+    const float u = __fmul_rn(x[j], r.x), v = __fmul_rn(load_elem(p, DT, base + (lo ? i + half : i - half)), r.y);
+    x[j] = lo ? __fsub_rn(u, v) : __fadd_rn(u, v);
+  }
+}
+
+// One CTA per token; a thread takes eight dimensions of a key, value or query
+// vector, four neighbouring lanes a group of 32.  What it cannot do without is
+// reading the projections once and writing queries and entries; the rest is
+// arithmetic per element (rotation, two divisions' worth of quantising), so the
+// loads are 16 bytes wide where the addresses allow (VEC).  Double precision
+// runs at 1/64 of the fp32 rate here: a chunk takes its angles from the
+// context's two tables with four operations per pair instead of some forty.
+template <int DT, bool VEC>
+__global__ void __launch_bounds__(1024) k_kv4_append(const Kv4AppendArgs a) {
+  __shared__ float2 s_cs[8 * 17];
   pdl_launch_dependents();
   pdl_wait();
   const int t = blockIdx.x, D = a.D;
@@ -86,34 +159,56 @@ __global__ void __launch_bounds__(256) k_kv4_append(const Kv4AppendArgs a) {
     slot = kv_slot(p, a.P, a.R);
   }
   if (a.rotate) {
-    for (int j = threadIdx.x; j < (a.rope_dims >> 1); j += blockDim.x) {
+    const int pairs = a.rope_dims >> 1;
+    for (int j = threadIdx.x; j < pairs; j += blockDim.x) {
       double sn, cs;
-      sincos_taylor((double)p * a.inv_freq[j], sn, cs);
-      s_cs[j] = make_float2((float)(a.amp * cs), (float)(a.amp * sn));
+      if (!a.pos && p < 65536) {
+        const double2 u = a.turns[(size_t)(p & 255) * (D >> 1) + j], v = a.turns[(size_t)(256 + (p >> 8)) * (D >> 1) + j];
+        cs = fma(u.x, v.x, -(u.y * v.y));
+        sn = fma(u.y, v.x, u.x * v.y);
+      } else {
+        sincos_taylor((double)p * a.inv_freq[j], sn, cs);
+      }
+      s_cs[turn_at(j)] = make_float2((float)(a.amp * cs), (float)(a.amp * sn));
     }
     __syncthreads();
   }
-  if (a.q_out)
-    for (int i = threadIdx.x; i < a.q_heads * D; i += blockDim.x)
-      a.q_out[(size_t)t * a.q_heads * D + i] = rotated(a.q, a.dtype, t * a.ldq + (i / D) * D, i % D, a, s_cs);
-
-  const int wpv = D / 8;  // words per vector
+  const int wpv = D >> 3, lw = 31 - __clz(wpv);  // words per vector, a power of two
   uint8_t* row4 = a.kv4 + (size_t)row * 2 * a.nh * a.tiles * kv4_tile_bytes(D);
   const int tile = slot >> 4, s = slot & 15;
-  const int total = 2 * a.nh * wpv;  // a multiple of 4
+  const int kv_items = 2 * a.nh << lw, total = kv_items + (a.q_heads << lw);  // multiples of 4
   for (int i0 = 0; i0 < total; i0 += blockDim.x) {
     const int i = i0 + threadIdx.x;
-    const bool in = i < total;
-    const int vec = in ? i / wpv : 0, w = in ? i % wpv : 0;
-    const int kv = vec >= a.nh, head = kv ? vec - a.nh : vec;
+    const int vec = i >> lw, w = i & (wpv - 1);
     float x[8];
+    if (i >= kv_items) {
+      if (i < total) {
+        const int h = vec - 2 * a.nh;
+        load8_rotated<DT, VEC>(a.q, t * a.ldq + (long long)h * D, 8 * w, a, s_cs, x);
+        float4* o = reinterpret_cast<float4*>(a.q_out + ((size_t)t * a.q_heads + h) * D + 8 * w);
+        if (VEC) {
+          o[0] = make_float4(x[0], x[1], x[2], x[3]);
+          o[1] = make_float4(x[4], x[5], x[6], x[7]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) reinterpret_cast<float*>(o)[j] = x[j];
+        }
+      }
+    }
+    const bool in = i < kv_items;
+    if (!__any_sync(0xffffffffu, in)) continue;
+    const int kv = vec >= a.nh, head = kv ? vec - a.nh : vec;
     float mn = INFINITY, mx = -INFINITY;
     bool ok = true;
     if (in) {
+      if (kv)
+        load8<DT, VEC>(a.v, t * a.ldv + head * a.lhk + 8 * w, x);
+      else if (a.rotate)
+        load8_rotated<DT, VEC>(a.k, t * a.ldk + head * a.lhk, 8 * w, a, s_cs, x);
+      else
+        load8<DT, VEC>(a.k, t * a.ldk + head * a.lhk + 8 * w, x);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        x[j] = kv ? load_elem(a.v, a.dtype, t * a.ldv + head * a.lhk + 8 * w + j)
-                  : rotated(a.k, a.dtype, t * a.ldk + head * a.lhk, 8 * w + j, a, s_cs);
         mn = fminf(mn, x[j]);
         mx = fmaxf(mx, x[j]);
         ok = ok && fabsf(x[j]) <= 65504.f;
@@ -135,8 +230,18 @@ __global__ void __launch_bounds__(256) k_kv4_append(const Kv4AppendArgs a) {
     __half* val = kv ? a.v_val : a.k_val;
     if (val) {
       val += ((size_t)t * a.nh + head) * D + 8 * w;
+      uint32_t v[4];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) val[j] = kv4_value(c[j], sc, lo);
+      for (int j = 0; j < 4; ++j) {
+        const __half2 h = __halves2half2(kv4_value(c[2 * j], sc, lo), kv4_value(c[2 * j + 1], sc, lo));
+        v[j] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+      if (VEC) {
+        *reinterpret_cast<uint4*>(val) = make_uint4(v[0], v[1], v[2], v[3]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) val[j] = __ushort_as_half((unsigned short)(v[j >> 1] >> (16 * (j & 1))));
+      }
     }
     if (!write) continue;
     uint8_t* tp = row4 + ((size_t)(kv * a.nh + head) * a.tiles + tile) * kv4_tile_bytes(D);
@@ -165,7 +270,23 @@ __global__ void __launch_bounds__(256) k_kv4_append(const Kv4AppendArgs a) {
 
 cudaError_t launch_kv4_append(const Kv4AppendArgs& a, int tokens, cudaStream_t st, bool pdl) {
   if (tokens <= 0) return cudaSuccess;
-  return launch_kernel(k_kv4_append, dim3(tokens), dim3(256), 0, st, pdl, a);
+  const long long e = a.dtype == 0 ? 4 : 2;
+  auto wide = [&](const void* p, long long ld) { return ((uintptr_t)p | (uintptr_t)(ld * e)) % 16 == 0; };
+  const bool vec = wide(a.q, a.ldq) && wide(a.k, a.ldk) && wide(a.v, a.ldv) && a.lhk * e % 16 == 0 &&
+                   ((uintptr_t)a.q_out | (uintptr_t)a.k_val | (uintptr_t)a.v_val) % 16 == 0;
+  // few tokens: one round of threads over the vectors, so that a step waits for one load
+  const int items = (2 * a.nh + a.q_heads) * (a.D / 8);
+  const int threads = tokens >= a.n_sm || items <= 256 ? 256 : items <= 512 ? 512 : 1024;
+#define UOCR_APPEND(DT_)                                                                                       \
+  return vec ? launch_kernel(k_kv4_append<DT_, true>, dim3(tokens), dim3(threads), 0, st, pdl, a)              \
+             : launch_kernel(k_kv4_append<DT_, false>, dim3(tokens), dim3(threads), 0, st, pdl, a);
+  switch (a.dtype) {
+    case 0: UOCR_APPEND(0)
+    case 1: UOCR_APPEND(1)
+    case 2: UOCR_APPEND(2)
+  }
+#undef UOCR_APPEND
+  return cudaErrorInvalidValue;
 }
 
 __global__ void k_kv4_zero(const Kv4AppendArgs a, int row, int slot0) {
