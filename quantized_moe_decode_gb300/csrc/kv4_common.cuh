@@ -172,6 +172,7 @@ struct Kv4EvictArgs {
   int* kept;                   // [layers][rows][nh][keep] or nullptr
   __half *k_val, *v_val;       // [layers][rows][nh][keep][D] or nullptr
   int MR, nh, D, tiles, layer0, layers, rows, n, keep, protect;
+  int in_place, wide;          // set by the launcher: a row is its own source; 16-byte aligned values
   unsigned char src[kKv4MaxRows], dst[kKv4MaxRows];
 };
 cudaError_t launch_kv4_evict(const Kv4EvictArgs& a, cudaStream_t st);

@@ -972,6 +972,26 @@ cudaError_t launch_kv4_attn(const Kv4AttnArgs& a, int tokens, cudaStream_t st, b
 }
 
 // ------------------------------------------------------------------ eviction
+// Eight or four fp16 values, in one store where the address allows.
+__device__ __forceinline__ void store16(__half* p, int wide, uint4 v) {
+  if (wide) {
+    *reinterpret_cast<uint4*>(p) = v;
+  } else {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) p[j] = __ushort_as_half((unsigned short)(w[j >> 1] >> (16 * (j & 1))));
+  }
+}
+__device__ __forceinline__ void store8(__half* p, int wide, uint2 v) {
+  if (wide) {
+    *reinterpret_cast<uint2*>(p) = v;
+  } else {
+    const uint32_t w[2] = {v.x, v.y};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) p[j] = __ushort_as_half((unsigned short)(w[j >> 1] >> (16 * (j & 1))));
+  }
+}
+
 // Order of the weights as unsigned integers; -0 counts as 0, a NaN as lowest.
 __device__ __forceinline__ uint32_t weight_key(float w) {
   if (w != w) return 0u;
@@ -979,16 +999,29 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// One CTA per (head, row, layer): the key of the keep-th largest weight by four
-// 8-bit radix passes, then the kept entries move, lowest slot first, to the
-// front of the destination row.  A chunk of kept entries is read into registers
-// before any of it is written, and a kept entry never moves up, so source and
-// destination may be the same row.
-__global__ void __launch_bounds__(256) k_kv4_evict(const Kv4EvictArgs a) {
-  __shared__ int s_hist[256], s_scan[256];
+// One CTA per (head, row, layer).  The key of the keep-th largest weight comes
+// from three radix passes (11, 11, 10 bits; the first digit holds the exponent
+// and two bits, which spreads weights over the bins; lanes with the same digit
+// add once).  Then the kept entries move, lowest slot first, to the front of
+// the destination row: live entries in blocks of the CTA's size are ranked by
+// ballots, and the kept ones go through registers, several per warp at a time.
+// A chunk is read before any of it is written and a kept entry never moves up,
+// so source and destination may be the same row.  Bound by the scattered reads
+// (a slot's values lie in 16-byte pieces of its tile) and the writes.
+constexpr int kEvictThreads = 512;
+constexpr int kEvictKeys = 4096;  // weights kept in shared memory between the passes
+constexpr int kEvictPer = 4;      // entries of a warp in flight
+
+template <int D>
+__global__ void __launch_bounds__(kEvictThreads) k_kv4_evict(const Kv4EvictArgs a) {
+  constexpr int T = kEvictThreads, NW = T / 32, NG = D / kKv4Group, E = kEvictPer, TB = kv4_tile_bytes(D);
+  __shared__ uint32_t s_key[kEvictKeys];
+  __shared__ int s_hist[2048];
+  __shared__ int s_warp[2][NW];
+  __shared__ int s_kept[T];
   __shared__ uint32_t s_prefix;
   __shared__ int s_need;
-  const int head = blockIdx.x, r = blockIdx.y, l = blockIdx.z, D = a.D, NG = D / kKv4Group;
+  const int head = blockIdx.x, r = blockIdx.y, l = blockIdx.z;
   const int layer = a.layer0 + l, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rs = a.src[r], rd = a.dst[r];
   const int2 hole = a.hole[(size_t)layer * a.MR + rs];
@@ -998,141 +1031,188 @@ __global__ void __launch_bounds__(256) k_kv4_evict(const Kv4EvictArgs a) {
   const size_t SLt = (size_t)a.tiles * kKv4Slots;
   const float* ws = a.wts + (((size_t)layer * a.MR + rs) * a.nh + head) * SLt;
   float* wd = a.wts + (((size_t)layer * a.MR + rd) * a.nh + head) * SLt;
-  auto key_of = [&](int i) { return weight_key(ws[slot_of(i)]); };
+  const bool cached = live <= kEvictKeys;
+  if (cached)
+    for (int i = tid; i < live; i += T) s_key[i] = weight_key(ws[slot_of(i)]);
+  auto key_of = [&](int i) { return cached ? s_key[i] : weight_key(ws[slot_of(i)]); };
   // the keep - protect largest of the entries behind the protected ones
   if (tid == 0) {
     s_prefix = 0u;
     s_need = a.keep - a.protect;
   }
-  __syncthreads();
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    s_hist[tid] = 0;
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
+    for (int i = tid; i < 2048; i += T) s_hist[i] = 0;
     __syncthreads();
     const uint32_t prefix = s_prefix;
-    for (int i = a.protect + tid; i < live; i += 256) {
-      const uint32_t k = key_of(i);
-      if (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&s_hist[(k >> shift) & 255], 1);
+    const int need = s_need;
+    for (int i0 = a.protect; i0 < live; i0 += T) {
+      const int i = i0 + tid;
+      const uint32_t k = i < live ? key_of(i) : 0u;
+      const bool in = i < live && (pass == 0 || (k >> (shift + bits)) == (prefix >> (shift + bits)));
+      const uint32_t digit = in ? (k >> shift) & ((1u << bits) - 1u) : 0xFFFFFFFFu;
+      const uint32_t same = __match_any_sync(0xffffffffu, digit);
+      if (in && lane == __ffs(same) - 1) atomicAdd(&s_hist[digit], __popc(same));
     }
     __syncthreads();
-    if (tid == 0) {
-      int need = s_need, b = 255;
-      for (; b > 0 && s_hist[b] < need; --b) need -= s_hist[b];
-      s_need = need;
-      s_prefix = prefix | ((uint32_t)b << shift);
+    // thread t holds the four bins below 2048 - 4t: counts of everything above them
+    int c[4], sum = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) sum += c[j] = s_hist[2047 - 4 * tid - j];
+    int up = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, up, o);
+      if (lane >= o) up += v;
+    }
+    if (lane == 31) s_warp[0][warp] = up;
+    __syncthreads();
+    int above = up - sum;
+    for (int w = 0; w < warp; ++w) above += s_warp[0][w];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {  // the bin that holds the need-th largest
+      if (above < need && above + c[j] >= need) {
+        s_prefix = prefix | ((uint32_t)(2047 - 4 * tid - j) << shift);
+        s_need = need - above;
+      }
+      above += c[j];
     }
     __syncthreads();
   }
+  // entries equal to the threshold stay while there is room, lowest slot first;
+  // nothing beyond the protected ones stays when none is needed
+  const bool some = a.keep > a.protect;
   const uint32_t kth = s_prefix;
-  const int ties = s_need;  // entries equal to the threshold that stay, lowest slot first
-  // move: blocks of 256 live entries, kept ones in order, eight entries at a time
-  const uint8_t* src = a.kv4 + ((size_t)layer * a.MR + rs) * 2 * a.nh * a.tiles * kv4_tile_bytes(D);
-  uint8_t* dst = a.kv4 + ((size_t)layer * a.MR + rd) * 2 * a.nh * a.tiles * kv4_tile_bytes(D);
-  const size_t voff = (size_t)a.nh * a.tiles * kv4_tile_bytes(D);
-  src += (size_t)head * a.tiles * kv4_tile_bytes(D);
-  dst += (size_t)head * a.tiles * kv4_tile_bytes(D);
+  const int ties = some ? s_need : 0;
+
+  const uint8_t* src = a.kv4 + (((size_t)layer * a.MR + rs) * 2 * a.nh + head) * a.tiles * TB;
+  uint8_t* dst = a.kv4 + (((size_t)layer * a.MR + rd) * 2 * a.nh + head) * a.tiles * TB;
+  const size_t voff = (size_t)a.nh * a.tiles * TB;
   const size_t out0 = (((size_t)l * a.rows + r) * a.nh + head) * a.keep;
-  __shared__ int s_kept[256];
-  __shared__ int s_n;
   int done = 0, tied = 0;
-  for (int i0 = 0; i0 < live; i0 += 256) {
+  for (int i0 = 0; i0 < live && done < a.keep; i0 += T) {
     const int i = i0 + tid;
-    uint32_t k = 0;
     bool eq = false, keep = false;
     if (i < live) {
       if (i < a.protect) {
         keep = true;
-      } else {
-        k = key_of(i);
+      } else if (some) {
+        const uint32_t k = key_of(i);
         eq = k == kth;
         keep = k > kth;
       }
     }
-    // rank among the ties of this block
-    s_scan[tid] = eq;
+    const uint32_t below = (1u << lane) - 1u;
+    const uint32_t eqs = __ballot_sync(0xffffffffu, eq);
+    if (lane == 0) s_warp[0][warp] = __popc(eqs);
     __syncthreads();
-    int before = 0, all = 0;
-    for (int j = 0; j < 256; ++j) {
-      const int e = s_scan[j];
-      if (j < tid) before += e;
-      all += e;
+    int before = tied + __popc(eqs & below);
+    for (int w = 0; w < NW; ++w) {
+      if (w < warp) before += s_warp[0][w];
+      tied += s_warp[0][w];
     }
-    if (eq && tied + before < ties) keep = true;
-    tied += all;
+    keep = keep || (eq && before < ties);
+    const uint32_t keeps = __ballot_sync(0xffffffffu, keep);
+    if (lane == 0) s_warp[1][warp] = __popc(keeps);
     __syncthreads();
-    s_scan[tid] = keep;
-    __syncthreads();
-    int at = 0, count = 0;
-    for (int j = 0; j < 256; ++j) {
-      const int e = s_scan[j];
-      if (j < tid) at += e;
-      count += e;
+    int at = __popc(keeps & below), count = 0;
+    for (int w = 0; w < NW; ++w) {
+      if (w < warp) at += s_warp[1][w];
+      count += s_warp[1][w];
     }
-    if (keep) s_kept[at] = i;
-    if (tid == 0) s_n = count;
+    if (keep) s_kept[at] = slot_of(i);
     __syncthreads();
-    for (int c0 = 0; c0 < s_n; c0 += 8) {
-      const bool in = c0 + warp < s_n;
-      const int ss = in ? slot_of(s_kept[c0 + warp]) : 0, ds = done + c0 + warp;
-      const uint8_t* kp = src + (size_t)(ss >> 4) * kv4_tile_bytes(D);
-      const uint8_t* vp = kp + voff;
-      uint32_t kw = 0, kpar = 0;
-      uint16_t vq[2] = {}, vpar = 0;
-      float wt = 0.f;
-      if (in) {
-        const int s = ss & 15;
-        if (lane < D / 8) kw = *reinterpret_cast<const uint32_t*>(kp + kv4_k_word(D, s, lane));
-        if (lane < NG) kpar = *reinterpret_cast<const uint32_t*>(kp + kv4_k_param(D, s, lane));
-        if (lane < D / 4) vq[0] = *reinterpret_cast<const uint16_t*>(vp + kv4_v_quad(D, s, lane));
-        if (lane + 32 < D / 4) vq[1] = *reinterpret_cast<const uint16_t*>(vp + kv4_v_quad(D, s, lane + 32));
-        if (lane < 2 * NG) vpar = *reinterpret_cast<const uint16_t*>(vp + kv4_v_param(D, s, lane >> 1, lane & 1));
-        wt = ws[ss];
-        if (lane == 0 && a.kept) a.kept[out0 + ds] = ss;
-        const size_t o = (out0 + ds) * D;
-        if (a.k_val && lane < D / 8) {
-          __half x[8];
-          key_values(kp, D, s, lane, x);
+    for (int c0 = 0; c0 < count; c0 += NW * E) {
+      uint32_t kw[E], kpar[E];
+      uint16_t vq[E][D == 256 ? 2 : 1], vpar[E];
+      float wt[E];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) a.k_val[o + 8 * lane + j] = x[j];
+      for (int e = 0; e < E; ++e) {
+        const int c = c0 + e * NW + warp;
+        if (c < count) {
+          const int ss = s_kept[c], s = ss & 15;
+          const uint8_t* kp = src + (size_t)(ss >> 4) * TB;
+          const uint8_t* vp = kp + voff;
+          if (lane < D / 8) kw[e] = *reinterpret_cast<const uint32_t*>(kp + kv4_k_word(D, s, lane));
+          if (lane < NG) kpar[e] = *reinterpret_cast<const uint32_t*>(kp + kv4_k_param(D, s, lane));
+          if (lane < D / 4) vq[e][0] = *reinterpret_cast<const uint16_t*>(vp + kv4_v_quad(D, s, lane));
+          if constexpr (D == 256) vq[e][1] = *reinterpret_cast<const uint16_t*>(vp + kv4_v_quad(D, s, lane + 32));
+          if (lane < 2 * NG) vpar[e] = *reinterpret_cast<const uint16_t*>(vp + kv4_v_param(D, s, lane >> 1, lane & 1));
+          if (lane == 0) wt[e] = ws[ss];
         }
-        if (a.v_val)
-          for (int w = lane; w < D / 4; w += 32) {
-            __half x[4];
-            value_values(vp, D, s, w, x);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) a.v_val[o + 4 * w + j] = x[j];
-          }
       }
       __syncthreads();  // the chunk is in registers
-      if (in) {
-        const int s = ds & 15;
-        uint8_t* kq = dst + (size_t)(ds >> 4) * kv4_tile_bytes(D);
-        uint8_t* vd = kq + voff;
-        if (lane < D / 8) *reinterpret_cast<uint32_t*>(kq + kv4_k_word(D, s, lane)) = kw;
-        if (lane < NG) *reinterpret_cast<uint32_t*>(kq + kv4_k_param(D, s, lane)) = kpar;
-        if (lane < D / 4) *reinterpret_cast<uint16_t*>(vd + kv4_v_quad(D, s, lane)) = vq[0];
-        if (lane + 32 < D / 4) *reinterpret_cast<uint16_t*>(vd + kv4_v_quad(D, s, lane + 32)) = vq[1];
-        if (lane < 2 * NG) *reinterpret_cast<uint16_t*>(vd + kv4_v_param(D, s, lane >> 1, lane & 1)) = vpar;
-        if (lane == 0) wd[ds] = wt;
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const int c = c0 + e * NW + warp;
+        if (c < count) {
+          const int ds = done + c, s = ds & 15;
+          uint8_t* kp = dst + (size_t)(ds >> 4) * TB;
+          uint8_t* vp = kp + voff;
+          if (lane < D / 8) *reinterpret_cast<uint32_t*>(kp + kv4_k_word(D, s, lane)) = kw[e];
+          if (lane < NG) *reinterpret_cast<uint32_t*>(kp + kv4_k_param(D, s, lane)) = kpar[e];
+          if (lane < D / 4) *reinterpret_cast<uint16_t*>(vp + kv4_v_quad(D, s, lane)) = vq[e][0];
+          if constexpr (D == 256) *reinterpret_cast<uint16_t*>(vp + kv4_v_quad(D, s, lane + 32)) = vq[e][1];
+          if (lane < 2 * NG) *reinterpret_cast<uint16_t*>(vp + kv4_v_param(D, s, lane >> 1, lane & 1)) = vpar[e];
+          if (lane == 0) {
+            wd[ds] = wt[e];
+            if (a.kept) a.kept[out0 + ds] = s_kept[c];
+          }
+          if (a.k_val) {  // word w belongs to group w / 4
+            const uint32_t p = __shfl_sync(0xffffffffu, kpar[e], lane >> 2);
+            const uint32_t sc = __byte_perm(p, 0, 0x1010), lo = __byte_perm(p, 0, 0x3232);
+            uint32_t x[4];
+            dequant8(kw[e], sc, lo, x);
+            if (lane < D / 8)
+              store16(a.k_val + (out0 + ds) * D + 8 * lane, a.wide, make_uint4(x[0], x[1], x[2], x[3]));
+          }
+          if (a.v_val) {  // quad i belongs to group i / 8
+#pragma unroll
+            for (int h = 0; h < (D == 256 ? 2 : 1); ++h) {
+              const int grp = (lane + 32 * h) >> 3;
+              const uint32_t sc = __shfl_sync(0xffffffffu, (uint32_t)vpar[e], 2 * grp) * 0x10001u;
+              const uint32_t lo = __shfl_sync(0xffffffffu, (uint32_t)vpar[e], 2 * grp + 1) * 0x10001u;
+              const uint32_t q = vq[e][h];
+              uint32_t x[4];
+              // nibbles 0, 1 to one word's halves and 2, 3 to the other's
+              dequant8((q & 0xFu) | ((q & 0xF0u) << 12) | ((q & 0xF00u) >> 4) | ((q & 0xF000u) << 8), sc, lo, x);
+              if (lane + 32 * h < D / 4)
+                store8(a.v_val + (out0 + ds) * D + 4 * (lane + 32 * h), a.wide, make_uint2(x[0], x[1]));
+            }
+          }
+        }
       }
-      __syncthreads();
+      __syncthreads();  // the next chunk's reads follow these writes
     }
-    done += s_n;
-    __syncthreads();
+    done += count;
   }
-  for (int i = a.keep + tid; i < a.n; i += 256) wd[i] = 0.f;
+  for (int i = a.keep + tid; i < a.n; i += T) wd[i] = 0.f;
+  if (!a.in_place && head == 0 && tid == 0)
+    a.hole[(size_t)layer * a.MR + rd] = a.keep < a.n ? make_int2(a.keep, a.n) : make_int2(0, 0);
 }
 
-// The destination rows' holes, once every head has moved.
+// The holes of rows that were their own source, whose heads all had to read them.
 __global__ void k_kv4_hole(const Kv4EvictArgs a) {
   const int r = threadIdx.x, l = blockIdx.x;
   if (r < a.rows)
     a.hole[(size_t)(a.layer0 + l) * a.MR + a.dst[r]] = a.keep < a.n ? make_int2(a.keep, a.n) : make_int2(0, 0);
 }
 
-cudaError_t launch_kv4_evict(const Kv4EvictArgs& a, cudaStream_t st) {
-  k_kv4_evict<<<dim3(a.nh, a.rows, a.layers), 256, 0, st>>>(a);
+cudaError_t launch_kv4_evict(const Kv4EvictArgs& args, cudaStream_t st) {
+  Kv4EvictArgs a = args;
+  a.in_place = 0;
+  for (int i = 0; i < a.rows; ++i) a.in_place |= a.src[i] == a.dst[i];
+  a.wide = ((uintptr_t)a.k_val | (uintptr_t)a.v_val) % 16 == 0;
+  const dim3 grid(a.nh, a.rows, a.layers);
+  switch (a.D) {
+    case 32: k_kv4_evict<32><<<grid, kEvictThreads, 0, st>>>(a); break;
+    case 64: k_kv4_evict<64><<<grid, kEvictThreads, 0, st>>>(a); break;
+    case 128: k_kv4_evict<128><<<grid, kEvictThreads, 0, st>>>(a); break;
+    case 256: k_kv4_evict<256><<<grid, kEvictThreads, 0, st>>>(a); break;
+    default: return cudaErrorInvalidValue;
+  }
   cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || !a.in_place) return e;
   k_kv4_hole<<<a.layers, kKv4MaxRows, 0, st>>>(a);
   return cudaGetLastError();
 }
