@@ -318,9 +318,9 @@ UOCR_API uocr_status uocr_kv_write_i8(uocr_ctx* ctx, int32_t row, int32_t layer,
  * The calls below need a context with kv_int4 = 1 (else UOCR_E_STATE); none
  * needs weights to be loaded, so they also serve a decoder whose projections
  * are the caller's.  A step or prefill of such a context runs the same
- * kernels.  Device pointers are aligned to their element.  Asynchronous (see
- * conventions) unless stated otherwise; they can be captured into a graph of
- * the caller's stream.  uocr_kv_write_prefix / uocr_kv_write quantise the given
+ * kernels.  Device pointers are aligned to their element.  Asynchronous unless
+ * stated otherwise, enqueued on the caller's stream itself (in order with the
+ * steps and the other calls), and can be captured into a graph of it.  uocr_kv_write_prefix / uocr_kv_write quantise the given
  * fp16 vectors and uocr_kv_read returns the entries' values.               */
 
 /* Entries of slots [slot0, slot0+n) of one row and layer, exactly: codes one

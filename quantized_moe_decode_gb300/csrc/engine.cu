@@ -1396,6 +1396,15 @@ uocr_status uocr_load_weights(uocr_ctx* ctx, const uocr_tensor* t, size_t n) {
 
 }  // extern "C"
 
+// The 4-bit cache's own calls run on the caller's stream itself (one launch, no
+// scratch but theirs); whatever runs on the internal stream waits for it first,
+// and the caller's stream for that (step_epilogue).
+static uocr_status kv4_begin(uocr_ctx* ctx) {
+  CK(cudaEventRecord(ctx->ev_in, ctx->ust), "event record");
+  CK(cudaStreamWaitEvent(ctx->st, ctx->ev_in, 0), "stream wait");
+  return UOCR_OK;
+}
+
 // Whether slots [slot0, slot0 + n) of a (row, layer) meet its evicted ones, and
 // whether positions from `pos` on would.
 static bool in_hole(uocr_ctx* ctx, int row, int layer, int slot0, int n) {
@@ -1414,6 +1423,10 @@ static uocr_status kv_put(uocr_ctx* ctx, int row, int layer, int slot0, int n, c
   const uocr_config& c = ctx->cfg;
   const size_t D = c.head_dim, nh = c.n_heads;
   if (n == 0) return UOCR_OK;
+  if (ctx->kv4) {
+    uocr_status s = kv4_begin(ctx);
+    if (s != UOCR_OK) return s;
+  }
   if (!ctx->kv8 && !ctx->kv4) {
     for (int kv = 0; kv < 2; ++kv) {
       const uint16_t* src = kv ? v : k;
@@ -1469,6 +1482,10 @@ static uocr_status kv_put(uocr_ctx* ctx, int row, int layer, int slot0, int n, c
 static uocr_status kv_get(uocr_ctx* ctx, int row, int layer, int slot0, int n, uint16_t* k, uint16_t* v) {
   const uocr_config& c = ctx->cfg;
   const size_t D = c.head_dim, nh = c.n_heads;
+  if (ctx->kv4) {
+    uocr_status s = kv4_begin(ctx);
+    if (s != UOCR_OK) return s;
+  }
   CK(cudaStreamSynchronize(ctx->st), "kv read");
   if (n == 0) return UOCR_OK;
   if (!ctx->kv8 && !ctx->kv4) {
@@ -1677,6 +1694,7 @@ uocr_status uocr_decode_step_host(uocr_ctx* ctx, int32_t rows, const int32_t* to
   if (!token_ids || !positions || !next_ids) return ctx->fail(UOCR_E_INVALID_ARG, "NULL host pointer");
   if (rows < 1 || rows > ctx->cfg.max_rows) return ctx->fail(UOCR_E_INVALID_ARG, "rows out of range");
   uocr_status s = check_complete(ctx);
+  if (s == UOCR_OK && ctx->kv4) s = kv4_begin(ctx);
   if (s != UOCR_OK) return s;
   CK(cudaMemcpyAsync(ctx->ids_buf, token_ids, rows * 4, cudaMemcpyHostToDevice, ctx->st), "ids copy");
   CK(cudaMemcpyAsync(ctx->pos_buf, positions, rows * 4, cudaMemcpyHostToDevice, ctx->st), "positions copy");
@@ -1824,6 +1842,10 @@ uocr_status uocr_kv_reset(uocr_ctx* ctx, int32_t row, int32_t keep_prefix) {
 uocr_status uocr_sync(uocr_ctx* ctx) {
   if (!ctx) return UOCR_E_INVALID_ARG;
   std::lock_guard<std::mutex> lk(ctx->mu);
+  if (ctx->kv4) {
+    uocr_status s = kv4_begin(ctx);
+    if (s != UOCR_OK) return s;
+  }
   CK(cudaStreamSynchronize(ctx->st), "sync");
   int st = 0;
   CK(cudaMemcpy(&st, ctx->status, 4, cudaMemcpyDeviceToHost), "status read");
@@ -2014,14 +2036,10 @@ struct OnDevice {
 };
 }  // namespace
 
-static uocr_status kv4_begin(uocr_ctx* ctx) {
-  CK(cudaEventRecord(ctx->ev_in, ctx->ust), "event record");
-  CK(cudaStreamWaitEvent(ctx->st, ctx->ev_in, 0), "stream wait");
-  return UOCR_OK;
-}
-
 static uocr_status kv4_reset(uocr_ctx* ctx, int r0, int r1, int from) {
   const uocr_config& c = ctx->cfg;
+  uocr_status s = kv4_begin(ctx);
+  if (s != UOCR_OK) return s;
   const size_t tb = kv4_tile_bytes(c.head_dim), SLt = (size_t)ctx->tiles * kKv4Slots;
   if (from == 0) {  // whole rows, and nothing stays evicted
     for (int l = 0; l < c.n_layers; ++l) {
@@ -2034,11 +2052,11 @@ static uocr_status kv4_reset(uocr_ctx* ctx, int r0, int r1, int from) {
            "kv reset");
       for (int r = r0; r < r1; ++r) ctx->hole_h[(size_t)l * c.max_rows + r] = int2{0, 0};
     }
-    return UOCR_OK;
+    return step_epilogue(ctx);
   }
   for (int l = 0; l < c.n_layers; ++l)
     for (int r = r0; r < r1; ++r) CK(launch_kv4_zero(kv4_append_args(ctx, l), r, from, ctx->SL - from, ctx->st), "kv reset");
-  return UOCR_OK;
+  return step_epilogue(ctx);
 }
 
 static uocr_status kv4_io(uocr_ctx* ctx, int row, int layer, int slot0, int n, uint8_t* const codes[2],
@@ -2150,8 +2168,6 @@ static uocr_status kv4_weights(uocr_ctx* ctx, const char* what, int layer, int r
     return ctx->fail(UOCR_E_INVALID_ARG, "%s: NULL pointer or bad layer/row/slot range", what);
   OnDevice dev(c.device);
   CK(dev.e, "set device");
-  uocr_status s = kv4_begin(ctx);
-  if (s != UOCR_OK) return s;
   Kv4WeightsArgs a{};
   a.wts = ctx->wts;
   a.dense = dense;
@@ -2165,8 +2181,8 @@ static uocr_status kv4_weights(uocr_ctx* ctx, const char* what, int layer, int r
   a.slot0 = slot0;
   a.n = n;
   a.put = put;
-  CK(launch_kv4_weights(a, ctx->st), "weights launch");
-  return step_epilogue(ctx);
+  CK(launch_kv4_weights(a, ctx->ust), "weights launch");
+  return UOCR_OK;
 }
 
 extern "C" {
@@ -2226,10 +2242,8 @@ uocr_status uocr_kv_append(uocr_ctx* ctx, int32_t layer, int32_t rows, const int
   a.kv_rstep = 1;
   OnDevice dev(ctx->cfg.device);
   CK(dev.e, "set device");
-  s = kv4_begin(ctx);
-  if (s != UOCR_OK) return s;
-  CK(launch_kv4_append(a, rows, ctx->st, false), "kv append launch");
-  return step_epilogue(ctx);
+  CK(launch_kv4_append(a, rows, ctx->ust, false), "kv append launch");
+  return UOCR_OK;
 }
 
 uocr_status uocr_kv_append_chunk(uocr_ctx* ctx, int32_t layer, int32_t row, int32_t start_pos, int32_t n,
@@ -2245,10 +2259,8 @@ uocr_status uocr_kv_append_chunk(uocr_ctx* ctx, int32_t layer, int32_t row, int3
   a.kv_row0 = row;
   OnDevice dev(ctx->cfg.device);
   CK(dev.e, "set device");
-  s = kv4_begin(ctx);
-  if (s != UOCR_OK) return s;
-  CK(launch_kv4_append(a, n, ctx->st, false), "kv append launch");
-  return step_epilogue(ctx);
+  CK(launch_kv4_append(a, n, ctx->ust, false), "kv append launch");
+  return UOCR_OK;
 }
 
 uocr_status uocr_attend(uocr_ctx* ctx, int32_t layer, int32_t rows, const int32_t* positions, int32_t q_heads,
@@ -2272,10 +2284,8 @@ uocr_status uocr_attend(uocr_ctx* ctx, int32_t layer, int32_t rows, const int32_
   a.kv_rstep = 1;
   OnDevice dev(ctx->cfg.device);
   CK(dev.e, "set device");
-  s = kv4_begin(ctx);
-  if (s != UOCR_OK) return s;
-  CK(launch_kv4_attn(a, rows, ctx->st, false), "attention launch");
-  return step_epilogue(ctx);
+  CK(launch_kv4_attn(a, rows, ctx->ust, false), "attention launch");
+  return UOCR_OK;
 }
 
 uocr_status uocr_attend_chunk(uocr_ctx* ctx, int32_t layer, int32_t row, int32_t start_pos, int32_t n, int32_t q_heads,
@@ -2290,8 +2300,6 @@ uocr_status uocr_attend_chunk(uocr_ctx* ctx, int32_t layer, int32_t row, int32_t
   if (ctx->cfg.use_sink && !ctx->sinks_set) return ctx->fail(UOCR_E_STATE, "use_sink = 1 but uocr_set_sinks was not called");
   OnDevice dev(ctx->cfg.device);
   CK(dev.e, "set device");
-  s = kv4_begin(ctx);
-  if (s != UOCR_OK) return s;
   // the accumulation's scratch holds track_q() queries per cache head
   const int step = ctx->wts ? ctx->track_q() / (q_heads / ctx->cfg.n_heads) : n;
   const int D = ctx->cfg.head_dim, esz = out_dtype == UOCR_DT_F32 ? 4 : 2;
@@ -2303,9 +2311,9 @@ uocr_status uocr_attend_chunk(uocr_ctx* ctx, int32_t layer, int32_t row, int32_t
     a.out_dtype = out_dtype;
     a.pos0 = start_pos + off;
     a.kv_row0 = row;
-    CK(launch_kv4_attn(a, n - off < step ? n - off : step, ctx->st, false), "attention launch");
+    CK(launch_kv4_attn(a, n - off < step ? n - off : step, ctx->ust, false), "attention launch");
   }
-  return step_epilogue(ctx);
+  return UOCR_OK;
 }
 
 uocr_status uocr_kv_evict(uocr_ctx* ctx, int32_t layer, int32_t n_rows, const int32_t* src_rows, const int32_t* dst_rows,
@@ -2360,13 +2368,11 @@ uocr_status uocr_kv_evict(uocr_ctx* ctx, int32_t layer, int32_t n_rows, const in
   a.protect = protect;
   OnDevice dev(c.device);
   CK(dev.e, "set device");
-  s = kv4_begin(ctx);
-  if (s != UOCR_OK) return s;
-  CK(launch_kv4_evict(a, ctx->st), "eviction launch");
+  CK(launch_kv4_evict(a, ctx->ust), "eviction launch");
   for (int l = a.layer0; l < a.layer0 + a.layers; ++l)
     for (int i = 0; i < n_rows; ++i)
       ctx->hole_h[(size_t)l * c.max_rows + dst_rows[i]] = keep < n ? int2{keep, n} : int2{0, 0};
-  return step_epilogue(ctx);
+  return UOCR_OK;
 }
 
 uocr_status uocr_kv_weights_read(uocr_ctx* ctx, int32_t layer, int32_t row0, int32_t n_rows, int32_t slot0, int32_t n,
