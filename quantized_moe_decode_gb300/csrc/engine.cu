@@ -145,6 +145,7 @@ struct uocr_ctx {
   int2* hole = nullptr;        // 4-bit cache: evicted slots [x, y) of each [L][MR]
   std::vector<int2> hole_h;    // ... the same on the host
   float* wts = nullptr;        // accumulated weights [L][MR][nh][16 tiles] (kv_track)
+  float* parts = nullptr;      // attention partials of one pass
   float* scores = nullptr;     // kv_track: scores of one pass [track_q][nh][16 tiles]
   float2* lse = nullptr;       // ... and softmax statistics [track_q][nh]
   // queries per cache head of one tracked pass: a step's rows with eight heads
@@ -410,6 +411,7 @@ static void carve(uocr_ctx* ctx, Carver& cv) {
     ctx->kv4_layer = (size_t)MR * 2 * c.n_heads * ctx->tiles * kv4_tile_bytes(c.head_dim);
     ctx->kv4 = cv.take<uint8_t>(ctx->kv4_layer * Lc, r.kv_cache);
     ctx->hole = cv.take<int2>((size_t)Lc * MR, r.kv_cache);
+    ctx->parts = cv.take<float>((size_t)kAttn4MaxParts * 2 * (c.head_dim + kAttn4PartHead), r.activations);
     ctx->turns = cv.take<double2>((size_t)512 * (c.head_dim / 2), r.weights);
     if (c.kv_track) {
       ctx->wts = cv.take<float>((size_t)Lc * MR * c.n_heads * ctx->tiles * kKv4Slots, r.kv_cache);
@@ -522,6 +524,7 @@ static Kv4AttnArgs kv4_attn_args(uocr_ctx* ctx, int layer) {
   a.sink = c.use_sink ? ctx->sinks + (size_t)layer * c.n_heads : nullptr;
   a.hole = ctx->hole + (size_t)layer * c.max_rows;
   a.wts = ctx->wts ? ctx->wts + (size_t)layer * c.max_rows * c.n_heads * ctx->tiles * kKv4Slots : nullptr;
+  a.parts = ctx->parts;
   a.scores = ctx->scores;
   a.lse = ctx->lse;
   a.n_sm = ctx->n_sm;

@@ -122,6 +122,9 @@ cudaError_t launch_kv4_append(const Kv4AppendArgs& a, int tokens, cudaStream_t s
 // Zero the entries and weights of slots [slot0, slot0 + n) of a row.
 cudaError_t launch_kv4_zero(const Kv4AppendArgs& a, int row, int slot0, int n, cudaStream_t st);
 
+constexpr int kAttn4MaxParts = 16384;  // (runs that the attention's tiles are cut into) x queries, at most
+constexpr int kAttn4PartHead = 4;      // floats before a partial's values: maximum, sum
+constexpr int kKv4MaxRows = 64;
 struct Kv4AttnArgs {
   const float* q;              // [tokens][q_heads][D]
   const uint8_t* kv4;          // layer base
@@ -134,6 +137,8 @@ struct Kv4AttnArgs {
   float* wts;                  // layer base of the accumulated weights, or nullptr
   float* scores;               // scratch when wts is given: [tokens][q_heads][16 tiles], log2 units
   float2* lse;                 // scratch: [tokens][q_heads] (maximum, 1 / sum)
+  float* parts;                // scratch: [runs][2][queries][kAttn4PartHead + D]
+  int n_runs;                  // set by the launcher; 0: one item per CTA
   int q_heads, nh, D, P, R, tiles;
   int kv_row0, kv_rstep;       // kv_rstep 0: every token belongs to cache row kv_row0
   int n_sm;
@@ -164,7 +169,6 @@ struct Kv4WeightsArgs {
 };
 cudaError_t launch_kv4_weights(const Kv4WeightsArgs& a, cudaStream_t st);
 
-constexpr int kKv4MaxRows = 64;
 struct Kv4EvictArgs {
   uint8_t* kv4;                // [L][MR][2][nh][tiles]
   float* wts;                  // [L][MR][nh][16 tiles]

@@ -1,7 +1,5 @@
 // The 4-bit KV cache: rotary positions and the append, attention over the
 // entries, and the eviction of the entries that attention uses least.
-#include <cooperative_groups.h>
-#include <limits.h>
 #include <math.h>
 
 #include "kv4_common.cuh"
@@ -441,16 +439,31 @@ cudaError_t launch_kv4_weights(const Kv4WeightsArgs& a, cudaStream_t st) {
 // outputs accumulate in fp32.  The running maximum of a query moves only when
 // a score exceeds it by 2^8 (weights up to 256 are held), so that almost no tile
 // rescales the accumulators.
-constexpr int kAttn4Warps = 8;
-constexpr int kAttn4Stages = 4;  // tiles of a warp's ring
+//
+// The work of a call is the list of its items' tiles, an item being one (row,
+// head) or one (tile of a chunk's tokens, head).  It is cut into equal runs, one
+// for each warp that fits on the GPU at once, whatever the rows' lengths: a warp
+// goes through its run item by item and meets no barrier.  It finishes an item
+// that lies in its run; of the first and the last, which it shares with its
+// neighbours, it leaves a partial (maximum, sum, weighted values), and a second,
+// small kernel merges those in order.  Items of a few tiles, and the many items
+// of a long chunk, are shared out one per CTA instead.
+constexpr int kAttn4Warps = 4;
 
-template <int D>
+template <int D, int NT>
 struct Attn4 {
   static constexpr int NG = D / 32;
   static constexpr int CB = D / 4;                // code bytes of a lane in a K or V tile
   static constexpr int KPB = D == 256 ? 16 : 8;   // its key parameter bytes
-  static constexpr int STAGE = 32 * (2 * CB + KPB + 16);
-  static constexpr int RING = kAttn4Stages * STAGE;
+  static constexpr int TILE = 32 * (2 * CB + KPB + 16);
+  // tiles of a warp's step (two independent product chains where the registers
+  // allow), steps in its ring, CTAs per SM
+  static constexpr int U = D * NT <= 128 ? 2 : 1;
+  static constexpr int ST = U == 2 || D == 256 ? 3 : 4;
+  static constexpr int CPS = D * NT <= 64 ? 4 : D * NT <= 128 ? 3 : 2;
+  static constexpr int RING = ST * U * TILE;
+  static constexpr bool QREG = D * NT <= 256;  // query fragments in registers, else in shared memory
+  static constexpr int QB = QREG ? 0 : NT * (D / 16) * 32 * 8;
 };
 
 // One exponential; the argument is in units of log2.
@@ -486,7 +499,8 @@ __device__ __forceinline__ void dequant8(uint32_t w, uint32_t s, uint32_t m, uin
   x[3] = hfma2u(s, hsub2u(lop_and_or(h, 0x00F000F0u, 0x54005400u), 0x54005400u), m);
 }
 
-// The slots a CTA reads, as whole tiles: those of [0, x) and of [y, lim).
+// The slots that queries up to `lim` read, as whole tiles: those of [0, x) and of
+// [y, lim).
 struct TileList {
   int ta, tb, count;
   __device__ TileList(int lim, int2 hole) {
@@ -499,417 +513,651 @@ struct TileList {
   __device__ int operator()(int j) const { return j < ta ? j : tb + (j - ta); }
 };
 
+// How a call's tiles are dealt out: item i has tiles [start(i), start(i) + tiles)
+// of the list, run c the tiles [c per, (c + 1) per).
+struct Attn4Runs {
+  const int* cum;  // [rows + 1] tiles of one head in the rows before (rows), shared memory
+  int nh, uniform, per;
+  __device__ int tiles(int z) const { return cum ? cum[z + 1] - cum[z] : uniform; }
+  __device__ long long start(int z, int head) const {
+    return cum ? (long long)cum[z] * nh + (long long)head * tiles(z) : ((long long)z * nh + head) * uniform;
+  }
+};
+
+// Position, and from it the limit, of token t; an invalid one is reported.
+__device__ __forceinline__ int token_limit(const Kv4AttnArgs& a, int t, int2 hole, bool report) {
+  int p = a.pos ? a.pos[t] : a.pos0 + t;
+  if (p < 0 || (hole.y > hole.x && p < hole.y)) {
+    if (report) atomicOr(a.status, kStatusPosition);
+    p = max(p, 0);
+  }
+  return kv_limit(p, a.P, a.R);
+}
+
+// Fill the runs of a call (every thread of a CTA of at least 32).  cum holds
+// kKv4MaxRows + 1 entries.  Returns the number of tiles.
+__device__ __forceinline__ long long attn4_runs(const Kv4AttnArgs& a, int tokens, int n_z, int* cum, Attn4Runs& r) {
+  r.nh = a.nh;
+  r.cum = nullptr;
+  long long total;
+  if (a.kv_rstep) {
+    if (threadIdx.x < 32) {
+      int before = 0;
+      for (int z0 = 0; z0 < tokens; z0 += 32) {
+        const int z = z0 + threadIdx.x;
+        int c = 0;
+        if (z < tokens) {
+          const int2 hole = a.hole[a.kv_row0 + z];
+          c = TileList(token_limit(a, z, hole, false), hole).count;
+        }
+        int up = c;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int v = __shfl_up_sync(0xffffffffu, up, o);
+          if (threadIdx.x >= o) up += v;
+        }
+        if (z < tokens) cum[z + 1] = before + up;
+        before += __shfl_sync(0xffffffffu, up, 31);
+      }
+      if (threadIdx.x == 0) cum[0] = 0;
+    }
+    __syncthreads();
+    r.cum = cum;
+    total = (long long)cum[tokens] * a.nh;
+  } else {  // a chunk: as many tiles for every item as its last token has
+    const int2 hole = a.hole[a.kv_row0];
+    r.uniform = TileList(token_limit(a, tokens - 1, hole, false), hole).count;
+    total = (long long)r.uniform * n_z * a.nh;
+  }
+  // at least two steps in a run
+  const long long per = (total + a.n_runs - 1) / a.n_runs;
+  r.per = (int)(per < 4 ? 4 : per);
+  return total;
+}
+
+// What a partial's sum counts for under the maximum M; one without a finite
+// maximum has summed nothing, or NaN.
+__device__ __forceinline__ float part_factor(float m, float l, float M) {
+  return m == -INFINITY ? (l == 0.f ? 0.f : 1.f) : ex2(m - M);
+}
+
+// Add the softmax weights that a row's queries gave to a head's slots, query by
+// query: four slots for every thread of `from, from + stride, ..`.
+__device__ __forceinline__ void add_weights(const Kv4AttnArgs& a, int z, int head, int row, const TileList& tiles, int nq,
+                                            const float2* fin, int from, int stride) {
+  const size_t SLt = (size_t)a.tiles * kKv4Slots;
+  float* wt = a.wts + ((size_t)row * a.nh + head) * SLt;
+  const float* sc = a.scores + ((size_t)z * a.q_heads + head * nq) * SLt;
+  for (int x = from; x < tiles.count * 4; x += stride) {
+    const int slot = tiles(x >> 2) * 16 + (x & 3) * 4;
+    float4 w = *reinterpret_cast<const float4*>(wt + slot);
+    float4 add = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < nq; ++i) {
+      const float4 v = *reinterpret_cast<const float4*>(sc + i * SLt + slot);
+      const float2 f = fin[i];
+      // a masked slot's score is -infinity: nothing, even under a NaN
+      add.x += v.x == -INFINITY ? 0.f : ex2(v.x - f.x) * f.y;
+      add.y += v.y == -INFINITY ? 0.f : ex2(v.y - f.x) * f.y;
+      add.z += v.z == -INFINITY ? 0.f : ex2(v.z - f.x) * f.y;
+      add.w += v.w == -INFINITY ? 0.f : ex2(v.w - f.x) * f.y;
+    }
+    w.x += add.x, w.y += add.y, w.z += add.z, w.w += add.w;
+    *reinterpret_cast<float4*>(wt + slot) = w;
+  }
+}
+
 template <int D, int NT>
-__global__ void __launch_bounds__(kAttn4Warps * 32, D * NT <= 128 ? 2 : 1) k_kv4_attn(const Kv4AttnArgs a, int n_queries) {
-  using C = Attn4<D>;
-  constexpr int NW = kAttn4Warps, ST = kAttn4Stages, NQ = 4 * NT;
-  constexpr bool QREG = D * NT <= 256;  // query fragments in registers, else in shared memory
+__global__ void __launch_bounds__(kAttn4Warps * 32, Attn4<D, NT>::CPS) k_kv4_attn(const Kv4AttnArgs a, int tokens, int n_z) {
+  using C = Attn4<D, NT>;
+  constexpr int NW = kAttn4Warps, ST = C::ST, U = C::U, NQ = 4 * NT;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ float s_m[NW][NQ], s_l[NW][NQ];
-  __shared__ float s_part[NQ][D + 2];
-  __shared__ float s_c[NQ];     // score factor of each query: scale log2(e) 2^e
-  __shared__ float2 s_fin[NQ];  // final maximum and 1 / sum
-  __shared__ int s_lim[NQ];
-  __shared__ uint2 s_q[QREG ? 1 : NT * (D / 16) * 32];
+  __shared__ float2 s_fin[NW][NQ];  // final maximum and 1 / sum, by the warp that finishes
+  __shared__ int s_cum[kKv4MaxRows + 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int split = blockIdx.x, head = blockIdx.y, G = a.q_heads / a.nh;
-  // queries of this CTA: u = token * G + head in the group
-  const int u0 = a.kv_rstep ? blockIdx.z * G : blockIdx.z * NQ;
-  const int nq = a.kv_rstep ? G : min(NQ, n_queries - u0);
-  const int row = a.kv_row0 + (a.kv_rstep ? blockIdx.z : 0);
-  auto token = [&](int i) { return (u0 + i) / G; };
-  auto q_index = [&](int i) { return (size_t)token(i) * a.q_heads + head * G + (u0 + i) % G; };
+  const int G = a.q_heads / a.nh, run = blockIdx.x * NW + warp;
 
   pdl_launch_dependents();
   pdl_wait();  // queries and new entries come from the previous kernels
-  const int2 hole = a.hole[row];
-  if (threadIdx.x < NQ) {
-    int lim = 0;
-    if (threadIdx.x < nq) {
-      const int tok = token(threadIdx.x);
-      int p = a.pos ? a.pos[tok] : a.pos0 + tok;
-      if (p < 0 || (hole.y > hole.x && p < hole.y)) {
-        atomicOr(a.status, kStatusPosition);
-        p = max(p, 0);
+  Attn4Runs runs;
+  long long at, end;
+  int z = 0, head = 0;
+  if (a.n_runs) {
+    const long long total = attn4_runs(a, tokens, n_z, s_cum, runs);
+    at = (long long)run * runs.per;
+    end = min(total, at + runs.per);
+    if (at >= end) return;  // no barrier follows in this mode
+    if (runs.cum) {
+      int lo = 0, hi = tokens;  // the row that holds tile `at`: the last with start <= at
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if ((long long)runs.cum[mid] * a.nh <= at) lo = mid; else hi = mid;
       }
-      lim = kv_limit(p, a.P, a.R);
+      z = lo;
+      head = (int)((at - (long long)runs.cum[z] * a.nh) / max(runs.tiles(z), 1));
+    } else {
+      const long long item = at / runs.uniform;
+      z = (int)(item / a.nh);
+      head = (int)(item - (long long)z * a.nh);
     }
-    s_lim[threadIdx.x] = lim;
+  } else {  // one item per CTA
+    z = blockIdx.x / a.nh;
+    head = blockIdx.x - z * a.nh;
+    if (!a.kv_rstep) z = n_z - 1 - z;  // a chunk's last tokens read most: first
+    at = 0;
+    end = 1;
   }
-  // queries to fp16 pairs (value, remainder): a warp per query
-  float* sq = reinterpret_cast<float*>(smem);  // [NQ][D], before the ring is used
-  for (int i = warp; i < NQ; i += NW) {
-    float mx = 0.f;
-    for (int d = lane; d < D; d += 32) {
-      const float x = i < nq ? a.q[q_index(i) * D + d] : 0.f;
-      sq[i * D + d] = x;
-      mx = fmaxf(mx, fabsf(x));
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    // 2^-e with e the exponent of the largest magnitude (0 and infinities stay)
-    const int e = mx > 0.f && mx < INFINITY ? min(max(ilogbf(mx), -100), 100) : 0;
-    const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-    for (int d = lane; d < D; d += 32) sq[i * D + d] *= down;
-    if (lane == 0) s_c[i] = a.scale * 1.4426950408889634f * __uint_as_float((uint32_t)(127 + e) << 23);
-  }
-  __syncthreads();
-  uint2 qf[QREG ? NT * (D / 16) : 1];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int k = 0; k < D / 16; ++k) {
-      // step k covers dimensions 8 (k/2) + 4 (k%2) .. + 3 of every lane's quarter
-      const float* s = sq + (4 * nt + (g >> 1)) * D + t * (D / 4) + 4 * k;
-      float v[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float hi = __half2float(__float2half_rn(s[j]));
-        v[j] = (g & 1) ? s[j] - hi : s[j];
-      }
-      const uint2 f = make_uint2(pack2(v[0], v[1]), pack2(v[2], v[3]));
-      if constexpr (QREG)
-        qf[nt * (D / 16) + k] = f;
-      else if (warp == 0)
-        s_q[(nt * (D / 16) + k) * 32 + lane] = f;
-    }
-  int lim_lo = INT_MAX, lim_hi = 0;
-  for (int i = 0; i < nq; ++i) {
-    lim_lo = min(lim_lo, s_lim[i]);
-    lim_hi = max(lim_hi, s_lim[i]);
-  }
-  int lim_q[NT];
-  float cq[NT];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    lim_q[nt] = s_lim[4 * nt + t];
-    cq[nt] = s_c[4 * nt + t];
-  }
-  __syncthreads();  // the ring overwrites sq
 
-  const TileList tiles(lim_hi, hole);
-  const int per = (tiles.count + gridDim.x - 1) / gridDim.x;
-  const int j0 = split * per, j1 = min(tiles.count, j0 + per);
-  const uint8_t* kt = a.kv4 + ((size_t)row * 2 * a.nh + head) * a.tiles * kv4_tile_bytes(D);
-  const uint8_t* vt = kt + (size_t)a.nh * a.tiles * kv4_tile_bytes(D);
-  unsigned char* ring = smem + warp * C::RING;
+  unsigned char* ring = smem + warp * (C::RING + C::QB);
+  uint2* s_q = reinterpret_cast<uint2*>(ring + C::RING);
   const int kp_off = 8 * D + (D == 256 ? g * 64 + t * 16 : (g * C::NG + t * C::NG / 4) * 8);
   const int vp_off = 8 * D + ((g * D / 256) * 4 + t) * 16;
-  auto issue = [&](int j, int stage) {
-    if (j < j1) {
-      const size_t off = (size_t)tiles(j) * kv4_tile_bytes(D);
-      unsigned char* d = ring + stage * C::STAGE;
-      if constexpr (D == 32) {
-        cp_async8(d + lane * 8, kt + off + lane * 8);
-        cp_async8(d + 32 * C::CB + lane * 8, vt + off + lane * 8);
-      } else {
+
+  for (int piece = 0; at < end; ++piece) {
+    // ---- the item: its row, queries (u = token * G + head in the group) and tiles
+    const int u0 = a.kv_rstep ? z * G : z * NQ;
+    const int nq = a.kv_rstep ? G : min(NQ, tokens * G - u0);
+    const int row = a.kv_row0 + (a.kv_rstep ? z : 0);
+    const int2 hole = a.hole[row];
+    const int lim_hi = token_limit(a, (u0 + nq - 1) / G, hole, false), lim_lo = token_limit(a, u0 / G, hole, false);
+    const TileList tiles(lim_hi, hole);
+    int j0 = 0, j1 = tiles.count, step = NW * U, first = warp * U;
+    bool whole = true;
+    if (a.n_runs) {
+      const long long s = runs.start(z, head);
+      const int cnt = runs.tiles(z);
+      const long long left = end - s;
+      j0 = (int)(at - s);
+      j1 = left < cnt ? (int)left : cnt;
+      at = s + j1;
+      whole = j0 == 0 && j1 == cnt;
+      j0 = min(j0, tiles.count);  // a chunk's earlier tokens have fewer
+      j1 = min(j1, tiles.count);
+      step = U;
+      first = j0;
+    } else {
+      at = end;
+    }
+    const uint8_t* kt = a.kv4 + ((size_t)row * 2 * a.nh + head) * a.tiles * kv4_tile_bytes(D);
+    const uint8_t* vt = kt + (size_t)a.nh * a.tiles * kv4_tile_bytes(D);
+    auto issue = [&](int j, int stage) {
 #pragma unroll
-        for (int p = 0; p < C::CB / 16; ++p) {
-          cp_async16(d + p * 512 + lane * 16, kt + off + p * 512 + lane * 16);
-          cp_async16(d + 32 * C::CB + p * 512 + lane * 16, vt + off + p * 512 + lane * 16);
+      for (int u = 0; u < U; ++u) {
+        if (j + u < j1) {
+          const size_t off = (size_t)tiles(j + u) * kv4_tile_bytes(D);
+          unsigned char* d = ring + (stage * U + u) * C::TILE;
+          const uint8_t *kp = kt + off, *vp = vt + off;
+          if constexpr (D == 32) {
+            cp_async8(d + lane * 8, kp + lane * 8);
+            cp_async8(d + 32 * C::CB + lane * 8, vp + lane * 8);
+          } else {
+#pragma unroll
+            for (int p = 0; p < C::CB / 16; ++p) {
+              cp_async16(d + p * 512 + lane * 16, kp + p * 512 + lane * 16);
+              cp_async16(d + 32 * C::CB + p * 512 + lane * 16, vp + p * 512 + lane * 16);
+            }
+          }
+          if constexpr (C::KPB == 16)
+            cp_async16(d + 64 * C::CB + lane * 16, kp + kp_off);
+          else
+            cp_async8(d + 64 * C::CB + lane * 8, kp + kp_off);
+          cp_async16(d + 64 * C::CB + 32 * C::KPB + lane * 16, vp + vp_off);
         }
       }
-      if constexpr (C::KPB == 16)
-        cp_async16(d + 64 * C::CB + lane * 16, kt + off + kp_off);
-      else
-        cp_async8(d + 64 * C::CB + lane * 8, kt + off + kp_off);
-      cp_async16(d + 64 * C::CB + 32 * C::KPB + lane * 16, vt + off + vp_off);
+      cp_commit();
+    };
+#pragma unroll
+    for (int k = 0; k < ST - 1; ++k) issue(first + k * step, k);
+
+    // ---- queries as fp16 pairs (value, remainder), four at a time through the
+    // ring's last slots, which the first step fills only after this
+    uint2 qf[C::QREG ? NT * (D / 16) : 1];
+    int lim_q[NT];
+    float cq[NT];   // score factor: scale log2(e) 2^e
+    float* so[NT];  // this lane's query in the scores' scratch
+    float* s_sq = reinterpret_cast<float*>(ring + (ST - 1) * U * C::TILE);  // [4][D]
+    static_assert(U * C::TILE >= 16 * D, "four queries fit a ring slot");
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float mine = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int u = u0 + 4 * nt + i;
+        const bool have = 4 * nt + i < nq;
+        float mx = 0.f, x[D / 32];
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k) {
+          x[k] = have ? a.q[((size_t)(u / G) * a.q_heads + head * G + u % G) * D + lane + 32 * k] : 0.f;
+          mx = fmaxf(mx, fabsf(x[k]));
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        // 2^-e with e the exponent of the largest magnitude (0 and infinities stay)
+        const int e = mx > 0.f && mx < INFINITY ? min(max(ilogbf(mx), -100), 100) : 0;
+        const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+        if (t == i) mine = a.scale * 1.4426950408889634f * __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k) s_sq[i * D + lane + 32 * k] = x[k] * down;
+      }
+      cq[nt] = mine;
+      {
+        const int i = 4 * nt + t, tok = (u0 + i) / G;
+        lim_q[nt] = i < nq ? token_limit(a, tok, hole, g == 0) : 0;
+        so[nt] = a.scores && i < nq
+                     ? a.scores + ((size_t)tok * a.q_heads + head * G + (u0 + i) % G) * a.tiles * kKv4Slots + g
+                     : nullptr;
+      }
+      __syncwarp();
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        // step k covers dimensions 4k .. 4k+3 of every lane's quarter
+        const float4 q4 = *reinterpret_cast<const float4*>(s_sq + (g >> 1) * D + t * (D / 4) + 4 * k);
+        float v[4] = {q4.x, q4.y, q4.z, q4.w};
+        if (g & 1)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[j] -= __half2float(__float2half_rn(v[j]));
+        const uint2 f = make_uint2(pack2(v[0], v[1]), pack2(v[2], v[3]));
+        if constexpr (C::QREG)
+          qf[nt * (D / 16) + k] = f;
+        else
+          s_q[(nt * (D / 16) + k) * 32 + lane] = f;  // read by this lane alone
+      }
+      __syncwarp();
     }
-    cp_commit();
-  };
 
-  float m_ref[NT], l[NT], acc[NT][D / 16][4];
+    float m_ref[NT], l[NT], acc[NT][D / 16][4];
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    m_ref[nt] = -INFINITY;
-    l[nt] = 0.f;
+    for (int nt = 0; nt < NT; ++nt) {
+      m_ref[nt] = -INFINITY;
+      l[nt] = 0.f;
 #pragma unroll
-    for (int i = 0; i < D / 16; ++i)
+      for (int i = 0; i < D / 16; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[nt][i][j] = 0.f;
-  }
-#pragma unroll
-  for (int s = 0; s < ST - 1; ++s) issue(j0 + warp + s * NW, s);
+        for (int j = 0; j < 4; ++j) acc[nt][i][j] = 0.f;
+    }
+    int stage = 0;
+    for (int j = first; j < j1; j += step) {
+      cp_wait<ST - 2>();
+      const unsigned char* d = ring + stage * U * C::TILE;
+      issue(j + (ST - 1) * step, stage == 0 ? ST - 1 : stage - 1);  // the slots that the last step left
+      stage = stage == ST - 1 ? 0 : stage + 1;
 
-  int stage = 0;
-  for (int j = j0 + warp; j < j1; j += NW) {
-    cp_wait<ST - 2>();
-    const unsigned char* d = ring + stage * C::STAGE;
-    issue(j + (ST - 1) * NW, stage == 0 ? ST - 1 : stage - 1);  // the slot that the last tile left
-    stage = stage == ST - 1 ? 0 : stage + 1;
-    const int slot0 = tiles(j) * 16;
-    const bool gap = hole.y > hole.x;
-    const bool full = slot0 + 16 <= lim_lo && (!gap || slot0 + 16 <= hole.x || slot0 >= hole.y);
+      // ---- scores
+      float sc[U][NT][4];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sc[u][nt][i] = 0.f;
+        const unsigned char* du = d + u * C::TILE;
+        constexpr int W = D / 32;  // words per slot
+        uint32_t w[2 * W];
+        if constexpr (D == 32) {
+          const uint2 v = *reinterpret_cast<const uint2*>(du + lane * 8);
+          w[0] = v.x;
+          w[1] = v.y;
+        } else {
+#pragma unroll
+          for (int p = 0; p < W / 2; ++p) {
+            const uint4 v = lds128(du + p * 512 + lane * 16);
+            w[4 * p] = v.x;
+            w[4 * p + 1] = v.y;
+            w[4 * p + 2] = v.z;
+            w[4 * p + 3] = v.w;
+          }
+        }
+        // (s, m) of slots g and g + 8, one or two groups
+        uint32_t par[4];
+        if constexpr (C::KPB == 16) {
+          const uint4 v = lds128(du + 64 * C::CB + lane * 16);
+          par[0] = v.x, par[1] = v.y, par[2] = v.z, par[3] = v.w;
+        } else {
+          const uint2 v = *reinterpret_cast<const uint2*>(du + 64 * C::CB + lane * 8);
+          par[0] = v.x, par[1] = v.y, par[2] = v.x, par[3] = v.y;
+        }
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+          const uint32_t p0 = par[i >= 4 ? 2 : 0], p1 = par[i >= 4 ? 3 : 1];
+          uint32_t e[4], f[4];
+          dequant8(w[i], __byte_perm(p0, 0, 0x1010), __byte_perm(p0, 0, 0x3232), e);
+          dequant8(w[W + i], __byte_perm(p1, 0, 0x1010), __byte_perm(p1, 0, 0x3232), f);
+          const uint32_t a0[4] = {e[0], f[0], e[1], f[1]}, a1[4] = {e[2], f[2], e[3], f[3]};
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            uint2 b0, b1;
+            if constexpr (C::QREG) {
+              b0 = qf[nt * (D / 16) + 2 * i];
+              b1 = qf[nt * (D / 16) + 2 * i + 1];
+            } else {
+              b0 = s_q[(nt * (D / 16) + 2 * i) * 32 + lane];
+              b1 = s_q[(nt * (D / 16) + 2 * i + 1) * 32 + lane];
+            }
+            mma_16816(sc[u][nt], a0, b0.x, b0.y);
+            mma_16816(sc[u][nt], a1, b1.x, b1.y);
+          }
+        }
+      }
+      // ---- softmax: lane (g, t) holds slots g and g + 8 of query t
+      float p[U][NT][2];
+      bool full[U];
+      int slot0[U];
+      bool raise = false;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const bool have = j + u < j1;
+        slot0[u] = have ? tiles(j + u) * 16 : 0x7FFFFF00;  // a missing second tile lies behind every limit
+        full[u] = slot0[u] + 16 <= lim_lo && (hole.y <= hole.x || slot0[u] + 16 <= hole.x || slot0[u] >= hole.y);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          p[u][nt][0] = (sc[u][nt][0] + sc[u][nt][1]) * cq[nt];
+          p[u][nt][1] = (sc[u][nt][2] + sc[u][nt][3]) * cq[nt];
+          if (!full[u]) {
+            const int s0 = slot0[u] + g, s1 = s0 + 8;
+            if (s0 >= lim_q[nt] || (s0 >= hole.x && s0 < hole.y)) p[u][nt][0] = -INFINITY;
+            if (s1 >= lim_q[nt] || (s1 >= hole.x && s1 < hole.y)) p[u][nt][1] = -INFINITY;
+          }
+          if (so[nt] && have) {
+            so[nt][slot0[u]] = p[u][nt][0];
+            so[nt][slot0[u] + 8] = p[u][nt][1];
+          }
+          raise = raise || fmaxf(p[u][nt][0], p[u][nt][1]) > m_ref[nt] + 8.f;
+        }
+      }
+      if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float mx = m_ref[nt];
+#pragma unroll
+          for (int u = 0; u < U; ++u) mx = fmaxf(mx, fmaxf(p[u][nt][0], p[u][nt][1]));
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+          const float corr = m_ref[nt] == mx ? 1.f : ex2(m_ref[nt] - mx);
+          m_ref[nt] = mx;
+          l[nt] *= corr;
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) acc[nt][i][k] *= corr;
+        }
+      }
+      uint32_t pb[U][NT][2];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const float m = m_ref[nt] == -INFINITY ? 0.f : m_ref[nt];
+          const float x = ex2(p[u][nt][0] - m), y = ex2(p[u][nt][1] - m);
+          l[nt] += x + y;
+          // column g of the B fragment: query g / 2, its weight or the remainder
+          const int src = 8 * t + (g >> 1);
+          const float v0 = __shfl_sync(0xffffffffu, x, src), v1 = __shfl_sync(0xffffffffu, x, src + 4);
+          const float v2 = __shfl_sync(0xffffffffu, y, src), v3 = __shfl_sync(0xffffffffu, y, src + 4);
+          const uint32_t h0 = pack2(v0, v1), h1 = pack2(v2, v3);
+          if (g & 1) {
+            const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&h0));
+            const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&h1));
+            pb[u][nt][0] = pack2(v0 - f0.x, v1 - f0.y);
+            pb[u][nt][1] = pack2(v2 - f1.x, v3 - f1.y);
+          } else {
+            pb[u][nt][0] = h0;
+            pb[u][nt][1] = h1;
+          }
+        }
+      // ---- values: slots 2t, 2t+1 (par.x, par.y) and 2t+8, 2t+9 (par.z, par.w)
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const unsigned char* du = d + u * C::TILE;
+        uint4 par = lds128(du + 64 * C::CB + 32 * C::KPB + lane * 16);
+        // slots that no query reads become zeros: their weight is zero, but an unread
+        // NaN or infinity times zero would not be
+        if (!full[u]) {
+          const int s = slot0[u] + 2 * t;
+          auto live = [&](int x) { return x < lim_hi && !(x >= hole.x && x < hole.y); };
+          const uint32_t k0 = (live(s) ? 0xFFFFu : 0u) | (live(s + 1) ? 0xFFFF0000u : 0u);
+          const uint32_t k1 = (live(s + 8) ? 0xFFFFu : 0u) | (live(s + 9) ? 0xFFFF0000u : 0u);
+          par.x &= k0, par.y &= k0, par.z &= k1, par.w &= k1;
+        }
+        if (!full[u] && lim_lo != lim_hi) {
+          // a slot that only some of the tile's queries read: where its group is not
+          // finite it is left out of the products, and the queries that do read it
+          // get NaN there (a lane's values of a slot all belong to one group)
+          auto odd = [](uint32_t s, uint32_t m) {
+            return (((s & 0x7C00u) == 0x7C00u || (m & 0x7C00u) == 0x7C00u) ? 1u : 0u) |
+                   (((s & 0x7C000000u) == 0x7C000000u || (m & 0x7C000000u) == 0x7C000000u) ? 2u : 0u);
+          };
+          const uint32_t b0 = odd(par.x, par.y), b1 = odd(par.z, par.w);
+          uint32_t bad = (b0 << (2 * t)) | (b1 << (2 * t + 8));
+          if (__any_sync(0xffffffffu, bad != 0u)) {
+            const uint32_t k0 = (b0 & 1 ? 0u : 0xFFFFu) | (b0 & 2 ? 0u : 0xFFFF0000u);
+            const uint32_t k1 = (b1 & 1 ? 0u : 0xFFFFu) | (b1 & 2 ? 0u : 0xFFFF0000u);
+            par.x &= k0, par.y &= k0, par.z &= k1, par.w &= k1;
+            bad |= __shfl_xor_sync(0xffffffffu, bad, 1);
+            bad |= __shfl_xor_sync(0xffffffffu, bad, 2);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              const int n = min(max(lim_q[nt] - slot0[u], 0), 16);  // the query reads the tile's first n slots
+              if (bad & ((1u << n) - 1u))
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) acc[nt][i][0] = acc[nt][i][2] = __int_as_float(0x7FFFFFFF);
+            }
+          }
+        }
+        constexpr int Q = D / 32;  // words per slot pair
+        uint32_t w[2 * Q];
+        if constexpr (D == 32) {
+          const uint2 v = *reinterpret_cast<const uint2*>(du + 32 * C::CB + lane * 8);
+          w[0] = v.x;
+          w[1] = v.y;
+        } else {
+#pragma unroll
+          for (int q = 0; q < Q / 2; ++q) {
+            const uint4 v = lds128(du + 32 * C::CB + q * 512 + lane * 16);
+            w[4 * q] = v.x;
+            w[4 * q + 1] = v.y;
+            w[4 * q + 2] = v.z;
+            w[4 * q + 3] = v.w;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < Q; ++i) {
+          uint32_t e[4], f[4];
+          dequant8(w[i], par.x, par.y, e);
+          dequant8(w[Q + i], par.z, par.w, f);
+          const uint32_t a0[4] = {e[0], e[1], f[0], f[1]}, a1[4] = {e[2], e[3], f[2], f[3]};
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            mma_16816(acc[nt][2 * i], a0, pb[u][nt][0], pb[u][nt][1]);
+            mma_16816(acc[nt][2 * i + 1], a1, pb[u][nt][0], pb[u][nt][1]);
+          }
+        }
+      }
+    }
+    cp_wait<0>();
 
-    // ---- scores
-    float sc[NT][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) sc[nt][i] = 0.f;
-    {
-      constexpr int W = D / 32;  // words per slot
-      uint32_t w[2 * W];
-      if constexpr (D == 32) {
-        const uint2 u = *reinterpret_cast<const uint2*>(d + lane * 8);
-        w[0] = u.x;
-        w[1] = u.y;
-      } else {
-#pragma unroll
-        for (int p = 0; p < W / 2; ++p) {
-          const uint4 u = lds128(d + p * 512 + lane * 16);
-          w[4 * p] = u.x;
-          w[4 * p + 1] = u.y;
-          w[4 * p + 2] = u.z;
-          w[4 * p + 3] = u.w;
-        }
-      }
-      // (s, m) of slots g and g + 8, one or two groups
-      uint32_t par[4];
-      if constexpr (C::KPB == 16) {
-        const uint4 u = lds128(d + 64 * C::CB + lane * 16);
-        par[0] = u.x, par[1] = u.y, par[2] = u.z, par[3] = u.w;
-      } else {
-        const uint2 u = *reinterpret_cast<const uint2*>(d + 64 * C::CB + lane * 8);
-        par[0] = u.x, par[1] = u.y, par[2] = u.x, par[3] = u.y;
-      }
-#pragma unroll
-      for (int i = 0; i < W; ++i) {
-        const uint32_t p0 = par[i >= 4 ? 2 : 0], p1 = par[i >= 4 ? 3 : 1];
-        uint32_t e[4], f[4];
-        dequant8(w[i], __byte_perm(p0, 0, 0x1010), __byte_perm(p0, 0, 0x3232), e);
-        dequant8(w[W + i], __byte_perm(p1, 0, 0x1010), __byte_perm(p1, 0, 0x3232), f);
-        const uint32_t a0[4] = {e[0], f[0], e[1], f[1]}, a1[4] = {e[2], f[2], e[3], f[3]};
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          uint2 b0, b1;
-          if constexpr (QREG) {
-            b0 = qf[nt * (D / 16) + 2 * i];
-            b1 = qf[nt * (D / 16) + 2 * i + 1];
-          } else {
-            b0 = s_q[(nt * (D / 16) + 2 * i) * 32 + lane];
-            b1 = s_q[(nt * (D / 16) + 2 * i + 1) * 32 + lane];
-          }
-          mma_16816(sc[nt], a0, b0.x, b0.y);
-          mma_16816(sc[nt], a1, b1.x, b1.y);
-        }
-      }
-    }
-    // ---- softmax: lane (g, t) holds slots g and g + 8 of query t
-    float p0[NT], p1[NT];
-    bool raise = false;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      p0[nt] = (sc[nt][0] + sc[nt][1]) * cq[nt];
-      p1[nt] = (sc[nt][2] + sc[nt][3]) * cq[nt];
-      if (!full) {
-        const int s0 = slot0 + g, s1 = s0 + 8;
-        if (s0 >= lim_q[nt] || (s0 >= hole.x && s0 < hole.y)) p0[nt] = -INFINITY;
-        if (s1 >= lim_q[nt] || (s1 >= hole.x && s1 < hole.y)) p1[nt] = -INFINITY;
-      }
-      if (a.scores && 4 * nt + t < nq) {
-        float* so = a.scores + q_index(4 * nt + t) * (size_t)a.tiles * kKv4Slots + slot0 + g;
-        so[0] = p0[nt];
-        so[8] = p1[nt];
-      }
-      raise = raise || fmaxf(p0[nt], p1[nt]) > m_ref[nt] + 8.f;
-    }
-    if (__any_sync(0xffffffffu, raise)) {
+      for (int o = 4; o < 32; o <<= 1) l[nt] += __shfl_xor_sync(0xffffffffu, l[nt], o);
+    const float sink = a.sink ? a.sink[head] * 1.4426950408889634f : -INFINITY;
+    if (a.n_runs) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        float mx = fmaxf(p0[nt], p1[nt]);
+        const int i = 4 * nt + t;
+        if (i >= nq) continue;
+        if (whole) {
+          const float M = fmaxf(m_ref[nt], sink), f = part_factor(m_ref[nt], l[nt], M);
+          const float L = l[nt] * f + (a.sink ? ex2(sink - M) : 0.f);
+          const float inv = L == 0.f ? 0.f : 1.f / L, c = f * inv;  // nothing to read: zeros
+          const size_t qi = (size_t)((u0 + i) / G) * a.q_heads + head * G + (u0 + i) % G;
+          const long long o = (long long)qi * D + g * (D / 8);
 #pragma unroll
-        for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        const float m_new = fmaxf(m_ref[nt], mx);
-        const float corr = m_ref[nt] == m_new ? 1.f : ex2(m_ref[nt] - m_new);
-        m_ref[nt] = m_new;
-        l[nt] *= corr;
+          for (int x = 0; x < D / 16; ++x) {
+            store_elem(a.out, a.out_dtype, o + 2 * x, (acc[nt][x][0] + acc[nt][x][1]) * c);
+            store_elem(a.out, a.out_dtype, o + 2 * x + 1, (acc[nt][x][2] + acc[nt][x][3]) * c);
+          }
+          if (g == 0) {
+            s_fin[warp][i] = make_float2(M, inv);
+            if (a.lse) a.lse[qi] = make_float2(M, inv);
+          }
+        } else {
+          float* o = a.parts + (((size_t)run * 2 + (piece > 0)) * NQ + i) * (D + kAttn4PartHead);
+          if (g == 0) *reinterpret_cast<float2*>(o) = make_float2(m_ref[nt], l[nt]);
+          o += kAttn4PartHead + g * (D / 8);
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) acc[nt][i][k] *= corr;
+          for (int x = 0; x < D / 16; x += 2)
+            *reinterpret_cast<float4*>(o + 2 * x) =
+                make_float4(acc[nt][x][0] + acc[nt][x][1], acc[nt][x][2] + acc[nt][x][3],
+                            acc[nt][x + 1][0] + acc[nt][x + 1][1], acc[nt][x + 1][2] + acc[nt][x + 1][3]);
+        }
       }
+      __syncwarp();
+      if (whole && a.wts && a.kv_rstep) add_weights(a, z, head, row, tiles, nq, s_fin[warp], lane, 32);
+      if (++head == a.nh) {
+        head = 0;
+        ++z;
+      }
+      __syncwarp();
+      continue;
     }
-    uint32_t pb[NT][2];
+    __syncthreads();  // the rings are free: they take the warps' partials
+    float* s_acc = reinterpret_cast<float*>(smem);  // [NW][NQ][D]
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const float m = m_ref[nt] == -INFINITY ? 0.f : m_ref[nt];
-      p0[nt] = ex2(p0[nt] - m);
-      p1[nt] = ex2(p1[nt] - m);
-      l[nt] += p0[nt] + p1[nt];
-      // column g of the B fragment: query g / 2, its weight or the remainder
-      const int src = 8 * t + (g >> 1);
-      const float v0 = __shfl_sync(0xffffffffu, p0[nt], src), v1 = __shfl_sync(0xffffffffu, p0[nt], src + 4);
-      const float v2 = __shfl_sync(0xffffffffu, p1[nt], src), v3 = __shfl_sync(0xffffffffu, p1[nt], src + 4);
-      const uint32_t h0 = pack2(v0, v1), h1 = pack2(v2, v3);
-      if (g & 1) {
-        const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&h0));
-        const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&h1));
-        pb[nt][0] = pack2(v0 - f0.x, v1 - f0.y);
-        pb[nt][1] = pack2(v2 - f1.x, v3 - f1.y);
-      } else {
-        pb[nt][0] = h0;
-        pb[nt][1] = h1;
+      const int i = 4 * nt + t;
+      if (g == 0) {
+        s_m[warp][i] = m_ref[nt];
+        s_l[warp][i] = l[nt];
       }
-    }
-    // ---- values: slots 2t, 2t+1 (par.x, par.y) and 2t+8, 2t+9 (par.z, par.w)
-    uint4 par = lds128(d + 64 * C::CB + 32 * C::KPB + lane * 16);
-    auto accumulate = [&](const uint4& vp) {
-      constexpr int Q = D / 32;  // words per slot pair
-      uint32_t w[2 * Q];
-      if constexpr (D == 32) {
-        const uint2 u = *reinterpret_cast<const uint2*>(d + 32 * C::CB + lane * 8);
-        w[0] = u.x;
-        w[1] = u.y;
-      } else {
+      if (i < nq) {
+        float* o = s_acc + (warp * NQ + i) * D + g * (D / 8);
 #pragma unroll
-        for (int p = 0; p < Q / 2; ++p) {
-          const uint4 u = lds128(d + 32 * C::CB + p * 512 + lane * 16);
-          w[4 * p] = u.x;
-          w[4 * p + 1] = u.y;
-          w[4 * p + 2] = u.z;
-          w[4 * p + 3] = u.w;
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < Q; ++i) {
-        uint32_t e[4], f[4];
-        dequant8(w[i], vp.x, vp.y, e);
-        dequant8(w[Q + i], vp.z, vp.w, f);
-        const uint32_t a0[4] = {e[0], e[1], f[0], f[1]}, a1[4] = {e[2], e[3], f[2], f[3]};
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          mma_16816(acc[nt][2 * i], a0, pb[nt][0], pb[nt][1]);
-          mma_16816(acc[nt][2 * i + 1], a1, pb[nt][0], pb[nt][1]);
-        }
-      }
-    };
-    // slots that no query reads become zeros: their weight is zero, but an unread
-    // NaN or infinity times zero would not be
-    if (!full) {
-      const int s = slot0 + 2 * t;
-      auto live = [&](int x) { return x < lim_hi && !(x >= hole.x && x < hole.y); };
-      const uint32_t k0 = (live(s) ? 0xFFFFu : 0u) | (live(s + 1) ? 0xFFFF0000u : 0u);
-      const uint32_t k1 = (live(s + 8) ? 0xFFFFu : 0u) | (live(s + 9) ? 0xFFFF0000u : 0u);
-      par.x &= k0, par.y &= k0, par.z &= k1, par.w &= k1;
-    }
-    if (!full && lim_lo != lim_hi) {
-      // a slot that only some of the tile's queries read: where its group is not
-      // finite it is left out of the products, and the queries that do read it
-      // get NaN there (a lane's values of a slot all belong to one group)
-      auto odd = [](uint32_t s, uint32_t m) {
-        return (((s & 0x7C00u) == 0x7C00u || (m & 0x7C00u) == 0x7C00u) ? 1u : 0u) |
-               (((s & 0x7C000000u) == 0x7C000000u || (m & 0x7C000000u) == 0x7C000000u) ? 2u : 0u);
-      };
-      const uint32_t b0 = odd(par.x, par.y), b1 = odd(par.z, par.w);
-      uint32_t bad = (b0 << (2 * t)) | (b1 << (2 * t + 8));
-      if (__any_sync(0xffffffffu, bad != 0u)) {
-        const uint32_t k0 = (b0 & 1 ? 0u : 0xFFFFu) | (b0 & 2 ? 0u : 0xFFFF0000u);
-        const uint32_t k1 = (b1 & 1 ? 0u : 0xFFFFu) | (b1 & 2 ? 0u : 0xFFFF0000u);
-        par.x &= k0, par.y &= k0, par.z &= k1, par.w &= k1;
-        bad |= __shfl_xor_sync(0xffffffffu, bad, 1);
-        bad |= __shfl_xor_sync(0xffffffffu, bad, 2);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const int n = min(max(lim_q[nt] - slot0, 0), 16);  // the query reads the tile's first n slots
-          if (bad & ((1u << n) - 1u))
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i) acc[nt][i][0] = acc[nt][i][2] = __int_as_float(0x7FFFFFFF);
+        for (int x = 0; x < D / 16; ++x) {
+          o[2 * x] = acc[nt][x][0] + acc[nt][x][1];
+          o[2 * x + 1] = acc[nt][x][2] + acc[nt][x][3];
         }
       }
     }
-    accumulate(par);
+    __syncthreads();
+    for (int i = warp; i < nq; i += NW) {
+      const size_t qi = (size_t)((u0 + i) / G) * a.q_heads + head * G + (u0 + i) % G;
+      float M = sink;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) M = fmaxf(M, s_m[w][i]);
+      float f[NW], L = a.sink ? ex2(sink - M) : 0.f;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+        f[w] = part_factor(s_m[w][i], s_l[w][i], M);
+        L += s_l[w][i] * f[w];
+      }
+      const float inv = L == 0.f ? 0.f : 1.f / L;  // nothing to read: zeros
+#pragma unroll
+      for (int d = lane; d < D; d += 32) {
+        float v = 0.f;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) v += s_acc[(w * NQ + i) * D + d] * f[w];
+        store_elem(a.out, a.out_dtype, (long long)(qi * D + d), v * inv);
+      }
+      if (lane == 0) {
+        s_fin[0][i] = make_float2(M, inv);
+        if (a.lse) a.lse[qi] = make_float2(M, inv);
+      }
+    }
+    if (a.wts && a.kv_rstep) {  // this CTA alone has the item's slots
+      __syncthreads();
+      add_weights(a, z, head, row, tiles, nq, s_fin[0], threadIdx.x, NW * 32);
+    }
   }
-  cp_wait<0>();
-  __syncthreads();  // the rings are free: they take the warps' partials
+}
 
-  float* s_acc = reinterpret_cast<float*>(smem);  // [NW][NQ][D]
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const int i = 4 * nt + t;
-#pragma unroll
-    for (int o = 4; o < 32; o <<= 1) l[nt] += __shfl_xor_sync(0xffffffffu, l[nt], o);
-    if (g == 0) {
-      s_m[warp][i] = m_ref[nt];
-      s_l[warp][i] = l[nt];
+// Merge the runs' partials: a CTA per (item, query of the item), which also adds
+// its share of the row's weights.  A partial's factor is taken once; the values
+// are then independent loads, so that the time is a few trips to the L2.
+__global__ void __launch_bounds__(256) k_kv4_merge(const Kv4AttnArgs a, int tokens, int n_z, int nq_tile) {
+  constexpr int CAP = 256;  // partials whose factors are held at a time
+  __shared__ int s_cum[kKv4MaxRows + 1];
+  __shared__ float2 s_fin[8];
+  __shared__ float s_f[CAP];
+  __shared__ float s_acc[8][256];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, D = a.D, G = a.q_heads / a.nh;
+  const int head = blockIdx.x % a.nh, z = blockIdx.x / a.nh, mine = blockIdx.y;
+  Attn4Runs runs;
+  attn4_runs(a, tokens, n_z, s_cum, runs);
+  const int cnt = runs.tiles(z);
+  const long long s = runs.start(z, head);
+  const int u0 = a.kv_rstep ? z * G : z * nq_tile;
+  const int nq = a.kv_rstep ? G : min(nq_tile, tokens * G - u0);
+  const int c0 = (int)(s / runs.per), n = cnt ? (int)((s + cnt - 1) / runs.per) - c0 + 1 : 0;
+  if (mine >= nq || n == 1) return;  // one run's: finished there
+  // no tile: no run saw the item, and its position has not been checked
+  if (cnt == 0 && threadIdx.x == 0) token_limit(a, z, a.hole[a.kv_row0 + z], true);
+  // a run's second partial is of an item that begins inside it
+  auto part = [&](int c, int i) {
+    c += c0;
+    return a.parts + (((size_t)c * 2 + (s > (long long)c * runs.per)) * nq_tile + i) * (D + kAttn4PartHead);
+  };
+  const float sink = a.sink ? a.sink[head] * 1.4426950408889634f : -INFINITY;
+  const bool track = a.wts && a.kv_rstep;
+  // maximum and sum of every query (for the weights) or of this CTA's
+  for (int i = warp; i < nq; i += 8) {
+    if (!track && i != mine) continue;
+    float m = -INFINITY, l = 0.f;  // of this lane's partials
+    for (int c = lane; c < n; c += 32) {
+      const float2 p = *reinterpret_cast<const float2*>(part(c, i));
+      const float hi = fmaxf(m, p.x);
+      l = l * part_factor(m, l, hi) + p.y * part_factor(p.x, p.y, hi);
+      m = hi;
     }
-    if (i < nq) {
-      float* o = s_acc + ((size_t)warp * NQ + i) * D + g * (D / 8);
+    float M = m;
 #pragma unroll
-      for (int x = 0; x < D / 16; ++x) {
-        o[2 * x] = acc[nt][x][0] + acc[nt][x][1];
-        o[2 * x + 1] = acc[nt][x][2] + acc[nt][x][3];
-      }
-    }
+    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    M = fmaxf(M, sink);
+    float L = l * part_factor(m, l, M);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+    if (a.sink) L += ex2(sink - M);
+    if (lane == 0) s_fin[i] = make_float2(M, L == 0.f ? 0.f : 1.f / L);
   }
   __syncthreads();
-  // the CTA's partial of each query: maximum, sum, weighted values
-  for (int i = warp; i < nq; i += NW) {
-    float M = -INFINITY;
+  const float2 fin = s_fin[mine];
+  float v[8];
 #pragma unroll
-    for (int w = 0; w < NW; ++w) M = fmaxf(M, s_m[w][i]);
-    float f[NW], L = 0.f;
+  for (int k = 0; k < 8; ++k) v[k] = 0.f;
+  for (int b = 0; b < n; b += CAP) {
+    if (b + threadIdx.x < n && threadIdx.x < CAP) {
+      const float2 p = *reinterpret_cast<const float2*>(part(b + threadIdx.x, mine));
+      s_f[threadIdx.x] = part_factor(p.x, p.y, fin.x);
+    }
+    __syncthreads();
+#pragma unroll 4
+    for (int c = warp; c < min(CAP, n - b); c += 8) {
+      const float* p = part(b + c, mine) + kAttn4PartHead;
+      const float f = s_f[c];
 #pragma unroll
-    for (int w = 0; w < NW; ++w) {  // a warp without a finite maximum has summed nothing, or NaN
-      f[w] = s_m[w][i] == -INFINITY ? (s_l[w][i] == 0.f ? 0.f : 1.f) : ex2(s_m[w][i] - M);
-      L += s_l[w][i] * f[w];
+      for (int k = 0; k < 8; ++k)
+        if (32 * k < D) v[k] += p[lane + 32 * k] * f;
     }
-    for (int d = lane; d < D; d += 32) {
-      float v = 0.f;
-#pragma unroll
-      for (int w = 0; w < NW; ++w) v += s_acc[((size_t)w * NQ + i) * D + d] * f[w];
-      s_part[i][2 + d] = v;
-    }
-    if (lane == 0) {
-      s_part[i][0] = M;
-      s_part[i][1] = L;
-    }
-  }
-  // the splits' partials meet through the cluster's shared memory; every CTA
-  // writes a slice of the output
-  namespace cg = cooperative_groups;
-  cg::cluster_group cluster = cg::this_cluster();
-  const int ns = gridDim.x;
-  if (ns > 1) {
-    cluster.sync();
-  } else {
     __syncthreads();
   }
-  auto part = [&](int sp, int i) { return ns > 1 ? cluster.map_shared_rank(&s_part[i][0], sp) : &s_part[i][0]; };
-  const float sink = a.sink ? a.sink[head] * 1.4426950408889634f : -INFINITY;
-  for (int i = warp; i < nq; i += NW) {
-    float M = sink;
-    for (int sp = 0; sp < ns; ++sp) M = fmaxf(M, part(sp, i)[0]);
-    float L = a.sink ? ex2(sink - M) : 0.f;
-    auto factor = [&](const float* pp) {
-      return pp[0] == -INFINITY ? (pp[1] == 0.f ? 0.f : 1.f) : ex2(pp[0] - M);
-    };
-    for (int sp = 0; sp < ns; ++sp) L += part(sp, i)[1] * factor(part(sp, i));
-    const float inv = L == 0.f ? 0.f : 1.f / L;  // nothing to read: zeros
-    const int d1 = (split + 1) * D / ns;
-    for (int d = split * D / ns + lane; d < d1; d += 32) {
-      float v = 0.f;
-      for (int sp = 0; sp < ns; ++sp) v += part(sp, i)[2 + d] * factor(part(sp, i));
-      store_elem(a.out, a.out_dtype, (long long)q_index(i) * D + d, v * inv);
-    }
-    if (lane == 0) {
-      s_fin[i] = make_float2(M, inv);
-      if (a.lse && split == 0) a.lse[q_index(i)] = s_fin[i];
-    }
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    if (32 * k < D) s_acc[warp][lane + 32 * k] = v[k];
+  __syncthreads();
+  const long long qi = (long long)((u0 + mine) / G) * a.q_heads + head * G + (u0 + mine) % G;
+  for (int d = threadIdx.x; d < D; d += blockDim.x) {
+    float o = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) o += s_acc[w][d];
+    store_elem(a.out, a.out_dtype, qi * D + d, o * fin.y);
   }
-  if (ns > 1) cluster.sync();  // a CTA keeps its partial until all slices are merged
-  if (a.wts && a.kv_rstep) {
-    // this CTA alone has these slots of the row: add its queries' weights in order
-    __syncthreads();
-    float* wt = a.wts + ((size_t)row * a.nh + head) * a.tiles * kKv4Slots;
-    for (int x = threadIdx.x; x < (j1 - j0) * 16; x += NW * 32) {
-      const int slot = tiles(j0 + (x >> 4)) * 16 + (x & 15);
-      float add = 0.f;
-      for (int i = 0; i < nq; ++i)
-        add += ex2(a.scores[q_index(i) * (size_t)a.tiles * kKv4Slots + slot] - s_fin[i].x) * s_fin[i].y;
-      if (add != 0.f) wt[slot] += add;
-    }
-  }
+  if (a.lse && threadIdx.x == 0) a.lse[qi] = fin;
+  if (!track) return;
+  const int row = a.kv_row0 + z;
+  const int2 hole = a.hole[row];
+  const TileList tiles(token_limit(a, z, hole, false), hole);
+  add_weights(a, z, head, row, tiles, nq, s_fin, mine * 256 + threadIdx.x, nq * 256);
 }
 
 // The weights of a chunk's queries, which several CTAs hold: one thread per
@@ -935,40 +1183,40 @@ __global__ void k_kv4_track(const Kv4AttnArgs a, int tokens) {
 }
 
 template <int D, int NT>
-static cudaError_t launch_attn4(const Kv4AttnArgs& a, int tokens, int nsplit, cudaStream_t st, bool pdl) {
-  constexpr int part = kAttn4Warps * 4 * NT * D * 4, ring = kAttn4Warps * Attn4<D>::RING;
-  const int queries = tokens * (a.q_heads / a.nh);
-  const int z = a.kv_rstep ? tokens : (queries + 4 * NT - 1) / (4 * NT);
-  return launch_kernel_cluster(k_kv4_attn<D, NT>, dim3(nsplit, a.nh, z), dim3(kAttn4Warps * 32),
-                               (size_t)(part > ring ? part : ring), st, pdl, nsplit, a, queries);
-}
-
-template <int NT>
-static cudaError_t launch_attn4(const Kv4AttnArgs& a, int tokens, int nsplit, cudaStream_t st, bool pdl) {
-  switch (a.D) {
-    case 32: return launch_attn4<32, NT>(a, tokens, nsplit, st, pdl);
-    case 64: return launch_attn4<64, NT>(a, tokens, nsplit, st, pdl);
-    case 128: return launch_attn4<128, NT>(a, tokens, nsplit, st, pdl);
-    case 256: return launch_attn4<256, NT>(a, tokens, nsplit, st, pdl);
-  }
-  return cudaErrorInvalidValue;
+static cudaError_t launch_attn4(const Kv4AttnArgs& args, int tokens, cudaStream_t st, bool pdl) {
+  using C = Attn4<D, NT>;
+  constexpr int part = kAttn4Warps * 4 * NT * D * 4, ring = kAttn4Warps * (C::RING + C::QB);
+  Kv4AttnArgs a = args;
+  const int n_z = a.kv_rstep ? tokens : (tokens * (a.q_heads / a.nh) + 4 * NT - 1) / (4 * NT);
+  const long long items = (long long)n_z * a.nh;
+  // One item per CTA where none can have more than 16 tiles, and in a chunk of two
+  // waves of items or more (its runs would take every item to be as long as the
+  // last); else a run for every resident warp.
+  int ctas = a.n_sm * C::CPS;
+  if (ctas * kAttn4Warps * 4 * NT > kAttn4MaxParts) ctas = kAttn4MaxParts / (kAttn4Warps * 4 * NT);
+  a.n_runs = a.tiles <= 16 || (!a.kv_rstep && items >= 2LL * ctas) ? 0 : ctas * kAttn4Warps;
+  cudaError_t e = launch_kernel(k_kv4_attn<D, NT>, dim3(a.n_runs ? ctas : (unsigned)items), dim3(kAttn4Warps * 32),
+                                (size_t)(part > ring ? part : ring), st, pdl, a, tokens, n_z);
+  if (e == cudaSuccess && a.n_runs)
+    e = launch_kernel(k_kv4_merge, dim3((unsigned)items, a.kv_rstep ? a.q_heads / a.nh : 4 * NT), dim3(256), 0, st, true,
+                      a, tokens, n_z, 4 * NT);
+  if (e == cudaSuccess && a.wts && !a.kv_rstep)
+    e = launch_kernel(k_kv4_track, dim3((a.P + a.R + 127) / 128, a.nh), dim3(128), 0, st, true, a, tokens);
+  return e;
 }
 
 cudaError_t launch_kv4_attn(const Kv4AttnArgs& a, int tokens, cudaStream_t st, bool pdl) {
   if (tokens <= 0) return cudaSuccess;
   const int G = a.q_heads / a.nh;
   // a second group of four queries costs registers: only where they exist
-  const int nt = (a.kv_rstep ? G : tokens * G) > 4 ? 2 : 1;
-  // splits: enough CTAs for two on every SM, each with a tile for every warp
-  const int ctas = a.nh * (a.kv_rstep ? tokens : (tokens * G + 4 * nt - 1) / (4 * nt));
-  int ns = (2 * a.n_sm + ctas - 1) / ctas;
-  const int cap = (a.tiles + kAttn4Warps - 1) / kAttn4Warps;
-  ns = ns > cap ? cap : ns;
-  ns = ns > 8 ? 8 : ns < 1 ? 1 : ns;
-  cudaError_t e = nt == 1 ? launch_attn4<1>(a, tokens, ns, st, pdl) : launch_attn4<2>(a, tokens, ns, st, pdl);
-  if (e == cudaSuccess && a.wts && !a.kv_rstep)
-    e = launch_kernel(k_kv4_track, dim3((a.P + a.R + 127) / 128, a.nh), dim3(128), 0, st, pdl, a, tokens);
-  return e;
+  const bool two = (a.kv_rstep ? G : tokens * G) > 4;
+  switch (a.D) {
+    case 32: return two ? launch_attn4<32, 2>(a, tokens, st, pdl) : launch_attn4<32, 1>(a, tokens, st, pdl);
+    case 64: return two ? launch_attn4<64, 2>(a, tokens, st, pdl) : launch_attn4<64, 1>(a, tokens, st, pdl);
+    case 128: return two ? launch_attn4<128, 2>(a, tokens, st, pdl) : launch_attn4<128, 1>(a, tokens, st, pdl);
+    case 256: return two ? launch_attn4<256, 2>(a, tokens, st, pdl) : launch_attn4<256, 1>(a, tokens, st, pdl);
+  }
+  return cudaErrorInvalidValue;
 }
 
 // ------------------------------------------------------------------ eviction

@@ -673,3 +673,38 @@ def test_repeated_calls_are_bit_identical(cuda):
     for r in runs[1:]:
         assert all(np.array_equal(u, v) for u, v in zip(r, runs[0]))
     ctx.close()
+
+
+@pytest.mark.parametrize("dim,group", [(32, 1), (64, 5), (128, 1), (128, 4), (256, 8)])
+def test_rows_of_very_different_lengths(cuda, dim, group):
+    """Rows from one slot to thousands, some of them evicted to almost nothing, in one call: work is shared out by
+    length, so that a row is read by one reader or by many."""
+    torch = cuda
+    rng = np.random.default_rng(dim)
+    P, R = 1500, 40
+    cfg = _cfg(head_dim=dim, n_heads=2, prefix_len=P, ring_len=R, max_rows=24, kv_track=1)
+    ctx = binding.Context(cfg, max_rows=24)
+    vals = _fill(ctx, cfg, rng)[0]
+    holes = [(0, 0)] * 24
+    w = rng.random((24, 2, P + R)).astype(np.float32)
+    _put_weights(torch, ctx, w)
+    w = w.astype(np.float64)
+    for r, keep in ((3, 0), (4, 1), (11, 17), (23, 0)):
+        _evict(torch, ctx, cfg, 0, [r], [r], P, keep, 0, vals=False)
+        for h in range(2):
+            at = oracle.evict_choice(w[r, h], P, keep, 0)
+            vals[r, :, h, :keep] = vals[r][:, h, at]
+            w[r, h, :keep] = w[r, h, at]
+            w[r, h, keep:P] = 0
+        holes[r] = (keep, P)
+    for rows in (24, 5, 1):
+        pos = [int(p) for p in rng.integers(0, P + 200, 24)]
+        pos[0], pos[1], pos[2], pos[5], pos[6] = 1200, 0, 15, 16, P + 3 * R
+        for r in (3, 4, 11, 23):
+            pos[r] = P + int(rng.integers(0, R))
+        q = rng.standard_normal((rows, 2 * group, dim)).astype(np.float32) * 2
+        want, add = oracle.attend_kv4(q, vals[:, 0], vals[:, 1], pos, P, R, holes)
+        _close(_attend(torch, ctx, cfg, q, pos[:rows]), want, 0)
+        w += add
+    _close(_weights(torch, ctx, cfg), w, 0)
+    ctx.close()
