@@ -2,6 +2,8 @@
 // entries, and the eviction of the entries that attention uses least.
 #include <math.h>
 
+#include <type_traits>
+
 #include "kv4_common.cuh"
 #include "launch.h"
 
@@ -400,22 +402,30 @@ cudaError_t launch_kv4_io(const Kv4IoArgs& a, cudaStream_t st) {
   return cudaGetLastError();
 }
 
+template <bool WIDE>
 __global__ void k_kv4_weights(const Kv4WeightsArgs a) {
   const int head = blockIdx.y % a.nh, r = blockIdx.y / a.nh, l = blockIdx.z;
   float* w = a.wts + (((size_t)(a.layer0 + l) * a.MR + a.row0 + r) * a.nh + head) * a.tiles * kKv4Slots + a.slot0;
   float* d = a.dense + (((size_t)l * a.rows + r) * a.nh + head) * a.n;
-  for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < a.n; i += gridDim.x * blockDim.x) {
-    if (a.put)
-      w[i] = d[i];
-    else
-      d[i] = w[i];
+  float* to = a.put ? w : d;
+  const float* from = a.put ? d : w;
+  if constexpr (WIDE) {
+    for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < a.n / 4; i += gridDim.x * blockDim.x)
+      reinterpret_cast<float4*>(to)[i] = reinterpret_cast<const float4*>(from)[i];
+  } else {
+    for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < a.n; i += gridDim.x * blockDim.x) to[i] = from[i];
   }
 }
 
 cudaError_t launch_kv4_weights(const Kv4WeightsArgs& a, cudaStream_t st) {
   if (a.n <= 0) return cudaSuccess;
+  const bool wide = (uintptr_t)a.dense % 16 == 0 && a.n % 4 == 0 && a.slot0 % 4 == 0;
   const int gx = (a.n + 1023) / 1024;
-  k_kv4_weights<<<dim3(gx < 64 ? gx : 64, a.rows * a.nh, a.layers), 256, 0, st>>>(a);
+  const dim3 grid(gx < 64 ? gx : 64, a.rows * a.nh, a.layers);
+  if (wide)
+    k_kv4_weights<true><<<grid, 256, 0, st>>>(a);
+  else
+    k_kv4_weights<false><<<grid, 256, 0, st>>>(a);
   return cudaGetLastError();
 }
 
@@ -443,7 +453,8 @@ cudaError_t launch_kv4_weights(const Kv4WeightsArgs& a, cudaStream_t st) {
 // The work of a call is the list of its items' tiles, an item being one (row,
 // head) or one (tile of a chunk's tokens, head).  It is cut into equal runs, one
 // for each warp that fits on the GPU at once, whatever the rows' lengths: a warp
-// goes through its run item by item and meets no barrier.  It finishes an item
+// goes through its run item by item and meets no barrier (but where one item
+// spans all four runs of a CTA, which then leave one partial).  It finishes an item
 // that lies in its run; of the first and the last, which it shares with its
 // neighbours, it leaves a partial (maximum, sum, weighted values), and a second,
 // small kernel merges those in order.  Items of a few tiles, and the many items
@@ -458,9 +469,21 @@ struct Attn4 {
   static constexpr int TILE = 32 * (2 * CB + KPB + 16);
   // tiles of a warp's step (two independent product chains where the registers
   // allow), steps in its ring, CTAs per SM
+#ifdef A4U
+  static constexpr int U = D * NT <= 128 ? A4U : 1;
+#else
   static constexpr int U = D * NT <= 128 ? 2 : 1;
+#endif
+#ifdef A4S
+  static constexpr int ST = D * NT <= 128 ? A4S : 3;
+#else
   static constexpr int ST = U == 2 || D == 256 ? 3 : 4;
+#endif
+#ifdef A4C
+  static constexpr int CPS = D * NT <= 64 ? A4C + 1 : D * NT <= 128 ? A4C : 2;
+#else
   static constexpr int CPS = D * NT <= 64 ? 4 : D * NT <= 128 ? 3 : 2;
+#endif
   static constexpr int RING = ST * U * TILE;
   static constexpr bool QREG = D * NT <= 256;  // query fragments in registers, else in shared memory
   static constexpr int QB = QREG ? 0 : NT * (D / 16) * 32 * 8;
@@ -575,10 +598,21 @@ __device__ __forceinline__ long long attn4_runs(const Kv4AttnArgs& a, int tokens
   return total;
 }
 
-// What a partial's sum counts for under the maximum M; one without a finite
-// maximum has summed nothing, or NaN.
-__device__ __forceinline__ float part_factor(float m, float l, float M) {
-  return m == -INFINITY ? (l == 0.f ? 0.f : 1.f) : ex2(m - M);
+// The running maximum before any score: low enough that the first one raises it,
+// and finite, so that masked scores (-infinity) weigh nothing under it.
+constexpr float kNoMax = -1e30f;
+
+__device__ __forceinline__ void cp_async16u(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async8u(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void lds128u(uint32_t p, uint32_t& x, uint32_t& y, uint32_t& z, uint32_t& w) {
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(x), "=r"(y), "=r"(z), "=r"(w) : "r"(p) : "memory");
+}
+__device__ __forceinline__ void lds64u(uint32_t p, uint32_t& x, uint32_t& y) {
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(x), "=r"(y) : "r"(p) : "memory");
 }
 
 // Add the softmax weights that a row's queries gave to a head's slots, query by
@@ -622,12 +656,14 @@ __global__ void __launch_bounds__(kAttn4Warps * 32, Attn4<D, NT>::CPS) k_kv4_att
   Attn4Runs runs;
   long long at, end;
   int z = 0, head = 0;
+  bool one_item = false;
   if (a.n_runs) {
     const long long total = attn4_runs(a, tokens, n_z, s_cum, runs);
     at = (long long)run * runs.per;
     end = min(total, at + runs.per);
-    if (at >= end) return;  // no barrier follows in this mode
-    if (runs.cum) {
+    if (at >= end) {
+      z = tokens - 1;  // past the list
+    } else if (runs.cum) {
       int lo = 0, hi = tokens;  // the row that holds tile `at`: the last with start <= at
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -640,6 +676,11 @@ __global__ void __launch_bounds__(kAttn4Warps * 32, Attn4<D, NT>::CPS) k_kv4_att
       z = (int)(item / a.nh);
       head = (int)(item - (long long)z * a.nh);
     }
+    // does the CTA's first run's item span all four?  (Then they meet in it, else
+    // no barrier follows.)
+    const long long s = runs.start(z, head), cta = (long long)blockIdx.x * NW * runs.per;
+    one_item = __syncthreads_and(at < end && s <= cta && s + runs.tiles(z) >= cta + NW * runs.per);
+    if (at >= end) return;
   } else {  // one item per CTA
     z = blockIdx.x / a.nh;
     head = blockIdx.x - z * a.nh;
@@ -649,9 +690,13 @@ __global__ void __launch_bounds__(kAttn4Warps * 32, Attn4<D, NT>::CPS) k_kv4_att
   }
 
   unsigned char* ring = smem + warp * (C::RING + C::QB);
+  const uint32_t ring_u = smem_u32(ring);
   uint2* s_q = reinterpret_cast<uint2*>(ring + C::RING);
+  constexpr int LB = D == 32 ? 8 : 16;            // bytes of a lane's piece of the codes
+  constexpr int KP = 64 * C::CB, VP = KP + 32 * C::KPB;  // parameters in a ring slot
   const int kp_off = 8 * D + (D == 256 ? g * 64 + t * 16 : (g * C::NG + t * C::NG / 4) * 8);
   const int vp_off = 8 * D + ((g * D / 256) * 4 + t) * 16;
+  const size_t v_off = (size_t)a.nh * a.tiles * kv4_tile_bytes(D);
 
   for (int piece = 0; at < end; ++piece) {
     // ---- the item: its row, queries (u = token * G + head in the group) and tiles
@@ -679,29 +724,31 @@ __global__ void __launch_bounds__(kAttn4Warps * 32, Attn4<D, NT>::CPS) k_kv4_att
       at = end;
     }
     const uint8_t* kt = a.kv4 + ((size_t)row * 2 * a.nh + head) * a.tiles * kv4_tile_bytes(D);
-    const uint8_t* vt = kt + (size_t)a.nh * a.tiles * kv4_tile_bytes(D);
+    // tiles [0, n_full) are read whole by every query, and lie in order
+    const int n_full = min(min(lim_lo, hole.y > hole.x ? hole.x : lim_lo) >> 4, j1);
     auto issue = [&](int j, int stage) {
+      const uint32_t d = ring_u + stage * (U * C::TILE);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         if (j + u < j1) {
-          const size_t off = (size_t)tiles(j + u) * kv4_tile_bytes(D);
-          unsigned char* d = ring + (stage * U + u) * C::TILE;
-          const uint8_t *kp = kt + off, *vp = vt + off;
+          const uint8_t* k = kt + (size_t)tiles(j + u) * kv4_tile_bytes(D);
+          const uint8_t *kc = k + lane * LB, *vc = kc + v_off, *kp = k + kp_off, *vp = k + v_off + vp_off;
+          const uint32_t du = d + u * C::TILE, dc = du + lane * LB;
           if constexpr (D == 32) {
-            cp_async8(d + lane * 8, kp + lane * 8);
-            cp_async8(d + 32 * C::CB + lane * 8, vp + lane * 8);
+            cp_async8u(dc, kc);
+            cp_async8u(dc + 32 * C::CB, vc);
           } else {
 #pragma unroll
             for (int p = 0; p < C::CB / 16; ++p) {
-              cp_async16(d + p * 512 + lane * 16, kp + p * 512 + lane * 16);
-              cp_async16(d + 32 * C::CB + p * 512 + lane * 16, vp + p * 512 + lane * 16);
+              cp_async16u(dc + p * 512, kc + p * 512);
+              cp_async16u(dc + 32 * C::CB + p * 512, vc + p * 512);
             }
           }
           if constexpr (C::KPB == 16)
-            cp_async16(d + 64 * C::CB + lane * 16, kp + kp_off);
+            cp_async16u(du + KP + lane * 16, kp);
           else
-            cp_async8(d + 64 * C::CB + lane * 8, kp + kp_off);
-          cp_async16(d + 64 * C::CB + 32 * C::KPB + lane * 16, vp + vp_off);
+            cp_async8u(du + KP + lane * 8, kp);
+          cp_async16u(du + VP + lane * 16, vp);
         }
       }
       cp_commit();
@@ -717,35 +764,43 @@ __global__ void __launch_bounds__(kAttn4Warps * 32, Attn4<D, NT>::CPS) k_kv4_att
     float* so[NT];  // this lane's query in the scores' scratch
     float* s_sq = reinterpret_cast<float*>(ring + (ST - 1) * U * C::TILE);  // [4][D]
     static_assert(U * C::TILE >= 16 * D, "four queries fit a ring slot");
+    int tok = u0 / G, rem = u0 - tok * G;  // token and head in the group of the next query
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      float mine = 0.f;
+      cq[nt] = 0.f;
+      lim_q[nt] = 0;
+      so[nt] = nullptr;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int u = u0 + 4 * nt + i;
-        const bool have = 4 * nt + i < nq;
-        float mx = 0.f, x[D / 32];
+        float x[D / 32];
+        if (4 * nt + i >= nq) {
+#pragma unroll
+          for (int k = 0; k < D / 32; ++k) s_sq[i * D + lane + 32 * k] = 0.f;
+          continue;
+        }
+        const size_t qi = (size_t)tok * a.q_heads + head * G + rem;
+        float mx = 0.f;
 #pragma unroll
         for (int k = 0; k < D / 32; ++k) {
-          x[k] = have ? a.q[((size_t)(u / G) * a.q_heads + head * G + u % G) * D + lane + 32 * k] : 0.f;
+          x[k] = a.q[qi * D + lane + 32 * k];
           mx = fmaxf(mx, fabsf(x[k]));
         }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        // 2^-e with e the exponent of the largest magnitude (0 and infinities stay)
-        const int e = mx > 0.f && mx < INFINITY ? min(max(ilogbf(mx), -100), 100) : 0;
+        // 2^-e with e the exponent of the largest magnitude (0 and infinities stay);
+        // magnitudes order as their bits
+        mx = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)));
+        const int e = mx > 0.f && mx < INFINITY ? min(max((int)(__float_as_uint(mx) >> 23) - 127, -100), 100) : 0;
         const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-        if (t == i) mine = a.scale * 1.4426950408889634f * __uint_as_float((uint32_t)(127 + e) << 23);
+        if (t == i) {
+          cq[nt] = a.scale * 1.4426950408889634f * __uint_as_float((uint32_t)(127 + e) << 23);
+          lim_q[nt] = token_limit(a, tok, hole, g == 0);
+          if (a.scores) so[nt] = a.scores + qi * a.tiles * kKv4Slots + g;
+        }
 #pragma unroll
         for (int k = 0; k < D / 32; ++k) s_sq[i * D + lane + 32 * k] = x[k] * down;
-      }
-      cq[nt] = mine;
-      {
-        const int i = 4 * nt + t, tok = (u0 + i) / G;
-        lim_q[nt] = i < nq ? token_limit(a, tok, hole, g == 0) : 0;
-        so[nt] = a.scores && i < nq
-                     ? a.scores + ((size_t)tok * a.q_heads + head * G + (u0 + i) % G) * a.tiles * kKv4Slots + g
-                     : nullptr;
+        if (++rem == G) {
+          rem = 0;
+          ++tok;
+        }
       }
       __syncwarp();
 #pragma unroll
@@ -768,7 +823,7 @@ __global__ void __launch_bounds__(kAttn4Warps * 32, Attn4<D, NT>::CPS) k_kv4_att
     float m_ref[NT], l[NT], acc[NT][D / 16][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      m_ref[nt] = -INFINITY;
+      m_ref[nt] = kNoMax;
       l[nt] = 0.f;
 #pragma unroll
       for (int i = 0; i < D / 16; ++i)
@@ -776,9 +831,11 @@ __global__ void __launch_bounds__(kAttn4Warps * 32, Attn4<D, NT>::CPS) k_kv4_att
         for (int j = 0; j < 4; ++j) acc[nt][i][j] = 0.f;
     }
     int stage = 0;
-    for (int j = first; j < j1; j += step) {
+    // One step: U tiles from j.  MASK: some slots are not read by every query.
+    auto tile_step = [&](auto mask_tag, int j) {
+      constexpr bool MASK = decltype(mask_tag)::value;
       cp_wait<ST - 2>();
-      const unsigned char* d = ring + stage * U * C::TILE;
+      const uint32_t d = ring_u + stage * (U * C::TILE);
       issue(j + (ST - 1) * step, stage == 0 ? ST - 1 : stage - 1);  // the slots that the last step left
       stage = stage == ST - 1 ? 0 : stage + 1;
 
@@ -786,35 +843,22 @@ __global__ void __launch_bounds__(kAttn4Warps * 32, Attn4<D, NT>::CPS) k_kv4_att
       float sc[U][NT][4];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) sc[u][nt][i] = 0.f;
-        const unsigned char* du = d + u * C::TILE;
+        const uint32_t du = d + u * C::TILE;
         constexpr int W = D / 32;  // words per slot
         uint32_t w[2 * W];
         if constexpr (D == 32) {
-          const uint2 v = *reinterpret_cast<const uint2*>(du + lane * 8);
-          w[0] = v.x;
-          w[1] = v.y;
+          lds64u(du + lane * 8, w[0], w[1]);
         } else {
 #pragma unroll
-          for (int p = 0; p < W / 2; ++p) {
-            const uint4 v = lds128(du + p * 512 + lane * 16);
-            w[4 * p] = v.x;
-            w[4 * p + 1] = v.y;
-            w[4 * p + 2] = v.z;
-            w[4 * p + 3] = v.w;
-          }
+          for (int p = 0; p < W / 2; ++p) lds128u(du + p * 512 + lane * 16, w[4 * p], w[4 * p + 1], w[4 * p + 2], w[4 * p + 3]);
         }
         // (s, m) of slots g and g + 8, one or two groups
         uint32_t par[4];
         if constexpr (C::KPB == 16) {
-          const uint4 v = lds128(du + 64 * C::CB + lane * 16);
-          par[0] = v.x, par[1] = v.y, par[2] = v.z, par[3] = v.w;
+          lds128u(du + KP + lane * 16, par[0], par[1], par[2], par[3]);
         } else {
-          const uint2 v = *reinterpret_cast<const uint2*>(du + 64 * C::CB + lane * 8);
-          par[0] = v.x, par[1] = v.y, par[2] = v.x, par[3] = v.y;
+          lds64u(du + KP + lane * 8, par[0], par[1]);
+          par[2] = par[0], par[3] = par[1];
         }
 #pragma unroll
         for (int i = 0; i < W; ++i) {
@@ -833,31 +877,32 @@ __global__ void __launch_bounds__(kAttn4Warps * 32, Attn4<D, NT>::CPS) k_kv4_att
               b0 = s_q[(nt * (D / 16) + 2 * i) * 32 + lane];
               b1 = s_q[(nt * (D / 16) + 2 * i + 1) * 32 + lane];
             }
-            mma_16816(sc[u][nt], a0, b0.x, b0.y);
+            if (i == 0)
+              mma_16816_z(sc[u][nt], a0, b0.x, b0.y);
+            else
+              mma_16816(sc[u][nt], a0, b0.x, b0.y);
             mma_16816(sc[u][nt], a1, b1.x, b1.y);
           }
         }
       }
       // ---- softmax: lane (g, t) holds slots g and g + 8 of query t
       float p[U][NT][2];
-      bool full[U];
       int slot0[U];
       bool raise = false;
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const bool have = j + u < j1;
-        slot0[u] = have ? tiles(j + u) * 16 : 0x7FFFFF00;  // a missing second tile lies behind every limit
-        full[u] = slot0[u] + 16 <= lim_lo && (hole.y <= hole.x || slot0[u] + 16 <= hole.x || slot0[u] >= hole.y);
+        // a missing second tile lies behind every limit
+        slot0[u] = !MASK ? (j + u) * 16 : j + u < j1 ? tiles(j + u) * 16 : 0x7FFFFF00;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           p[u][nt][0] = (sc[u][nt][0] + sc[u][nt][1]) * cq[nt];
           p[u][nt][1] = (sc[u][nt][2] + sc[u][nt][3]) * cq[nt];
-          if (!full[u]) {
+          if constexpr (MASK) {
             const int s0 = slot0[u] + g, s1 = s0 + 8;
             if (s0 >= lim_q[nt] || (s0 >= hole.x && s0 < hole.y)) p[u][nt][0] = -INFINITY;
             if (s1 >= lim_q[nt] || (s1 >= hole.x && s1 < hole.y)) p[u][nt][1] = -INFINITY;
           }
-          if (so[nt] && have) {
+          if (so[nt] && (!MASK || j + u < j1)) {
             so[nt][slot0[u]] = p[u][nt][0];
             so[nt][slot0[u] + 8] = p[u][nt][1];
           }
@@ -886,78 +931,69 @@ __global__ void __launch_bounds__(kAttn4Warps * 32, Attn4<D, NT>::CPS) k_kv4_att
       for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          const float m = m_ref[nt] == -INFINITY ? 0.f : m_ref[nt];
-          const float x = ex2(p[u][nt][0] - m), y = ex2(p[u][nt][1] - m);
+          const float x = ex2(p[u][nt][0] - m_ref[nt]), y = ex2(p[u][nt][1] - m_ref[nt]);
           l[nt] += x + y;
-          // column g of the B fragment: query g / 2, its weight or the remainder
+          // each weight as a pair (fp16 value, fp16 remainder); column g of the B
+          // fragment takes the values (g even) or remainders of query g / 2
+          const uint32_t h = pack2(x, y);
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+          const uint32_t r = pack2(x - f.x, y - f.y);
+          const uint32_t px = __byte_perm(h, r, 0x5410), py = __byte_perm(h, r, 0x7632);
           const int src = 8 * t + (g >> 1);
-          const float v0 = __shfl_sync(0xffffffffu, x, src), v1 = __shfl_sync(0xffffffffu, x, src + 4);
-          const float v2 = __shfl_sync(0xffffffffu, y, src), v3 = __shfl_sync(0xffffffffu, y, src + 4);
-          const uint32_t h0 = pack2(v0, v1), h1 = pack2(v2, v3);
-          if (g & 1) {
-            const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&h0));
-            const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&h1));
-            pb[u][nt][0] = pack2(v0 - f0.x, v1 - f0.y);
-            pb[u][nt][1] = pack2(v2 - f1.x, v3 - f1.y);
-          } else {
-            pb[u][nt][0] = h0;
-            pb[u][nt][1] = h1;
-          }
+          const uint32_t v0 = __shfl_sync(0xffffffffu, px, src), v1 = __shfl_sync(0xffffffffu, px, src + 4);
+          const uint32_t v2 = __shfl_sync(0xffffffffu, py, src), v3 = __shfl_sync(0xffffffffu, py, src + 4);
+          const uint32_t sel = (g & 1) ? 0x7632u : 0x5410u;
+          pb[u][nt][0] = __byte_perm(v0, v1, sel);
+          pb[u][nt][1] = __byte_perm(v2, v3, sel);
         }
       // ---- values: slots 2t, 2t+1 (par.x, par.y) and 2t+8, 2t+9 (par.z, par.w)
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const unsigned char* du = d + u * C::TILE;
-        uint4 par = lds128(du + 64 * C::CB + 32 * C::KPB + lane * 16);
-        // slots that no query reads become zeros: their weight is zero, but an unread
-        // NaN or infinity times zero would not be
-        if (!full[u]) {
+        const uint32_t du = d + u * C::TILE;
+        uint4 par;
+        lds128u(du + VP + lane * 16, par.x, par.y, par.z, par.w);
+        if constexpr (MASK) {
+          // slots that no query reads become zeros: their weight is zero, but an
+          // unread NaN or infinity times zero would not be
           const int s = slot0[u] + 2 * t;
           auto live = [&](int x) { return x < lim_hi && !(x >= hole.x && x < hole.y); };
           const uint32_t k0 = (live(s) ? 0xFFFFu : 0u) | (live(s + 1) ? 0xFFFF0000u : 0u);
           const uint32_t k1 = (live(s + 8) ? 0xFFFFu : 0u) | (live(s + 9) ? 0xFFFF0000u : 0u);
           par.x &= k0, par.y &= k0, par.z &= k1, par.w &= k1;
-        }
-        if (!full[u] && lim_lo != lim_hi) {
-          // a slot that only some of the tile's queries read: where its group is not
-          // finite it is left out of the products, and the queries that do read it
-          // get NaN there (a lane's values of a slot all belong to one group)
-          auto odd = [](uint32_t s, uint32_t m) {
-            return (((s & 0x7C00u) == 0x7C00u || (m & 0x7C00u) == 0x7C00u) ? 1u : 0u) |
-                   (((s & 0x7C000000u) == 0x7C000000u || (m & 0x7C000000u) == 0x7C000000u) ? 2u : 0u);
-          };
-          const uint32_t b0 = odd(par.x, par.y), b1 = odd(par.z, par.w);
-          uint32_t bad = (b0 << (2 * t)) | (b1 << (2 * t + 8));
-          if (__any_sync(0xffffffffu, bad != 0u)) {
-            const uint32_t k0 = (b0 & 1 ? 0u : 0xFFFFu) | (b0 & 2 ? 0u : 0xFFFF0000u);
-            const uint32_t k1 = (b1 & 1 ? 0u : 0xFFFFu) | (b1 & 2 ? 0u : 0xFFFF0000u);
-            par.x &= k0, par.y &= k0, par.z &= k1, par.w &= k1;
-            bad |= __shfl_xor_sync(0xffffffffu, bad, 1);
-            bad |= __shfl_xor_sync(0xffffffffu, bad, 2);
+          if (lim_lo != lim_hi) {
+            // a slot that only some of the tile's queries read: where its group is not
+            // finite it is left out of the products, and the queries that do read it
+            // get NaN there (a lane's values of a slot all belong to one group)
+            auto odd = [](uint32_t s, uint32_t m) {
+              return (((s & 0x7C00u) == 0x7C00u || (m & 0x7C00u) == 0x7C00u) ? 1u : 0u) |
+                     (((s & 0x7C000000u) == 0x7C000000u || (m & 0x7C000000u) == 0x7C000000u) ? 2u : 0u);
+            };
+            const uint32_t b0 = odd(par.x, par.y), b1 = odd(par.z, par.w);
+            uint32_t bad = (b0 << (2 * t)) | (b1 << (2 * t + 8));
+            if (__any_sync(0xffffffffu, bad != 0u)) {
+              const uint32_t k0 = (b0 & 1 ? 0u : 0xFFFFu) | (b0 & 2 ? 0u : 0xFFFF0000u);
+              const uint32_t k1 = (b1 & 1 ? 0u : 0xFFFFu) | (b1 & 2 ? 0u : 0xFFFF0000u);
+              par.x &= k0, par.y &= k0, par.z &= k1, par.w &= k1;
+              bad |= __shfl_xor_sync(0xffffffffu, bad, 1);
+              bad |= __shfl_xor_sync(0xffffffffu, bad, 2);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              const int n = min(max(lim_q[nt] - slot0[u], 0), 16);  // the query reads the tile's first n slots
-              if (bad & ((1u << n) - 1u))
+              for (int nt = 0; nt < NT; ++nt) {
+                const int n = min(max(lim_q[nt] - slot0[u], 0), 16);  // the query reads the tile's first n slots
+                if (bad & ((1u << n) - 1u))
 #pragma unroll
-                for (int i = 0; i < D / 16; ++i) acc[nt][i][0] = acc[nt][i][2] = __int_as_float(0x7FFFFFFF);
+                  for (int i = 0; i < D / 16; ++i) acc[nt][i][0] = acc[nt][i][2] = __int_as_float(0x7FFFFFFF);
+              }
             }
           }
         }
         constexpr int Q = D / 32;  // words per slot pair
         uint32_t w[2 * Q];
         if constexpr (D == 32) {
-          const uint2 v = *reinterpret_cast<const uint2*>(du + 32 * C::CB + lane * 8);
-          w[0] = v.x;
-          w[1] = v.y;
+          lds64u(du + 32 * C::CB + lane * 8, w[0], w[1]);
         } else {
 #pragma unroll
-          for (int q = 0; q < Q / 2; ++q) {
-            const uint4 v = lds128(du + 32 * C::CB + q * 512 + lane * 16);
-            w[4 * q] = v.x;
-            w[4 * q + 1] = v.y;
-            w[4 * q + 2] = v.z;
-            w[4 * q + 3] = v.w;
-          }
+          for (int q = 0; q < Q / 2; ++q)
+            lds128u(du + 32 * C::CB + q * 512 + lane * 16, w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
         }
 #pragma unroll
         for (int i = 0; i < Q; ++i) {
@@ -972,7 +1008,10 @@ __global__ void __launch_bounds__(kAttn4Warps * 32, Attn4<D, NT>::CPS) k_kv4_att
           }
         }
       }
-    }
+    };
+    int j = first;
+    for (; j + U <= n_full; j += step) tile_step(std::false_type{}, j);
+    for (; j < j1; j += step) tile_step(std::true_type{}, j);
     cp_wait<0>();
 
 #pragma unroll
@@ -980,13 +1019,13 @@ __global__ void __launch_bounds__(kAttn4Warps * 32, Attn4<D, NT>::CPS) k_kv4_att
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) l[nt] += __shfl_xor_sync(0xffffffffu, l[nt], o);
     const float sink = a.sink ? a.sink[head] * 1.4426950408889634f : -INFINITY;
-    if (a.n_runs) {
+    if (a.n_runs && !one_item) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const int i = 4 * nt + t;
         if (i >= nq) continue;
         if (whole) {
-          const float M = fmaxf(m_ref[nt], sink), f = part_factor(m_ref[nt], l[nt], M);
+          const float M = fmaxf(m_ref[nt], sink), f = ex2(m_ref[nt] - M);
           const float L = l[nt] * f + (a.sink ? ex2(sink - M) : 0.f);
           const float inv = L == 0.f ? 0.f : 1.f / L, c = f * inv;  // nothing to read: zeros
           const size_t qi = (size_t)((u0 + i) / G) * a.q_heads + head * G + (u0 + i) % G;
@@ -1041,13 +1080,15 @@ __global__ void __launch_bounds__(kAttn4Warps * 32, Attn4<D, NT>::CPS) k_kv4_att
     __syncthreads();
     for (int i = warp; i < nq; i += NW) {
       const size_t qi = (size_t)((u0 + i) / G) * a.q_heads + head * G + (u0 + i) % G;
-      float M = sink;
+      // the four runs' partial, written as the first's; the others' count for nothing
+      float* part = a.parts + ((size_t)blockIdx.x * NW * 2 * NQ + i) * (D + kAttn4PartHead);
+      float M = one_item ? kNoMax : sink;
 #pragma unroll
       for (int w = 0; w < NW; ++w) M = fmaxf(M, s_m[w][i]);
-      float f[NW], L = a.sink ? ex2(sink - M) : 0.f;
+      float f[NW], L = a.sink && !one_item ? ex2(sink - M) : 0.f;
 #pragma unroll
       for (int w = 0; w < NW; ++w) {
-        f[w] = part_factor(s_m[w][i], s_l[w][i], M);
+        f[w] = ex2(s_m[w][i] - M);
         L += s_l[w][i] * f[w];
       }
       const float inv = L == 0.f ? 0.f : 1.f / L;  // nothing to read: zeros
@@ -1056,14 +1097,21 @@ __global__ void __launch_bounds__(kAttn4Warps * 32, Attn4<D, NT>::CPS) k_kv4_att
         float v = 0.f;
 #pragma unroll
         for (int w = 0; w < NW; ++w) v += s_acc[(w * NQ + i) * D + d] * f[w];
-        store_elem(a.out, a.out_dtype, (long long)(qi * D + d), v * inv);
+        if (one_item)
+          part[kAttn4PartHead + d] = v;
+        else
+          store_elem(a.out, a.out_dtype, (long long)(qi * D + d), v * inv);
       }
-      if (lane == 0) {
+      if (one_item) {
+        if (lane < NW)
+          *reinterpret_cast<float2*>(part + (size_t)lane * 2 * NQ * (D + kAttn4PartHead)) =
+              make_float2(lane ? kNoMax : M, lane ? 0.f : L);
+      } else if (lane == 0) {
         s_fin[0][i] = make_float2(M, inv);
         if (a.lse) a.lse[qi] = make_float2(M, inv);
       }
     }
-    if (a.wts && a.kv_rstep) {  // this CTA alone has the item's slots
+    if (a.wts && a.kv_rstep && !a.n_runs) {  // this CTA alone has the item's slots
       __syncthreads();
       add_weights(a, z, head, row, tiles, nq, s_fin[0], threadIdx.x, NW * 32);
     }
@@ -1093,28 +1141,29 @@ __global__ void __launch_bounds__(256) k_kv4_merge(const Kv4AttnArgs a, int toke
   if (mine >= nq || n == 1) return;  // one run's: finished there
   // no tile: no run saw the item, and its position has not been checked
   if (cnt == 0 && threadIdx.x == 0) token_limit(a, z, a.hole[a.kv_row0 + z], true);
-  // a run's second partial is of an item that begins inside it
-  auto part = [&](int c, int i) {
-    c += c0;
-    return a.parts + (((size_t)c * 2 + (s > (long long)c * runs.per)) * nq_tile + i) * (D + kAttn4PartHead);
-  };
+  // a run's second partial is of an item that begins inside it: the first run's, if any
+  const size_t step = (size_t)2 * nq_tile * (D + kAttn4PartHead);
+  const float* base = a.parts + c0 * step;
+  const int shift = s > (long long)c0 * runs.per ? (int)(step >> 1) : 0;
+  auto part = [&](int c, int i) { return base + c * step + (c ? 0 : shift) + i * (D + kAttn4PartHead); };
   const float sink = a.sink ? a.sink[head] * 1.4426950408889634f : -INFINITY;
   const bool track = a.wts && a.kv_rstep;
   // maximum and sum of every query (for the weights) or of this CTA's
   for (int i = warp; i < nq; i += 8) {
     if (!track && i != mine) continue;
-    float m = -INFINITY, l = 0.f;  // of this lane's partials
+    float m = kNoMax, l = 0.f;  // of this lane's partials
+#pragma unroll 4
     for (int c = lane; c < n; c += 32) {
       const float2 p = *reinterpret_cast<const float2*>(part(c, i));
       const float hi = fmaxf(m, p.x);
-      l = l * part_factor(m, l, hi) + p.y * part_factor(p.x, p.y, hi);
+      l = l * ex2(m - hi) + p.y * ex2(p.x - hi);
       m = hi;
     }
     float M = m;
 #pragma unroll
     for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
     M = fmaxf(M, sink);
-    float L = l * part_factor(m, l, M);
+    float L = l * ex2(m - M);
 #pragma unroll
     for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
     if (a.sink) L += ex2(sink - M);
@@ -1128,16 +1177,17 @@ __global__ void __launch_bounds__(256) k_kv4_merge(const Kv4AttnArgs a, int toke
   for (int b = 0; b < n; b += CAP) {
     if (b + threadIdx.x < n && threadIdx.x < CAP) {
       const float2 p = *reinterpret_cast<const float2*>(part(b + threadIdx.x, mine));
-      s_f[threadIdx.x] = part_factor(p.x, p.y, fin.x);
+      s_f[threadIdx.x] = ex2(p.x - fin.x);
     }
     __syncthreads();
 #pragma unroll 4
     for (int c = warp; c < min(CAP, n - b); c += 8) {
       const float* p = part(b + c, mine) + kAttn4PartHead;
       const float f = s_f[c];
+      if (f != 0.f)
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (32 * k < D) v[k] += p[lane + 32 * k] * f;
+        for (int k = 0; k < 8; ++k)
+          if (32 * k < D) v[k] += p[lane + 32 * k] * f;
     }
     __syncthreads();
   }
