@@ -139,6 +139,7 @@ struct Kv4AttnArgs {
   float2* lse;                 // scratch: [tokens][q_heads] (maximum, 1 / sum)
   float* parts;                // scratch: [runs][2][queries][kAttn4PartHead + D]
   int n_runs;                  // set by the launcher; 0: one item per CTA
+  int q_wide;                  // set by the launcher: q is 16-byte aligned
   int q_heads, nh, D, P, R, tiles;
   int kv_row0, kv_rstep;       // kv_rstep 0: every token belongs to cache row kv_row0
   int n_sm;

@@ -526,6 +526,7 @@ __device__ __forceinline__ void dequant8(uint32_t w, uint32_t s, uint32_t m, uin
 // [y, lim).
 struct TileList {
   int ta, tb, count;
+  TileList() = default;
   __device__ TileList(int lim, int2 hole) {
     const int x = min(hole.x, lim);
     const bool gap = hole.y > hole.x && lim > hole.x;
@@ -557,11 +558,18 @@ __device__ __forceinline__ int token_limit(const Kv4AttnArgs& a, int t, int2 hol
   return kv_limit(p, a.P, a.R);
 }
 
-// Fill the runs of a call (every thread of a CTA of at least 32).  cum holds
-// kKv4MaxRows + 1 entries.  Returns the number of tiles.
-__device__ __forceinline__ long long attn4_runs(const Kv4AttnArgs& a, int tokens, int n_z, int* cum, Attn4Runs& r) {
+// What the rows of a call read, for the CTAs that share it out.
+struct Attn4Rows {
+  int cum[kKv4MaxRows + 1];  // tiles of one head in the rows before
+  int lim[kKv4MaxRows];
+  int2 hole[kKv4MaxRows];
+};
+
+// Fill the runs of a call (every thread of a CTA).  Returns the number of tiles.
+__device__ __forceinline__ long long attn4_runs(const Kv4AttnArgs& a, int tokens, int n_z, Attn4Rows& rows, Attn4Runs& r) {
   r.nh = a.nh;
   r.cum = nullptr;
+  r.uniform = 0;
   long long total;
   if (a.kv_rstep) {
     if (threadIdx.x < 32) {
@@ -571,7 +579,10 @@ __device__ __forceinline__ long long attn4_runs(const Kv4AttnArgs& a, int tokens
         int c = 0;
         if (z < tokens) {
           const int2 hole = a.hole[a.kv_row0 + z];
-          c = TileList(token_limit(a, z, hole, false), hole).count;
+          const int lim = token_limit(a, z, hole, blockIdx.x == 0);
+          c = TileList(lim, hole).count;
+          rows.lim[z] = lim;
+          rows.hole[z] = hole;
         }
         int up = c;
 #pragma unroll
@@ -579,14 +590,14 @@ __device__ __forceinline__ long long attn4_runs(const Kv4AttnArgs& a, int tokens
           const int v = __shfl_up_sync(0xffffffffu, up, o);
           if (threadIdx.x >= o) up += v;
         }
-        if (z < tokens) cum[z + 1] = before + up;
+        if (z < tokens) rows.cum[z + 1] = before + up;
         before += __shfl_sync(0xffffffffu, up, 31);
       }
-      if (threadIdx.x == 0) cum[0] = 0;
+      if (threadIdx.x == 0) rows.cum[0] = 0;
     }
     __syncthreads();
-    r.cum = cum;
-    total = (long long)cum[tokens] * a.nh;
+    r.cum = rows.cum;
+    total = (long long)rows.cum[tokens] * a.nh;
   } else {  // a chunk: as many tiles for every item as its last token has
     const int2 hole = a.hole[a.kv_row0];
     r.uniform = TileList(token_limit(a, tokens - 1, hole, false), hole).count;
@@ -647,18 +658,18 @@ __global__ void __launch_bounds__(kAttn4Warps * 32, Attn4<D, NT>::CPS) k_kv4_att
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ float s_m[NW][NQ], s_l[NW][NQ];
   __shared__ float2 s_fin[NW][NQ];  // final maximum and 1 / sum, by the warp that finishes
-  __shared__ int s_cum[kKv4MaxRows + 1];
+  __shared__ Attn4Rows s_rows;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int G = a.q_heads / a.nh, run = blockIdx.x * NW + warp;
 
-  pdl_launch_dependents();
   pdl_wait();  // queries and new entries come from the previous kernels
+  pdl_launch_dependents();  // (the merge reads positions before its own wait)
   Attn4Runs runs;
   long long at, end;
   int z = 0, head = 0;
   bool one_item = false;
   if (a.n_runs) {
-    const long long total = attn4_runs(a, tokens, n_z, s_cum, runs);
+    const long long total = attn4_runs(a, tokens, n_z, s_rows, runs);
     at = (long long)run * runs.per;
     end = min(total, at + runs.per);
     if (at >= end) {
@@ -698,116 +709,130 @@ __global__ void __launch_bounds__(kAttn4Warps * 32, Attn4<D, NT>::CPS) k_kv4_att
   const int vp_off = 8 * D + ((g * D / 256) * 4 + t) * 16;
   const size_t v_off = (size_t)a.nh * a.tiles * kv4_tile_bytes(D);
 
+  // Item (z, head) from tile `at` of the list on: its tiles [j, j1) of this run.
+  struct Item {
+    const uint8_t* kt;
+    TileList tiles;
+    int2 hole;
+    int lim_lo, lim_hi, j, j1;
+    bool whole;
+  };
+  auto item_at = [&](int z, int head, long long& at) {
+    Item it;
+    const int row = a.kv_row0 + (a.kv_rstep ? z : 0);
+    if (a.n_runs && a.kv_rstep) {
+      it.hole = s_rows.hole[z];
+      it.lim_lo = it.lim_hi = s_rows.lim[z];
+    } else {
+      it.hole = a.hole[row];
+      const int u0 = a.kv_rstep ? z * G : z * NQ, nq = a.kv_rstep ? G : min(NQ, tokens * G - u0);
+      it.lim_lo = token_limit(a, u0 / G, it.hole, true);
+      it.lim_hi = a.kv_rstep ? it.lim_lo : token_limit(a, (u0 + nq - 1) / G, it.hole, false);
+    }
+    it.tiles = TileList(it.lim_hi, it.hole);
+    const int count = it.tiles.count;
+    it.kt = a.kv4 + ((size_t)row * 2 * a.nh + head) * a.tiles * kv4_tile_bytes(D);
+    if (a.n_runs) {
+      const long long s = runs.start(z, head), left = end - s;
+      const int cnt = runs.tiles(z), j0 = (int)(at - s), j1 = left < cnt ? (int)left : cnt;
+      at = s + j1;
+      it.whole = j0 == 0 && j1 == cnt;
+      it.j = min(j0, count);  // a chunk's earlier tokens have fewer
+      it.j1 = min(j1, count);
+    } else {
+      at = end;
+      it.whole = true;
+      it.j = warp * U;
+      it.j1 = count;
+    }
+    return it;
+  };
+  const int step = a.n_runs ? U : NW * U;
+  // The copies run ahead of the products by ST - 1 steps, across the items' bounds.
+  int pf_z = z, pf_head = head;
+  long long pf_at = at;
+  Item pf{};
+  if (at < end) pf = item_at(pf_z, pf_head, pf_at);
+  auto issue = [&](int stage) {
+    while (pf.j >= pf.j1 && pf_at < end) {
+      if (++pf_head == a.nh) {
+        pf_head = 0;
+        ++pf_z;
+      }
+      pf = item_at(pf_z, pf_head, pf_at);
+    }
+    const uint32_t d = ring_u + stage * (U * C::TILE);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (pf.j + u < pf.j1) {
+        const uint8_t* k = pf.kt + (size_t)pf.tiles(pf.j + u) * kv4_tile_bytes(D);
+        const uint8_t *kc = k + lane * LB, *vc = kc + v_off, *kp = k + kp_off, *vp = k + v_off + vp_off;
+        const uint32_t du = d + u * C::TILE, dc = du + lane * LB;
+        if constexpr (D == 32) {
+          cp_async8u(dc, kc);
+          cp_async8u(dc + 32 * C::CB, vc);
+        } else {
+#pragma unroll
+          for (int p = 0; p < C::CB / 16; ++p) {
+            cp_async16u(dc + p * 512, kc + p * 512);
+            cp_async16u(dc + 32 * C::CB + p * 512, vc + p * 512);
+          }
+        }
+        if constexpr (C::KPB == 16)
+          cp_async16u(du + KP + lane * 16, kp);
+        else
+          cp_async8u(du + KP + lane * 8, kp);
+        cp_async16u(du + VP + lane * 16, vp);
+      }
+    }
+    pf.j += step;
+    cp_commit();
+  };
+#pragma unroll
+  for (int k = 0; k < ST - 1; ++k) issue(k);
+  int stage = 0;
+
   for (int piece = 0; at < end; ++piece) {
-    // ---- the item: its row, queries (u = token * G + head in the group) and tiles
+    // ---- the item: its queries (u = token * G + head in the group) and tiles
     const int u0 = a.kv_rstep ? z * G : z * NQ;
     const int nq = a.kv_rstep ? G : min(NQ, tokens * G - u0);
     const int row = a.kv_row0 + (a.kv_rstep ? z : 0);
-    const int2 hole = a.hole[row];
-    const int lim_hi = token_limit(a, (u0 + nq - 1) / G, hole, false), lim_lo = token_limit(a, u0 / G, hole, false);
-    const TileList tiles(lim_hi, hole);
-    int j0 = 0, j1 = tiles.count, step = NW * U, first = warp * U;
-    bool whole = true;
-    if (a.n_runs) {
-      const long long s = runs.start(z, head);
-      const int cnt = runs.tiles(z);
-      const long long left = end - s;
-      j0 = (int)(at - s);
-      j1 = left < cnt ? (int)left : cnt;
-      at = s + j1;
-      whole = j0 == 0 && j1 == cnt;
-      j0 = min(j0, tiles.count);  // a chunk's earlier tokens have fewer
-      j1 = min(j1, tiles.count);
-      step = U;
-      first = j0;
-    } else {
-      at = end;
-    }
-    const uint8_t* kt = a.kv4 + ((size_t)row * 2 * a.nh + head) * a.tiles * kv4_tile_bytes(D);
+    const Item it = item_at(z, head, at);
+    const int2 hole = it.hole;
+    const int lim_lo = it.lim_lo, lim_hi = it.lim_hi, j1 = it.j1;
+    const bool whole = it.whole;
+    const TileList tiles = it.tiles;
     // tiles [0, n_full) are read whole by every query, and lie in order
     const int n_full = min(min(lim_lo, hole.y > hole.x ? hole.x : lim_lo) >> 4, j1);
-    auto issue = [&](int j, int stage) {
-      const uint32_t d = ring_u + stage * (U * C::TILE);
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (j + u < j1) {
-          const uint8_t* k = kt + (size_t)tiles(j + u) * kv4_tile_bytes(D);
-          const uint8_t *kc = k + lane * LB, *vc = kc + v_off, *kp = k + kp_off, *vp = k + v_off + vp_off;
-          const uint32_t du = d + u * C::TILE, dc = du + lane * LB;
-          if constexpr (D == 32) {
-            cp_async8u(dc, kc);
-            cp_async8u(dc + 32 * C::CB, vc);
-          } else {
-#pragma unroll
-            for (int p = 0; p < C::CB / 16; ++p) {
-              cp_async16u(dc + p * 512, kc + p * 512);
-              cp_async16u(dc + 32 * C::CB + p * 512, vc + p * 512);
-            }
-          }
-          if constexpr (C::KPB == 16)
-            cp_async16u(du + KP + lane * 16, kp);
-          else
-            cp_async8u(du + KP + lane * 8, kp);
-          cp_async16u(du + VP + lane * 16, vp);
-        }
-      }
-      cp_commit();
-    };
-#pragma unroll
-    for (int k = 0; k < ST - 1; ++k) issue(first + k * step, k);
 
-    // ---- queries as fp16 pairs (value, remainder), four at a time through the
-    // ring's last slots, which the first step fills only after this
+    // ---- queries as fp16 pairs (value, remainder), straight into fragments: lane
+    // (g, t) takes a quarter of query g / 2, its values (g even) or remainders
     uint2 qf[C::QREG ? NT * (D / 16) : 1];
     int lim_q[NT];
     float cq[NT];   // score factor: scale log2(e) 2^e
     float* so[NT];  // this lane's query in the scores' scratch
-    float* s_sq = reinterpret_cast<float*>(ring + (ST - 1) * U * C::TILE);  // [4][D]
-    static_assert(U * C::TILE >= 16 * D, "four queries fit a ring slot");
-    int tok = u0 / G, rem = u0 - tok * G;  // token and head in the group of the next query
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      cq[nt] = 0.f;
-      lim_q[nt] = 0;
-      so[nt] = nullptr;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float x[D / 32];
-        if (4 * nt + i >= nq) {
-#pragma unroll
-          for (int k = 0; k < D / 32; ++k) s_sq[i * D + lane + 32 * k] = 0.f;
-          continue;
-        }
-        const size_t qi = (size_t)tok * a.q_heads + head * G + rem;
-        float mx = 0.f;
-#pragma unroll
-        for (int k = 0; k < D / 32; ++k) {
-          x[k] = a.q[qi * D + lane + 32 * k];
-          mx = fmaxf(mx, fabsf(x[k]));
-        }
-        // 2^-e with e the exponent of the largest magnitude (0 and infinities stay);
-        // magnitudes order as their bits
-        mx = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)));
-        const int e = mx > 0.f && mx < INFINITY ? min(max((int)(__float_as_uint(mx) >> 23) - 127, -100), 100) : 0;
-        const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-        if (t == i) {
-          cq[nt] = a.scale * 1.4426950408889634f * __uint_as_float((uint32_t)(127 + e) << 23);
-          lim_q[nt] = token_limit(a, tok, hole, g == 0);
-          if (a.scores) so[nt] = a.scores + qi * a.tiles * kKv4Slots + g;
-        }
-#pragma unroll
-        for (int k = 0; k < D / 32; ++k) s_sq[i * D + lane + 32 * k] = x[k] * down;
-        if (++rem == G) {
-          rem = 0;
-          ++tok;
-        }
-      }
-      __syncwarp();
+      const int i = 4 * nt + (g >> 1), tok = a.kv_rstep ? z : (u0 + i) / G;
+      const size_t qi = (size_t)tok * a.q_heads + head * G + (u0 + i - tok * G);
+      float4 q4[D / 16];
+      float mx = 0.f;
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
         // step k covers dimensions 4k .. 4k+3 of every lane's quarter
-        const float4 q4 = *reinterpret_cast<const float4*>(s_sq + (g >> 1) * D + t * (D / 4) + 4 * k);
-        float v[4] = {q4.x, q4.y, q4.z, q4.w};
+        const float* qp = a.q + qi * D + t * (D / 4) + 4 * k;
+        q4[k] = i >= nq ? make_float4(0.f, 0.f, 0.f, 0.f)
+                : a.q_wide ? *reinterpret_cast<const float4*>(qp) : make_float4(qp[0], qp[1], qp[2], qp[3]);
+        mx = fmaxf(mx, fmaxf(fmaxf(fabsf(q4[k].x), fabsf(q4[k].y)), fmaxf(fabsf(q4[k].z), fabsf(q4[k].w))));
+      }
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      // 2^-e with e the exponent of the largest magnitude (0 and infinities stay)
+      const int e = mx > 0.f && mx < INFINITY ? min(max((int)(__float_as_uint(mx) >> 23) - 127, -100), 100) : 0;
+      const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        float v[4] = {q4[k].x * down, q4[k].y * down, q4[k].z * down, q4[k].w * down};
         if (g & 1)
 #pragma unroll
           for (int j = 0; j < 4; ++j) v[j] -= __half2float(__float2half_rn(v[j]));
@@ -817,7 +842,14 @@ __global__ void __launch_bounds__(kAttn4Warps * 32, Attn4<D, NT>::CPS) k_kv4_att
         else
           s_q[(nt * (D / 16) + k) * 32 + lane] = f;  // read by this lane alone
       }
-      __syncwarp();
+      // the lane's own query t: its factor from a lane that holds query t
+      const float c = a.scale * 1.4426950408889634f * __uint_as_float((uint32_t)(127 + e) << 23);
+      cq[nt] = __shfl_sync(0xffffffffu, c, 8 * t);
+      const int m = 4 * nt + t, mtok = a.kv_rstep ? z : (u0 + m) / G;
+      lim_q[nt] = m < nq ? (a.kv_rstep ? lim_hi : token_limit(a, mtok, hole, false)) : 0;
+      so[nt] = a.scores && m < nq
+                   ? a.scores + ((size_t)mtok * a.q_heads + head * G + (u0 + m - mtok * G)) * a.tiles * kKv4Slots + g
+                   : nullptr;
     }
 
     float m_ref[NT], l[NT], acc[NT][D / 16][4];
@@ -830,13 +862,12 @@ __global__ void __launch_bounds__(kAttn4Warps * 32, Attn4<D, NT>::CPS) k_kv4_att
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[nt][i][j] = 0.f;
     }
-    int stage = 0;
     // One step: U tiles from j.  MASK: some slots are not read by every query.
     auto tile_step = [&](auto mask_tag, int j) {
       constexpr bool MASK = decltype(mask_tag)::value;
       cp_wait<ST - 2>();
       const uint32_t d = ring_u + stage * (U * C::TILE);
-      issue(j + (ST - 1) * step, stage == 0 ? ST - 1 : stage - 1);  // the slots that the last step left
+      issue(stage == 0 ? ST - 1 : stage - 1);  // into the slots that the last step left
       stage = stage == ST - 1 ? 0 : stage + 1;
 
       // ---- scores
@@ -1009,11 +1040,9 @@ __global__ void __launch_bounds__(kAttn4Warps * 32, Attn4<D, NT>::CPS) k_kv4_att
         }
       }
     };
-    int j = first;
+    int j = it.j;
     for (; j + U <= n_full; j += step) tile_step(std::false_type{}, j);
     for (; j < j1; j += step) tile_step(std::true_type{}, j);
-    cp_wait<0>();
-
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -1059,6 +1088,7 @@ __global__ void __launch_bounds__(kAttn4Warps * 32, Attn4<D, NT>::CPS) k_kv4_att
       __syncwarp();
       continue;
     }
+    cp_wait<0>();
     __syncthreads();  // the rings are free: they take the warps' partials
     float* s_acc = reinterpret_cast<float*>(smem);  // [NW][NQ][D]
 #pragma unroll
@@ -1123,24 +1153,22 @@ __global__ void __launch_bounds__(kAttn4Warps * 32, Attn4<D, NT>::CPS) k_kv4_att
 // are then independent loads, so that the time is a few trips to the L2.
 __global__ void __launch_bounds__(256) k_kv4_merge(const Kv4AttnArgs a, int tokens, int n_z, int nq_tile) {
   constexpr int CAP = 256;  // partials whose factors are held at a time
-  __shared__ int s_cum[kKv4MaxRows + 1];
+  __shared__ Attn4Rows s_rows;
   __shared__ float2 s_fin[8];
   __shared__ float s_f[CAP];
   __shared__ float s_acc[8][256];
-  pdl_launch_dependents();
-  pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, D = a.D, G = a.q_heads / a.nh;
   const int head = blockIdx.x % a.nh, z = blockIdx.x / a.nh, mine = blockIdx.y;
   Attn4Runs runs;
-  attn4_runs(a, tokens, n_z, s_cum, runs);
+  attn4_runs(a, tokens, n_z, s_rows, runs);  // positions and holes: written before the attention began
+  pdl_launch_dependents();
+  pdl_wait();
   const int cnt = runs.tiles(z);
   const long long s = runs.start(z, head);
   const int u0 = a.kv_rstep ? z * G : z * nq_tile;
   const int nq = a.kv_rstep ? G : min(nq_tile, tokens * G - u0);
   const int c0 = (int)(s / runs.per), n = cnt ? (int)((s + cnt - 1) / runs.per) - c0 + 1 : 0;
   if (mine >= nq || n == 1) return;  // one run's: finished there
-  // no tile: no run saw the item, and its position has not been checked
-  if (cnt == 0 && threadIdx.x == 0) token_limit(a, z, a.hole[a.kv_row0 + z], true);
   // a run's second partial is of an item that begins inside it: the first run's, if any
   const size_t step = (size_t)2 * nq_tile * (D + kAttn4PartHead);
   const float* base = a.parts + c0 * step;
@@ -1204,10 +1232,8 @@ __global__ void __launch_bounds__(256) k_kv4_merge(const Kv4AttnArgs a, int toke
   }
   if (a.lse && threadIdx.x == 0) a.lse[qi] = fin;
   if (!track) return;
-  const int row = a.kv_row0 + z;
-  const int2 hole = a.hole[row];
-  const TileList tiles(token_limit(a, z, hole, false), hole);
-  add_weights(a, z, head, row, tiles, nq, s_fin, mine * 256 + threadIdx.x, nq * 256);
+  const TileList tiles(s_rows.lim[z], s_rows.hole[z]);
+  add_weights(a, z, head, a.kv_row0 + z, tiles, nq, s_fin, mine * 256 + threadIdx.x, nq * 256);
 }
 
 // The weights of a chunk's queries, which several CTAs hold: one thread per
@@ -1237,6 +1263,7 @@ static cudaError_t launch_attn4(const Kv4AttnArgs& args, int tokens, cudaStream_
   using C = Attn4<D, NT>;
   constexpr int part = kAttn4Warps * 4 * NT * D * 4, ring = kAttn4Warps * (C::RING + C::QB);
   Kv4AttnArgs a = args;
+  a.q_wide = (uintptr_t)a.q % 16 == 0;
   const int n_z = a.kv_rstep ? tokens : (tokens * (a.q_heads / a.nh) + 4 * NT - 1) / (4 * NT);
   const long long items = (long long)n_z * a.nh;
   // One item per CTA where none can have more than 16 tiles, and in a chunk of two

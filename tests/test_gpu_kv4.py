@@ -708,3 +708,42 @@ def test_rows_of_very_different_lengths(cuda, dim, group):
         w += add
     _close(_weights(torch, ctx, cfg), w, 0)
     ctx.close()
+
+
+@pytest.mark.parametrize("dim", [32, 128])
+def test_buffers_aligned_to_their_elements_only(cuda, dim):
+    """Inputs and outputs one element past a 16-byte boundary give what aligned ones give, bit for bit."""
+    torch = cuda
+    cfg = _cfg(head_dim=dim, n_heads=2, prefix_len=50, ring_len=9, max_rows=2, kv_track=1)
+    rng = np.random.default_rng(dim)
+
+    def off(x):  # a copy that starts one element past an aligned address
+        b = torch.empty(x.numel() + 1, dtype=x.dtype, device="cuda")
+        b[1:].copy_(x.reshape(-1))
+        return b[1:]
+
+    for dtype in (0, 1, 2):
+        got = []
+        x = [torch.from_numpy(rng.standard_normal((21, h, dim)).astype(np.float32)).to(_dt(torch, dtype)).cuda() for h in (4, 2, 2)]
+        for shift in (lambda v: v, off):
+            ctx = binding.Context(cfg, max_rows=2)
+            ins = [shift(v) for v in x]
+            q = shift(torch.zeros(21, 4, dim, device="cuda"))
+            k, v, out = shift(torch.zeros(21, 2, dim, device="cuda").half()), shift(torch.zeros(21, 2, dim, device="cuda").half()), \
+                shift(torch.zeros(21, 4, dim, device="cuda", dtype=_dt(torch, dtype)))
+            ctx.uocr_kv_append_chunk(0, 1, 31, 21, *(t.data_ptr() for t in ins), dtype=dtype, q_heads=4, q_out=q.data_ptr(),
+                                     k_val=k.data_ptr(), v_val=v.data_ptr())
+            ctx.uocr_attend_chunk(0, 1, 31, 21, 4, q.data_ptr(), out.data_ptr(), dtype)
+            pos = torch.tensor([20, 51], dtype=torch.int32, device="cuda")
+            one = shift(torch.zeros(2, 4, dim, device="cuda", dtype=_dt(torch, dtype)))
+            ctx.uocr_attend(0, 2, pos.data_ptr(), 4, q.data_ptr(), one.data_ptr(), dtype)
+            kept = shift(torch.zeros(2, 7, dtype=torch.int32, device="cuda"))
+            ke, ve = (shift(torch.zeros(2, 7, dim, device="cuda").half()) for _ in range(2))
+            ctx.uocr_kv_evict(0, [1], [0], 49, 7, kept_ptr=kept.data_ptr(), k_val_ptr=ke.data_ptr(), v_val_ptr=ve.data_ptr())
+            w = shift(torch.zeros(2, 2, 59, device="cuda"))
+            ctx.uocr_kv_weights_read(0, 0, 2, 0, 59, w.data_ptr())
+            ctx.uocr_sync()
+            got.append([t.reshape(-1).clone() for t in (q, k, v, out, one, kept, ke, ve, w)])
+            ctx.close()
+        for u, v in zip(*got):
+            assert torch.equal(u, v) and u.float().abs().sum() > 0
