@@ -2184,7 +2184,7 @@ static uocr_status kv4_weights(uocr_ctx* ctx, const char* what, int layer, int r
   a.slot0 = slot0;
   a.n = n;
   a.put = put;
-  CK(launch_kv4_weights(a, ctx->ust), "weights launch");
+  CK(launch_kv4_weights(a, ctx->ust, ctx->pdl), "weights launch");
   return UOCR_OK;
 }
 
@@ -2245,7 +2245,7 @@ uocr_status uocr_kv_append(uocr_ctx* ctx, int32_t layer, int32_t rows, const int
   a.kv_rstep = 1;
   OnDevice dev(ctx->cfg.device);
   CK(dev.e, "set device");
-  CK(launch_kv4_append(a, rows, ctx->ust, false), "kv append launch");
+  CK(launch_kv4_append(a, rows, ctx->ust, ctx->pdl), "kv append launch");
   return UOCR_OK;
 }
 
@@ -2262,7 +2262,7 @@ uocr_status uocr_kv_append_chunk(uocr_ctx* ctx, int32_t layer, int32_t row, int3
   a.kv_row0 = row;
   OnDevice dev(ctx->cfg.device);
   CK(dev.e, "set device");
-  CK(launch_kv4_append(a, n, ctx->ust, false), "kv append launch");
+  CK(launch_kv4_append(a, n, ctx->ust, ctx->pdl), "kv append launch");
   return UOCR_OK;
 }
 
@@ -2287,7 +2287,7 @@ uocr_status uocr_attend(uocr_ctx* ctx, int32_t layer, int32_t rows, const int32_
   a.kv_rstep = 1;
   OnDevice dev(ctx->cfg.device);
   CK(dev.e, "set device");
-  CK(launch_kv4_attn(a, rows, ctx->ust, false), "attention launch");
+  CK(launch_kv4_attn(a, rows, ctx->ust, ctx->pdl), "attention launch");
   return UOCR_OK;
 }
 
@@ -2314,7 +2314,7 @@ uocr_status uocr_attend_chunk(uocr_ctx* ctx, int32_t layer, int32_t row, int32_t
     a.out_dtype = out_dtype;
     a.pos0 = start_pos + off;
     a.kv_row0 = row;
-    CK(launch_kv4_attn(a, n - off < step ? n - off : step, ctx->ust, false), "attention launch");
+    CK(launch_kv4_attn(a, n - off < step ? n - off : step, ctx->ust, ctx->pdl), "attention launch");
   }
   return UOCR_OK;
 }
@@ -2371,7 +2371,7 @@ uocr_status uocr_kv_evict(uocr_ctx* ctx, int32_t layer, int32_t n_rows, const in
   a.protect = protect;
   OnDevice dev(c.device);
   CK(dev.e, "set device");
-  CK(launch_kv4_evict(a, ctx->ust), "eviction launch");
+  CK(launch_kv4_evict(a, ctx->ust, ctx->pdl), "eviction launch");
   for (int l = a.layer0; l < a.layer0 + a.layers; ++l)
     for (int i = 0; i < n_rows; ++i)
       ctx->hole_h[(size_t)l * c.max_rows + dst_rows[i]] = keep < n ? int2{keep, n} : int2{0, 0};

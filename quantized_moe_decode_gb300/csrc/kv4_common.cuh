@@ -168,7 +168,7 @@ struct Kv4WeightsArgs {
   float* dense;
   int MR, nh, tiles, layer0, layers, row0, rows, slot0, n, put;
 };
-cudaError_t launch_kv4_weights(const Kv4WeightsArgs& a, cudaStream_t st);
+cudaError_t launch_kv4_weights(const Kv4WeightsArgs& a, cudaStream_t st, bool pdl);
 
 struct Kv4EvictArgs {
   uint8_t* kv4;                // [L][MR][2][nh][tiles]
@@ -180,7 +180,7 @@ struct Kv4EvictArgs {
   int in_place, wide;          // set by the launcher: a row is its own source; 16-byte aligned values
   unsigned char src[kKv4MaxRows], dst[kKv4MaxRows];
 };
-cudaError_t launch_kv4_evict(const Kv4EvictArgs& a, cudaStream_t st);
+cudaError_t launch_kv4_evict(const Kv4EvictArgs& a, cudaStream_t st, bool pdl);
 cudaError_t init_kv4_attributes();
 
 }  // namespace uocr

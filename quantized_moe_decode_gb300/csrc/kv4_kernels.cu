@@ -404,6 +404,8 @@ cudaError_t launch_kv4_io(const Kv4IoArgs& a, cudaStream_t st) {
 
 template <bool WIDE>
 __global__ void k_kv4_weights(const Kv4WeightsArgs a) {
+  pdl_launch_dependents();
+  pdl_wait();
   const int head = blockIdx.y % a.nh, r = blockIdx.y / a.nh, l = blockIdx.z;
   float* w = a.wts + (((size_t)(a.layer0 + l) * a.MR + a.row0 + r) * a.nh + head) * a.tiles * kKv4Slots + a.slot0;
   float* d = a.dense + (((size_t)l * a.rows + r) * a.nh + head) * a.n;
@@ -417,16 +419,13 @@ __global__ void k_kv4_weights(const Kv4WeightsArgs a) {
   }
 }
 
-cudaError_t launch_kv4_weights(const Kv4WeightsArgs& a, cudaStream_t st) {
+cudaError_t launch_kv4_weights(const Kv4WeightsArgs& a, cudaStream_t st, bool pdl) {
   if (a.n <= 0) return cudaSuccess;
   const bool wide = (uintptr_t)a.dense % 16 == 0 && a.n % 4 == 0 && a.slot0 % 4 == 0;
   const int gx = (a.n + 1023) / 1024;
   const dim3 grid(gx < 64 ? gx : 64, a.rows * a.nh, a.layers);
-  if (wide)
-    k_kv4_weights<true><<<grid, 256, 0, st>>>(a);
-  else
-    k_kv4_weights<false><<<grid, 256, 0, st>>>(a);
-  return cudaGetLastError();
+  return wide ? launch_kernel(k_kv4_weights<true>, grid, dim3(256), 0, st, pdl, a)
+              : launch_kernel(k_kv4_weights<false>, grid, dim3(256), 0, st, pdl, a);
 }
 
 // ------------------------------------------------------------------ attention
@@ -437,8 +436,8 @@ cudaError_t launch_kv4_weights(const Kv4WeightsArgs& a, cudaStream_t st) {
 // an online softmax per query.  Both products run on the tensor cores with the
 // cache as the A operand (m16n8k16): scores = K q with slots as rows, then
 // out = V^T p with dimensions as rows.  The cache's layout puts the A fragments
-// into a lane's own bytes, so a lane copies them with cp.async into its own
-// ring slots (no barrier guards them), turns a word of eight codes into four
+// into a lane's own bytes, so a warp copies whole tiles with cp.async into its
+// own ring slots (no barrier guards them), and a lane turns a word of eight codes into four
 // fp16 pairs with three masks and a shift, and applies scale and minimum with
 // one fused multiply-add each, which gives the entry's value exactly.
 //
@@ -465,8 +464,7 @@ template <int D, int NT>
 struct Attn4 {
   static constexpr int NG = D / 32;
   static constexpr int CB = D / 4;                // code bytes of a lane in a K or V tile
-  static constexpr int KPB = D == 256 ? 16 : 8;   // its key parameter bytes
-  static constexpr int TILE = 32 * (2 * CB + KPB + 16);
+  static constexpr int TILE = 20 * D;             // K codes, V codes, K parameters, V parameters
   // tiles of a warp's step (two independent product chains where the registers
   // allow), steps in its ring, CTAs per SM
 #ifdef A4U
@@ -538,14 +536,13 @@ struct TileList {
 };
 
 // How a call's tiles are dealt out: item i has tiles [start(i), start(i) + tiles)
-// of the list, run c the tiles [c per, (c + 1) per).
+// of the list, run c the tiles [c per, (c + 1) per).  32 bits hold them: a tile
+// is 640 bytes of cache at least, and a chunk has few items where it has runs.
 struct Attn4Runs {
   const int* cum;  // [rows + 1] tiles of one head in the rows before (rows), shared memory
   int nh, uniform, per;
   __device__ int tiles(int z) const { return cum ? cum[z + 1] - cum[z] : uniform; }
-  __device__ long long start(int z, int head) const {
-    return cum ? (long long)cum[z] * nh + (long long)head * tiles(z) : ((long long)z * nh + head) * uniform;
-  }
+  __device__ int start(int z, int head) const { return cum ? cum[z] * nh + head * tiles(z) : (z * nh + head) * uniform; }
 };
 
 // Position, and from it the limit, of token t; an invalid one is reported.
@@ -566,11 +563,11 @@ struct Attn4Rows {
 };
 
 // Fill the runs of a call (every thread of a CTA).  Returns the number of tiles.
-__device__ __forceinline__ long long attn4_runs(const Kv4AttnArgs& a, int tokens, int n_z, Attn4Rows& rows, Attn4Runs& r) {
+__device__ __forceinline__ int attn4_runs(const Kv4AttnArgs& a, int tokens, int n_z, Attn4Rows& rows, Attn4Runs& r) {
   r.nh = a.nh;
   r.cum = nullptr;
   r.uniform = 0;
-  long long total;
+  int total;
   if (a.kv_rstep) {
     if (threadIdx.x < 32) {
       int before = 0;
@@ -597,15 +594,14 @@ __device__ __forceinline__ long long attn4_runs(const Kv4AttnArgs& a, int tokens
     }
     __syncthreads();
     r.cum = rows.cum;
-    total = (long long)rows.cum[tokens] * a.nh;
+    total = rows.cum[tokens] * a.nh;
   } else {  // a chunk: as many tiles for every item as its last token has
     const int2 hole = a.hole[a.kv_row0];
     r.uniform = TileList(token_limit(a, tokens - 1, hole, false), hole).count;
-    total = (long long)r.uniform * n_z * a.nh;
+    total = r.uniform * n_z * a.nh;
   }
   // at least two steps in a run
-  const long long per = (total + a.n_runs - 1) / a.n_runs;
-  r.per = (int)(per < 4 ? 4 : per);
+  r.per = max((int)(((unsigned)total + a.n_runs - 1) / (unsigned)a.n_runs), 4);
   return total;
 }
 
@@ -665,12 +661,11 @@ __global__ void __launch_bounds__(kAttn4Warps * 32, Attn4<D, NT>::CPS) k_kv4_att
   pdl_wait();  // queries and new entries come from the previous kernels
   pdl_launch_dependents();  // (the merge reads positions before its own wait)
   Attn4Runs runs;
-  long long at, end;
-  int z = 0, head = 0;
+  int at, end, z = 0, head = 0;
   bool one_item = false;
   if (a.n_runs) {
-    const long long total = attn4_runs(a, tokens, n_z, s_rows, runs);
-    at = (long long)run * runs.per;
+    const int total = attn4_runs(a, tokens, n_z, s_rows, runs);
+    at = min(run * runs.per, total);
     end = min(total, at + runs.per);
     if (at >= end) {
       z = tokens - 1;  // past the list
@@ -678,18 +673,18 @@ __global__ void __launch_bounds__(kAttn4Warps * 32, Attn4<D, NT>::CPS) k_kv4_att
       int lo = 0, hi = tokens;  // the row that holds tile `at`: the last with start <= at
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if ((long long)runs.cum[mid] * a.nh <= at) lo = mid; else hi = mid;
+        if (runs.cum[mid] * a.nh <= at) lo = mid; else hi = mid;
       }
       z = lo;
-      head = (int)((at - (long long)runs.cum[z] * a.nh) / max(runs.tiles(z), 1));
+      head = (at - runs.cum[z] * a.nh) / max(runs.tiles(z), 1);
     } else {
-      const long long item = at / runs.uniform;
-      z = (int)(item / a.nh);
-      head = (int)(item - (long long)z * a.nh);
+      const int item = at / runs.uniform;
+      z = item / a.nh;
+      head = item - z * a.nh;
     }
     // does the CTA's first run's item span all four?  (Then they meet in it, else
     // no barrier follows.)
-    const long long s = runs.start(z, head), cta = (long long)blockIdx.x * NW * runs.per;
+    const int s = runs.start(z, head), cta = (int)blockIdx.x * NW * runs.per;
     one_item = __syncthreads_and(at < end && s <= cta && s + runs.tiles(z) >= cta + NW * runs.per);
     if (at >= end) return;
   } else {  // one item per CTA
@@ -704,9 +699,10 @@ __global__ void __launch_bounds__(kAttn4Warps * 32, Attn4<D, NT>::CPS) k_kv4_att
   const uint32_t ring_u = smem_u32(ring);
   uint2* s_q = reinterpret_cast<uint2*>(ring + C::RING);
   constexpr int LB = D == 32 ? 8 : 16;            // bytes of a lane's piece of the codes
-  constexpr int KP = 64 * C::CB, VP = KP + 32 * C::KPB;  // parameters in a ring slot
-  const int kp_off = 8 * D + (D == 256 ? g * 64 + t * 16 : (g * C::NG + t * C::NG / 4) * 8);
-  const int vp_off = 8 * D + ((g * D / 256) * 4 + t) * 16;
+  // this lane's parameters in a ring slot
+  const int kp_off = 16 * D + (D == 256 ? g * 64 + t * 16 : (g * C::NG + t * C::NG / 4) * 8);
+  const int vp_off = 18 * D + ((g * D / 256) * 4 + t) * 16;
+  constexpr int PL = D / 8;  // lanes that copy one vector's parameters of a tile
   const size_t v_off = (size_t)a.nh * a.tiles * kv4_tile_bytes(D);
 
   // Item (z, head) from tile `at` of the list on: its tiles [j, j1) of this run.
@@ -717,7 +713,7 @@ __global__ void __launch_bounds__(kAttn4Warps * 32, Attn4<D, NT>::CPS) k_kv4_att
     int lim_lo, lim_hi, j, j1;
     bool whole;
   };
-  auto item_at = [&](int z, int head, long long& at) {
+  auto item_at = [&](int z, int head, int& at) {
     Item it;
     const int row = a.kv_row0 + (a.kv_rstep ? z : 0);
     if (a.n_runs && a.kv_rstep) {
@@ -733,8 +729,7 @@ __global__ void __launch_bounds__(kAttn4Warps * 32, Attn4<D, NT>::CPS) k_kv4_att
     const int count = it.tiles.count;
     it.kt = a.kv4 + ((size_t)row * 2 * a.nh + head) * a.tiles * kv4_tile_bytes(D);
     if (a.n_runs) {
-      const long long s = runs.start(z, head), left = end - s;
-      const int cnt = runs.tiles(z), j0 = (int)(at - s), j1 = left < cnt ? (int)left : cnt;
+      const int s = runs.start(z, head), cnt = runs.tiles(z), j0 = at - s, j1 = min(end - s, cnt);
       at = s + j1;
       it.whole = j0 == 0 && j1 == cnt;
       it.j = min(j0, count);  // a chunk's earlier tokens have fewer
@@ -750,7 +745,7 @@ __global__ void __launch_bounds__(kAttn4Warps * 32, Attn4<D, NT>::CPS) k_kv4_att
   const int step = a.n_runs ? U : NW * U;
   // The copies run ahead of the products by ST - 1 steps, across the items' bounds.
   int pf_z = z, pf_head = head;
-  long long pf_at = at;
+  int pf_at = at;
   Item pf{};
   if (at < end) pf = item_at(pf_z, pf_head, pf_at);
   auto issue = [&](int stage) {
@@ -766,7 +761,7 @@ __global__ void __launch_bounds__(kAttn4Warps * 32, Attn4<D, NT>::CPS) k_kv4_att
     for (int u = 0; u < U; ++u) {
       if (pf.j + u < pf.j1) {
         const uint8_t* k = pf.kt + (size_t)pf.tiles(pf.j + u) * kv4_tile_bytes(D);
-        const uint8_t *kc = k + lane * LB, *vc = kc + v_off, *kp = k + kp_off, *vp = k + v_off + vp_off;
+        const uint8_t *kc = k + lane * LB, *vc = kc + v_off;
         const uint32_t du = d + u * C::TILE, dc = du + lane * LB;
         if constexpr (D == 32) {
           cp_async8u(dc, kc);
@@ -778,11 +773,13 @@ __global__ void __launch_bounds__(kAttn4Warps * 32, Attn4<D, NT>::CPS) k_kv4_att
             cp_async16u(dc + 32 * C::CB + p * 512, vc + p * 512);
           }
         }
-        if constexpr (C::KPB == 16)
-          cp_async16u(du + KP + lane * 16, kp);
-        else
-          cp_async8u(du + KP + lane * 8, kp);
-        cp_async16u(du + VP + lane * 16, vp);
+        const uint8_t* pp = k + 8 * D + lane * 16;
+        if constexpr (D == 256) {
+          cp_async16u(du + 16 * D + lane * 16, pp);
+          cp_async16u(du + 18 * D + lane * 16, pp + v_off);
+        } else if (lane < 2 * PL) {
+          cp_async16u(du + 16 * D + lane * 16, lane < PL ? pp : pp + v_off - 2 * D);
+        }
       }
     }
     pf.j += step;
@@ -866,6 +863,7 @@ __global__ void __launch_bounds__(kAttn4Warps * 32, Attn4<D, NT>::CPS) k_kv4_att
     auto tile_step = [&](auto mask_tag, int j) {
       constexpr bool MASK = decltype(mask_tag)::value;
       cp_wait<ST - 2>();
+      __syncwarp();  // every lane's copies have landed, and the last step's slots are read
       const uint32_t d = ring_u + stage * (U * C::TILE);
       issue(stage == 0 ? ST - 1 : stage - 1);  // into the slots that the last step left
       stage = stage == ST - 1 ? 0 : stage + 1;
@@ -885,10 +883,10 @@ __global__ void __launch_bounds__(kAttn4Warps * 32, Attn4<D, NT>::CPS) k_kv4_att
         }
         // (s, m) of slots g and g + 8, one or two groups
         uint32_t par[4];
-        if constexpr (C::KPB == 16) {
-          lds128u(du + KP + lane * 16, par[0], par[1], par[2], par[3]);
+        if constexpr (D == 256) {
+          lds128u(du + kp_off, par[0], par[1], par[2], par[3]);
         } else {
-          lds64u(du + KP + lane * 8, par[0], par[1]);
+          lds64u(du + kp_off, par[0], par[1]);
           par[2] = par[0], par[3] = par[1];
         }
 #pragma unroll
@@ -982,7 +980,7 @@ __global__ void __launch_bounds__(kAttn4Warps * 32, Attn4<D, NT>::CPS) k_kv4_att
       for (int u = 0; u < U; ++u) {
         const uint32_t du = d + u * C::TILE;
         uint4 par;
-        lds128u(du + VP + lane * 16, par.x, par.y, par.z, par.w);
+        lds128u(du + vp_off, par.x, par.y, par.z, par.w);
         if constexpr (MASK) {
           // slots that no query reads become zeros: their weight is zero, but an
           // unread NaN or infinity times zero would not be
@@ -1149,79 +1147,144 @@ __global__ void __launch_bounds__(kAttn4Warps * 32, Attn4<D, NT>::CPS) k_kv4_att
 }
 
 // Merge the runs' partials: a CTA per (item, query of the item), which also adds
-// its share of the row's weights.  A partial's factor is taken once; the values
-// are then independent loads, so that the time is a few trips to the L2.
+// its share of the row's weights.  A trip to the L2 for all maxima and sums, one
+// for the values of the partials that hold any.
 __global__ void __launch_bounds__(256) k_kv4_merge(const Kv4AttnArgs a, int tokens, int n_z, int nq_tile) {
-  constexpr int CAP = 256;  // partials whose factors are held at a time
+  constexpr int T = 256, CAP = 1024;  // partials listed at a time
   __shared__ Attn4Rows s_rows;
   __shared__ float2 s_fin[8];
+  __shared__ float s_red[2][8];
   __shared__ float s_f[CAP];
+  __shared__ unsigned short s_idx[CAP];
+  __shared__ int s_n;
   __shared__ float s_acc[8][256];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, D = a.D, G = a.q_heads / a.nh;
   const int head = blockIdx.x % a.nh, z = blockIdx.x / a.nh, mine = blockIdx.y;
   Attn4Runs runs;
   attn4_runs(a, tokens, n_z, s_rows, runs);  // positions and holes: written before the attention began
   pdl_launch_dependents();
-  pdl_wait();
-  const int cnt = runs.tiles(z);
-  const long long s = runs.start(z, head);
+  const int cnt = runs.tiles(z), s = runs.start(z, head);
   const int u0 = a.kv_rstep ? z * G : z * nq_tile;
   const int nq = a.kv_rstep ? G : min(nq_tile, tokens * G - u0);
-  const int c0 = (int)(s / runs.per), n = cnt ? (int)((s + cnt - 1) / runs.per) - c0 + 1 : 0;
+  const int c0 = s / runs.per, n = cnt ? (s + cnt - 1) / runs.per - c0 + 1 : 0;
+  pdl_wait();
   if (mine >= nq || n == 1) return;  // one run's: finished there
   // a run's second partial is of an item that begins inside it: the first run's, if any
   const size_t step = (size_t)2 * nq_tile * (D + kAttn4PartHead);
   const float* base = a.parts + c0 * step;
-  const int shift = s > (long long)c0 * runs.per ? (int)(step >> 1) : 0;
+  const int shift = s > c0 * runs.per ? (int)(step >> 1) : 0;
   auto part = [&](int c, int i) { return base + c * step + (c ? 0 : shift) + i * (D + kAttn4PartHead); };
   const float sink = a.sink ? a.sink[head] * 1.4426950408889634f : -INFINITY;
   const bool track = a.wts && a.kv_rstep;
-  // maximum and sum of every query (for the weights) or of this CTA's
-  for (int i = warp; i < nq; i += 8) {
-    if (!track && i != mine) continue;
-    float m = kNoMax, l = 0.f;  // of this lane's partials
-#pragma unroll 4
-    for (int c = lane; c < n; c += 32) {
-      const float2 p = *reinterpret_cast<const float2*>(part(c, i));
-      const float hi = fmaxf(m, p.x);
-      l = l * ex2(m - hi) + p.y * ex2(p.x - hi);
-      m = hi;
-    }
-    float M = m;
+
+  float m = kNoMax, l = 0.f;  // of this thread's partials
+  float2 own[4];               // the first four of them
 #pragma unroll
-    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    M = fmaxf(M, sink);
-    float L = l * ex2(m - M);
+  for (int k = 0; k < 4; ++k) own[k] = threadIdx.x + k * T < n ? *reinterpret_cast<const float2*>(part(threadIdx.x + k * T, mine))
+                                                           : make_float2(kNoMax, 0.f);
 #pragma unroll
-    for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-    if (a.sink) L += ex2(sink - M);
-    if (lane == 0) s_fin[i] = make_float2(M, L == 0.f ? 0.f : 1.f / L);
+  for (int k = 0; k < 4; ++k) m = fmaxf(m, own[k].x);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) l += own[k].y * ex2(own[k].x - m);
+  for (int c = threadIdx.x + 4 * T; c < n; c += T) {
+    const float2 p = *reinterpret_cast<const float2*>(part(c, mine));
+    const float hi = fmaxf(m, p.x);
+    l = l * ex2(m - hi) + p.y * ex2(p.x - hi);
+    m = hi;
   }
+  float M = m;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  if (lane == 0) s_red[0][warp] = M;
   __syncthreads();
-  const float2 fin = s_fin[mine];
+  M = sink;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) M = fmaxf(M, s_red[0][w]);
+  float L = l * ex2(m - M);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+  if (lane == 0) s_red[1][warp] = L;
+  __syncthreads();
+  L = a.sink ? ex2(sink - M) : 0.f;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) L += s_red[1][w];
+  const float2 fin = make_float2(M, L == 0.f ? 0.f : 1.f / L);  // nothing to read: zeros
+  if (threadIdx.x == 0) s_fin[mine] = fin;
+
+  // the values, D / 32 of a lane, of the partials that hold any, in order
   float v[8];
 #pragma unroll
   for (int k = 0; k < 8; ++k) v[k] = 0.f;
   for (int b = 0; b < n; b += CAP) {
-    if (b + threadIdx.x < n && threadIdx.x < CAP) {
-      const float2 p = *reinterpret_cast<const float2*>(part(b + threadIdx.x, mine));
-      s_f[threadIdx.x] = ex2(p.x - fin.x);
+    if (threadIdx.x == 0) s_n = 0;
+    __syncthreads();
+#pragma unroll 1
+    for (int k = 0; k < CAP / T; ++k) {
+      const int c = b + k * T + threadIdx.x;
+      float2 p = make_float2(kNoMax, 0.f);
+      if (b == 0) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (j == k) p = own[j];
+      } else if (c < n) {
+        p = *reinterpret_cast<const float2*>(part(c, mine));
+      }
+      const bool has = c < n && p.y != 0.f;
+      const uint32_t votes = __ballot_sync(0xffffffffu, has);
+      if (lane == 0) s_red[0][warp] = __int_as_float(__popc(votes));
+      __syncthreads();
+      int pos = s_n + __popc(votes & ((1u << lane) - 1u)), all = 0;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) {
+        const int x = __float_as_int(s_red[0][w]);
+        if (w < warp) pos += x;
+        all += x;
+      }
+      if (has) {
+        s_f[pos] = ex2(p.x - M);
+        s_idx[pos] = (unsigned short)(c - b);
+      }
+      __syncthreads();
+      if (threadIdx.x == 0) s_n += all;
+      if (b + (k + 1) * T >= n) break;
     }
     __syncthreads();
+    const int listed = s_n;
 #pragma unroll 4
-    for (int c = warp; c < min(CAP, n - b); c += 8) {
-      const float* p = part(b + c, mine) + kAttn4PartHead;
-      const float f = s_f[c];
-      if (f != 0.f)
+    for (int i = warp; i < listed; i += 8) {
+      const float* p = part(b + s_idx[i], mine) + kAttn4PartHead;
+      const float f = s_f[i];
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (32 * k < D) v[k] += p[lane + 32 * k] * f;
+      for (int k = 0; k < 8; ++k)
+        if (32 * k < D) v[k] += p[lane + 32 * k] * f;
     }
     __syncthreads();
   }
 #pragma unroll
   for (int k = 0; k < 8; ++k)
     if (32 * k < D) s_acc[warp][lane + 32 * k] = v[k];
+  // the other queries' maximum and sum, for the weights
+  if (track)
+    for (int i = warp; i < nq; i += 8) {
+      if (i == mine) continue;
+      float m = kNoMax, l = 0.f;
+#pragma unroll 4
+      for (int c = lane; c < n; c += 32) {
+        const float2 p = *reinterpret_cast<const float2*>(part(c, i));
+        const float hi = fmaxf(m, p.x);
+        l = l * ex2(m - hi) + p.y * ex2(p.x - hi);
+        m = hi;
+      }
+      float M = m;
+#pragma unroll
+      for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+      M = fmaxf(M, sink);
+      float L = l * ex2(m - M);
+#pragma unroll
+      for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+      if (a.sink) L += ex2(sink - M);
+      if (lane == 0) s_fin[i] = make_float2(M, L == 0.f ? 0.f : 1.f / L);
+    }
   __syncthreads();
   const long long qi = (long long)((u0 + mine) / G) * a.q_heads + head * G + (u0 + mine) % G;
   for (int d = threadIdx.x; d < D; d += blockDim.x) {
@@ -1349,6 +1412,8 @@ __global__ void __launch_bounds__(kEvictThreads) k_kv4_evict(const Kv4EvictArgs 
   const int head = blockIdx.x, r = blockIdx.y, l = blockIdx.z;
   const int layer = a.layer0 + l, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rs = a.src[r], rd = a.dst[r];
+  pdl_launch_dependents();
+  pdl_wait();
   const int2 hole = a.hole[(size_t)layer * a.MR + rs];
   const int gap = hole.y > hole.x ? hole.y - hole.x : 0;
   const int live = a.n - gap;  // live entry i is slot i, or i + gap behind the hole
@@ -1523,20 +1588,19 @@ __global__ void k_kv4_hole(const Kv4EvictArgs a) {
     a.hole[(size_t)(a.layer0 + l) * a.MR + a.dst[r]] = a.keep < a.n ? make_int2(a.keep, a.n) : make_int2(0, 0);
 }
 
-cudaError_t launch_kv4_evict(const Kv4EvictArgs& args, cudaStream_t st) {
+cudaError_t launch_kv4_evict(const Kv4EvictArgs& args, cudaStream_t st, bool pdl) {
   Kv4EvictArgs a = args;
   a.in_place = 0;
   for (int i = 0; i < a.rows; ++i) a.in_place |= a.src[i] == a.dst[i];
   a.wide = ((uintptr_t)a.k_val | (uintptr_t)a.v_val) % 16 == 0;
   const dim3 grid(a.nh, a.rows, a.layers);
+  cudaError_t e = cudaErrorInvalidValue;
   switch (a.D) {
-    case 32: k_kv4_evict<32><<<grid, kEvictThreads, 0, st>>>(a); break;
-    case 64: k_kv4_evict<64><<<grid, kEvictThreads, 0, st>>>(a); break;
-    case 128: k_kv4_evict<128><<<grid, kEvictThreads, 0, st>>>(a); break;
-    case 256: k_kv4_evict<256><<<grid, kEvictThreads, 0, st>>>(a); break;
-    default: return cudaErrorInvalidValue;
+    case 32: e = launch_kernel(k_kv4_evict<32>, grid, dim3(kEvictThreads), 0, st, pdl, a); break;
+    case 64: e = launch_kernel(k_kv4_evict<64>, grid, dim3(kEvictThreads), 0, st, pdl, a); break;
+    case 128: e = launch_kernel(k_kv4_evict<128>, grid, dim3(kEvictThreads), 0, st, pdl, a); break;
+    case 256: e = launch_kernel(k_kv4_evict<256>, grid, dim3(kEvictThreads), 0, st, pdl, a); break;
   }
-  cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !a.in_place) return e;
   k_kv4_hole<<<a.layers, kKv4MaxRows, 0, st>>>(a);
   return cudaGetLastError();
