@@ -255,18 +255,14 @@ class Context:
         self._ck(self.lib.uocr_kv_read_i4(self.h, row, layer, slot0, n, *(x.ctypes.data for x in out)))
         return tuple(out)
 
-    def _qkv(self, q_ptr, k_ptr, v_ptr, dtype, q_heads, ld_q, ld_k, ld_v, q_out, k_val, v_val):
-        return uocr_qkv(q_ptr or None, k_ptr or None, v_ptr or None, ld_q, ld_k, ld_v, dtype, q_heads, q_out or None,
-                        k_val or None, v_val or None)
-
     def uocr_kv_append(self, layer, rows, pos_ptr, q_ptr, k_ptr, v_ptr, *, dtype=DT_F16, q_heads=0, ld_q=0, ld_k=0,
                        ld_v=0, q_out=0, k_val=0, v_val=0):
-        x = self._qkv(q_ptr, k_ptr, v_ptr, dtype, q_heads, ld_q, ld_k, ld_v, q_out, k_val, v_val)
+        x = uocr_qkv(q_ptr, k_ptr, v_ptr, ld_q, ld_k, ld_v, dtype, q_heads, q_out, k_val, v_val)
         self._ck(self.lib.uocr_kv_append(self.h, layer, rows, pos_ptr or None, C.byref(x)))
 
     def uocr_kv_append_chunk(self, layer, row, start_pos, n, q_ptr, k_ptr, v_ptr, *, dtype=DT_F16, q_heads=0, ld_q=0,
                              ld_k=0, ld_v=0, q_out=0, k_val=0, v_val=0):
-        x = self._qkv(q_ptr, k_ptr, v_ptr, dtype, q_heads, ld_q, ld_k, ld_v, q_out, k_val, v_val)
+        x = uocr_qkv(q_ptr, k_ptr, v_ptr, ld_q, ld_k, ld_v, dtype, q_heads, q_out, k_val, v_val)
         self._ck(self.lib.uocr_kv_append_chunk(self.h, layer, row, start_pos, n, C.byref(x)))
 
     def uocr_attend(self, layer, rows, pos_ptr, q_heads, q_ptr, out_ptr, out_dtype=DT_F16):
@@ -278,11 +274,13 @@ class Context:
                                             out_ptr or None))
 
     def uocr_kv_evict(self, layer, src_rows, dst_rows, n, keep, protect=0, *, kept_ptr=0, k_val_ptr=0, v_val_ptr=0):
-        src, dst = np.asarray(list(src_rows), np.int32), np.asarray(list(dst_rows), np.int32)
-        if src.shape != dst.shape:
+        count = len(src_rows)
+        if count != len(dst_rows):
             raise ValueError("uocr_kv_evict: src_rows and dst_rows have different lengths")
-        self._ck(self.lib.uocr_kv_evict(self.h, layer, src.size, src.ctypes.data, dst.ctypes.data, n, keep, protect,
-                                        kept_ptr or None, k_val_ptr or None, v_val_ptr or None))
+        rows = (C.c_int32 * (2 * count + 1))(*src_rows, *dst_rows)
+        at = C.addressof(rows)
+        self._ck(self.lib.uocr_kv_evict(self.h, layer, count, at, at + 4 * count, n, keep, protect, kept_ptr or None,
+                                        k_val_ptr or None, v_val_ptr or None))
 
     def uocr_kv_weights_read(self, layer, row0, n_rows, slot0, n, out_ptr):
         self._ck(self.lib.uocr_kv_weights_read(self.h, layer, row0, n_rows, slot0, n, out_ptr or None))

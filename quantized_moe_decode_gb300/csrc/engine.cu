@@ -2358,6 +2358,9 @@ uocr_status uocr_kv_evict(uocr_ctx* ctx, int32_t layer, int32_t n_rows, const in
   a.kv4 = ctx->kv4;
   a.wts = ctx->wts;
   a.hole = ctx->hole;
+  // the accumulation's scratch: eight slots for every row, head and slot of a layer
+  a.list = reinterpret_cast<int*>(ctx->scores);
+  a.list_cap = (size_t)ctx->track_q() * c.n_heads * ctx->tiles * kKv4Slots;
   a.kept = kept;
   a.k_val = reinterpret_cast<__half*>(k_val);
   a.v_val = reinterpret_cast<__half*>(v_val);

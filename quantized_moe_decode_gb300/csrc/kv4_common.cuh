@@ -27,6 +27,7 @@ constexpr int kKv4Group = 32;  // dimensions that share a scale and a minimum
 
 __host__ __device__ constexpr int kv4_tile_bytes(int D) { return 10 * D; }
 
+// Every address below is a term of the slot plus a term of the piece (i, grp).
 // byte o of lane's stream of D/4 bytes
 __device__ __forceinline__ int kv4_stream(int D, int lane, int o) {
   return D >= 64 ? (o >> 4) * 512 + lane * 16 + (o & 15) : lane * 8 + o;
@@ -177,7 +178,9 @@ struct Kv4EvictArgs {
   int* kept;                   // [layers][rows][nh][keep] or nullptr
   __half *k_val, *v_val;       // [layers][rows][nh][keep][D] or nullptr
   int MR, nh, D, tiles, layer0, layers, rows, n, keep, protect;
-  int in_place, wide;          // set by the launcher: a row is its own source; 16-byte aligned values
+  int* list;                   // scratch: kept slots of rows that are not their own source
+  size_t list_cap;             // slots that it holds, a layer's at least
+  int wide;                    // set by the launcher: the values are 16-byte aligned
   unsigned char src[kKv4MaxRows], dst[kKv4MaxRows];
 };
 cudaError_t launch_kv4_evict(const Kv4EvictArgs& a, cudaStream_t st, bool pdl);

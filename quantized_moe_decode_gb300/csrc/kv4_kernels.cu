@@ -1177,6 +1177,45 @@ __global__ void __launch_bounds__(256) k_kv4_merge(const Kv4AttnArgs a, int toke
   const float sink = a.sink ? a.sink[head] * 1.4426950408889634f : -INFINITY;
   const bool track = a.wts && a.kv_rstep;
 
+  const long long qi = (long long)((u0 + mine) / G) * a.q_heads + head * G + (u0 + mine) % G;
+  if (n <= 32) {  // every warp takes all maxima and sums by itself, a thread one dimension
+    auto stats = [&](int i, float2& p) {
+      p = lane < n ? *reinterpret_cast<const float2*>(part(lane, i)) : make_float2(kNoMax, 0.f);
+      float M = p.x;
+#pragma unroll
+      for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+      M = fmaxf(M, sink);
+      p.x = ex2(p.x - M);
+      float L = p.y * p.x;
+#pragma unroll
+      for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+      if (a.sink) L += ex2(sink - M);
+      return make_float2(M, L == 0.f ? 0.f : 1.f / L);  // nothing to read: zeros
+    };
+    const int d = threadIdx.x;
+    if (d < D) {
+      float2 p;
+      const float2 fin = stats(mine, p);
+      const float* v0 = part(0, mine) + kAttn4PartHead + d;
+      float o = n ? v0[0] * __shfl_sync(0xffffffffu, p.x, 0) : 0.f;
+      const float* v = base + mine * (D + kAttn4PartHead) + kAttn4PartHead + d;
+#pragma unroll 4
+      for (int c = 1; c < n; ++c) o += v[c * step] * __shfl_sync(0xffffffffu, p.x, c);
+      store_elem(a.out, a.out_dtype, qi * D + d, o * fin.y);
+      if (a.lse && d == 0) a.lse[qi] = fin;
+    }
+    if (!track) return;
+    for (int i = warp; i < nq; i += 8) {
+      float2 p;
+      const float2 fin = stats(i, p);
+      if (lane == 0) s_fin[i] = fin;
+    }
+    __syncthreads();
+    add_weights(a, z, head, a.kv_row0 + z, TileList(s_rows.lim[z], s_rows.hole[z]), nq, s_fin, mine * 256 + threadIdx.x,
+                nq * 256);
+    return;
+  }
+
   float m = kNoMax, l = 0.f;  // of this thread's partials
   float2 own[4];               // the first four of them
 #pragma unroll
@@ -1286,7 +1325,6 @@ __global__ void __launch_bounds__(256) k_kv4_merge(const Kv4AttnArgs a, int toke
       if (lane == 0) s_fin[i] = make_float2(M, L == 0.f ? 0.f : 1.f / L);
     }
   __syncthreads();
-  const long long qi = (long long)((u0 + mine) / G) * a.q_heads + head * G + (u0 + mine) % G;
   for (int d = threadIdx.x; d < D; d += blockDim.x) {
     float o = 0.f;
 #pragma unroll
@@ -1387,26 +1425,90 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// One CTA per (head, row, layer).  The key of the keep-th largest weight comes
-// from three radix passes (11, 11, 10 bits; the first digit holds the exponent
-// and two bits, which spreads weights over the bins; lanes with the same digit
-// add once).  Then the kept entries move, lowest slot first, to the front of
-// the destination row: live entries in blocks of the CTA's size are ranked by
-// ballots, and the kept ones go through registers, several per warp at a time.
-// A chunk is read before any of it is written and a kept entry never moves up,
-// so source and destination may be the same row.  Bound by the scattered reads
-// (a slot's values lie in 16-byte pieces of its tile) and the writes.
+// The key of the keep-th largest weight comes from three radix passes (11, 11,
+// 10 bits; the first digit holds the exponent and two bits, which spreads weights
+// over the bins), one CTA per (head, row, layer).  Live entries are then ranked
+// in blocks of the CTA's size by ballots.  Between different rows the kept slots
+// are listed, and a second kernel moves the entries with as many warps as there
+// are entries.  A row that is its own source is compacted by the selecting CTA
+// itself: a chunk is read into registers before any of it is written, and a kept
+// entry never moves up.  Bound by the scattered reads (a slot's values lie in
+// 16-byte pieces of its tile) and the writes.
 constexpr int kEvictThreads = 512;
 constexpr int kEvictKeys = 4096;  // weights kept in shared memory between the passes
 constexpr int kEvictPer = 4;      // entries of a warp in flight
 
+// An entry in a warp's registers, and the places of a lane's pieces: an entry's
+// pieces lie at a place of its slot plus a place of the piece.
 template <int D>
+struct Kv4Entry {
+  static constexpr int VQ = D == 256 ? 2 : 1, NG = D / kKv4Group;
+  uint32_t kw, kpar;
+  uint16_t vq[VQ], vpar;
+  struct At {
+    int k, v[VQ], vp;
+    __device__ explicit At(int lane) {
+      k = lane < D / 8 ? kv4_k_word(D, 0, lane) : 0;
+#pragma unroll
+      for (int h = 0; h < VQ; ++h) v[h] = lane + 32 * h < D / 4 ? kv4_v_quad(D, 0, lane + 32 * h) : 0;
+      vp = kv4_v_param(D, 0, lane >> 1, lane & 1) - kv4_v_param(D, 0, 0, 0);
+    }
+  };
+  __device__ __forceinline__ void load(const uint8_t* keys, size_t voff, int slot, const At& at, int lane) {
+    const int s = slot & 15;
+    const uint8_t* kp = keys + (size_t)(slot >> 4) * kv4_tile_bytes(D);
+    const uint8_t* vp = kp + voff;
+    if (lane < D / 8) kw = *reinterpret_cast<const uint32_t*>(kp + kv4_k_word(D, s, 0) + at.k);
+    if (lane < NG) kpar = *reinterpret_cast<const uint32_t*>(kp + kv4_k_param(D, s, 0) + lane * 8);
+#pragma unroll
+    for (int h = 0; h < VQ; ++h)
+      if (lane < D / 4) vq[h] = *reinterpret_cast<const uint16_t*>(vp + kv4_v_quad(D, s, 0) + at.v[h]);
+    if (lane < 2 * NG) vpar = *reinterpret_cast<const uint16_t*>(vp + kv4_v_param(D, s, 0, 0) + at.vp);
+  }
+  __device__ __forceinline__ void store(uint8_t* keys, size_t voff, int slot, const At& at, int lane) const {
+    const int s = slot & 15;
+    uint8_t* kp = keys + (size_t)(slot >> 4) * kv4_tile_bytes(D);
+    uint8_t* vp = kp + voff;
+    if (lane < D / 8) *reinterpret_cast<uint32_t*>(kp + kv4_k_word(D, s, 0) + at.k) = kw;
+    if (lane < NG) *reinterpret_cast<uint32_t*>(kp + kv4_k_param(D, s, 0) + lane * 8) = kpar;
+#pragma unroll
+    for (int h = 0; h < VQ; ++h)
+      if (lane < D / 4) *reinterpret_cast<uint16_t*>(vp + kv4_v_quad(D, s, 0) + at.v[h]) = vq[h];
+    if (lane < 2 * NG) *reinterpret_cast<uint16_t*>(vp + kv4_v_param(D, s, 0, 0) + at.vp) = vpar;
+  }
+  // the values, to [D] arrays (whole warp)
+  __device__ __forceinline__ void values(__half* k_val, __half* v_val, int wide, int lane) const {
+    if (k_val) {  // word w belongs to group w / 4
+      const uint32_t p = __shfl_sync(0xffffffffu, kpar, lane >> 2);
+      uint32_t x[4];
+      dequant8(kw, __byte_perm(p, 0, 0x1010), __byte_perm(p, 0, 0x3232), x);
+      if (lane < D / 8) store16(k_val + 8 * lane, wide, make_uint4(x[0], x[1], x[2], x[3]));
+    }
+    if (v_val) {  // quad i belongs to group i / 8
+#pragma unroll
+      for (int h = 0; h < VQ; ++h) {
+        const int grp = (lane + 32 * h) >> 3;
+        const uint32_t sc = __shfl_sync(0xffffffffu, (uint32_t)vpar, 2 * grp) * 0x10001u;
+        const uint32_t lo = __shfl_sync(0xffffffffu, (uint32_t)vpar, 2 * grp + 1) * 0x10001u;
+        const uint32_t q = vq[h];
+        // nibbles 0 | 1 to bits 0-3 of the halves, 2 | 3 to bits 4-7
+        const uint32_t w = (q & 0xFu) | ((q & 0xF0u) << 12) | ((q & 0xF00u) >> 4) | ((q & 0xF000u) << 8);
+        const uint32_t x0 = hfma2u(sc, hsub2u(lop_and_or(w, 0x000F000Fu, 0x64006400u), 0x64006400u), lo);
+        const uint32_t x1 = hfma2u(sc, hsub2u(lop_and_or(w, 0x00F000F0u, 0x54005400u), 0x54005400u), lo);
+        if (lane < D / 4) store8(v_val + 4 * (lane + 32 * h), wide, make_uint2(x0, x1));
+      }
+    }
+  }
+};
+
+// MOVE: compact here (a row may be its own source); else list the kept slots.
+template <int D, bool MOVE>
 __global__ void __launch_bounds__(kEvictThreads) k_kv4_evict(const Kv4EvictArgs a) {
-  constexpr int T = kEvictThreads, NW = T / 32, NG = D / kKv4Group, E = kEvictPer, TB = kv4_tile_bytes(D);
+  constexpr int T = kEvictThreads, NW = T / 32, E = kEvictPer, TB = kv4_tile_bytes(D);
   __shared__ uint32_t s_key[kEvictKeys];
   __shared__ int s_hist[2048];
   __shared__ int s_warp[2][NW];
-  __shared__ int s_kept[T];
+  __shared__ int s_kept[MOVE ? T : 1];
   __shared__ uint32_t s_prefix;
   __shared__ int s_need;
   const int head = blockIdx.x, r = blockIdx.y, l = blockIdx.z;
@@ -1436,13 +1538,10 @@ __global__ void __launch_bounds__(kEvictThreads) k_kv4_evict(const Kv4EvictArgs 
     __syncthreads();
     const uint32_t prefix = s_prefix;
     const int need = s_need;
-    for (int i0 = a.protect; i0 < live; i0 += T) {
-      const int i = i0 + tid;
-      const uint32_t k = i < live ? key_of(i) : 0u;
-      const bool in = i < live && (pass == 0 || (k >> (shift + bits)) == (prefix >> (shift + bits)));
-      const uint32_t digit = in ? (k >> shift) & ((1u << bits) - 1u) : 0xFFFFFFFFu;
-      const uint32_t same = __match_any_sync(0xffffffffu, digit);
-      if (in && lane == __ffs(same) - 1) atomicAdd(&s_hist[digit], __popc(same));
+    for (int i = a.protect + tid; i < live; i += T) {
+      const uint32_t k = key_of(i);
+      if (pass == 0 || (k >> (shift + bits)) == (prefix >> (shift + bits)))
+        atomicAdd(&s_hist[(k >> shift) & ((1u << bits) - 1u)], 1);
     }
     __syncthreads();
     // thread t holds the four bins below 2048 - 4t: counts of everything above them
@@ -1475,10 +1574,10 @@ __global__ void __launch_bounds__(kEvictThreads) k_kv4_evict(const Kv4EvictArgs 
   const uint32_t kth = s_prefix;
   const int ties = some ? s_need : 0;
 
-  const uint8_t* src = a.kv4 + (((size_t)layer * a.MR + rs) * 2 * a.nh + head) * a.tiles * TB;
-  uint8_t* dst = a.kv4 + (((size_t)layer * a.MR + rd) * 2 * a.nh + head) * a.tiles * TB;
-  const size_t voff = (size_t)a.nh * a.tiles * TB;
+  uint8_t* const base = a.kv4 + ((size_t)layer * a.MR * 2 * a.nh + head) * a.tiles * TB;
+  const size_t row_bytes = (size_t)2 * a.nh * a.tiles * TB, voff = row_bytes / 2;
   const size_t out0 = (((size_t)l * a.rows + r) * a.nh + head) * a.keep;
+  const typename Kv4Entry<D>::At at_lane(lane);
   int done = 0, tied = 0;
   for (int i0 = 0; i0 < live && done < a.keep; i0 += T) {
     const int i = i0 + tid;
@@ -1510,75 +1609,82 @@ __global__ void __launch_bounds__(kEvictThreads) k_kv4_evict(const Kv4EvictArgs 
       if (w < warp) at += s_warp[1][w];
       count += s_warp[1][w];
     }
-    if (keep) s_kept[at] = slot_of(i);
-    __syncthreads();
-    for (int c0 = 0; c0 < count; c0 += NW * E) {
-      uint32_t kw[E], kpar[E];
-      uint16_t vq[E][D == 256 ? 2 : 1], vpar[E];
-      float wt[E];
+    if constexpr (!MOVE) {
+      if (keep) a.list[out0 + done + at] = slot_of(i);
+    } else {
+      if (keep) s_kept[at] = slot_of(i);
+      __syncthreads();
+      for (int c0 = 0; c0 < count; c0 += NW * E) {
+        Kv4Entry<D> x[E];
+        float wt[E];
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const int c = c0 + e * NW + warp;
-        if (c < count) {
-          const int ss = s_kept[c], s = ss & 15;
-          const uint8_t* kp = src + (size_t)(ss >> 4) * TB;
-          const uint8_t* vp = kp + voff;
-          if (lane < D / 8) kw[e] = *reinterpret_cast<const uint32_t*>(kp + kv4_k_word(D, s, lane));
-          if (lane < NG) kpar[e] = *reinterpret_cast<const uint32_t*>(kp + kv4_k_param(D, s, lane));
-          if (lane < D / 4) vq[e][0] = *reinterpret_cast<const uint16_t*>(vp + kv4_v_quad(D, s, lane));
-          if constexpr (D == 256) vq[e][1] = *reinterpret_cast<const uint16_t*>(vp + kv4_v_quad(D, s, lane + 32));
-          if (lane < 2 * NG) vpar[e] = *reinterpret_cast<const uint16_t*>(vp + kv4_v_param(D, s, lane >> 1, lane & 1));
-          if (lane == 0) wt[e] = ws[ss];
+        for (int e = 0; e < E; ++e) {
+          const int c = c0 + e * NW + warp;
+          if (c < count) {
+            x[e].load(base + rs * row_bytes, voff, s_kept[c], at_lane, lane);
+            if (lane == 0) wt[e] = ws[s_kept[c]];
+          }
         }
-      }
-      __syncthreads();  // the chunk is in registers
+        __syncthreads();  // the chunk is in registers
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const int c = c0 + e * NW + warp;
-        if (c < count) {
-          const int ds = done + c, s = ds & 15;
-          uint8_t* kp = dst + (size_t)(ds >> 4) * TB;
-          uint8_t* vp = kp + voff;
-          if (lane < D / 8) *reinterpret_cast<uint32_t*>(kp + kv4_k_word(D, s, lane)) = kw[e];
-          if (lane < NG) *reinterpret_cast<uint32_t*>(kp + kv4_k_param(D, s, lane)) = kpar[e];
-          if (lane < D / 4) *reinterpret_cast<uint16_t*>(vp + kv4_v_quad(D, s, lane)) = vq[e][0];
-          if constexpr (D == 256) *reinterpret_cast<uint16_t*>(vp + kv4_v_quad(D, s, lane + 32)) = vq[e][1];
-          if (lane < 2 * NG) *reinterpret_cast<uint16_t*>(vp + kv4_v_param(D, s, lane >> 1, lane & 1)) = vpar[e];
-          if (lane == 0) {
-            wd[ds] = wt[e];
-            if (a.kept) a.kept[out0 + ds] = s_kept[c];
-          }
-          if (a.k_val) {  // word w belongs to group w / 4
-            const uint32_t p = __shfl_sync(0xffffffffu, kpar[e], lane >> 2);
-            const uint32_t sc = __byte_perm(p, 0, 0x1010), lo = __byte_perm(p, 0, 0x3232);
-            uint32_t x[4];
-            dequant8(kw[e], sc, lo, x);
-            if (lane < D / 8)
-              store16(a.k_val + (out0 + ds) * D + 8 * lane, a.wide, make_uint4(x[0], x[1], x[2], x[3]));
-          }
-          if (a.v_val) {  // quad i belongs to group i / 8
-#pragma unroll
-            for (int h = 0; h < (D == 256 ? 2 : 1); ++h) {
-              const int grp = (lane + 32 * h) >> 3;
-              const uint32_t sc = __shfl_sync(0xffffffffu, (uint32_t)vpar[e], 2 * grp) * 0x10001u;
-              const uint32_t lo = __shfl_sync(0xffffffffu, (uint32_t)vpar[e], 2 * grp + 1) * 0x10001u;
-              const uint32_t q = vq[e][h];
-              uint32_t x[4];
-              // nibbles 0, 1 to one word's halves and 2, 3 to the other's
-              dequant8((q & 0xFu) | ((q & 0xF0u) << 12) | ((q & 0xF00u) >> 4) | ((q & 0xF000u) << 8), sc, lo, x);
-              if (lane + 32 * h < D / 4)
-                store8(a.v_val + (out0 + ds) * D + 4 * (lane + 32 * h), a.wide, make_uint2(x[0], x[1]));
+        for (int e = 0; e < E; ++e) {
+          const int c = c0 + e * NW + warp;
+          if (c < count) {
+            const int ds = done + c;
+            x[e].store(base + rd * row_bytes, voff, ds, at_lane, lane);
+            x[e].values(a.k_val ? a.k_val + (out0 + ds) * D : nullptr, a.v_val ? a.v_val + (out0 + ds) * D : nullptr, a.wide,
+                        lane);
+            if (lane == 0) {
+              wd[ds] = wt[e];
+              if (a.kept) a.kept[out0 + ds] = s_kept[c];
             }
           }
         }
+        __syncthreads();  // the next chunk's reads follow these writes
       }
-      __syncthreads();  // the next chunk's reads follow these writes
     }
     done += count;
   }
   for (int i = a.keep + tid; i < a.n; i += T) wd[i] = 0.f;
-  if (!a.in_place && head == 0 && tid == 0)
+  if (!MOVE && head == 0 && tid == 0)
     a.hole[(size_t)layer * a.MR + rd] = a.keep < a.n ? make_int2(a.keep, a.n) : make_int2(0, 0);
+}
+
+// Move the listed entries between rows: a warp takes kEvictPer of them.
+template <int D>
+__global__ void __launch_bounds__(256) k_kv4_move(const Kv4EvictArgs a) {
+  constexpr int E = kEvictPer, TB = kv4_tile_bytes(D);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int head = blockIdx.y % a.nh, r = blockIdx.y / a.nh, l = blockIdx.z, layer = a.layer0 + l;
+  const size_t SLt = (size_t)a.tiles * kKv4Slots, out0 = (((size_t)l * a.rows + r) * a.nh + head) * a.keep;
+  uint8_t* const base = a.kv4 + ((size_t)layer * a.MR * 2 * a.nh + head) * a.tiles * TB;
+  const size_t row_bytes = (size_t)2 * a.nh * a.tiles * TB, voff = row_bytes / 2;
+  const float* ws = a.wts + (((size_t)layer * a.MR + a.src[r]) * a.nh + head) * SLt;
+  float* wd = a.wts + (((size_t)layer * a.MR + a.dst[r]) * a.nh + head) * SLt;
+  const typename Kv4Entry<D>::At at(lane);
+  const int c0 = (blockIdx.x * 8 + warp) * E;
+  pdl_launch_dependents();
+  pdl_wait();
+  if (c0 >= a.keep) return;
+  int slot = lane < E && c0 + lane < a.keep ? a.list[out0 + c0 + lane] : 0;
+  Kv4Entry<D> x[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const int ss = __shfl_sync(0xffffffffu, slot, e);
+    if (c0 + e < a.keep) x[e].load(base + a.src[r] * row_bytes, voff, ss, at, lane);
+  }
+  if (lane < E && c0 + lane < a.keep) {
+    wd[c0 + lane] = ws[slot];
+    if (a.kept) a.kept[out0 + c0 + lane] = slot;
+  }
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const int ds = c0 + e;
+    if (ds < a.keep) {
+      x[e].store(base + a.dst[r] * row_bytes, voff, ds, at, lane);
+      x[e].values(a.k_val ? a.k_val + (out0 + ds) * D : nullptr, a.v_val ? a.v_val + (out0 + ds) * D : nullptr, a.wide, lane);
+    }
+  }
 }
 
 // The holes of rows that were their own source, whose heads all had to read them.
@@ -1588,22 +1694,50 @@ __global__ void k_kv4_hole(const Kv4EvictArgs a) {
     a.hole[(size_t)(a.layer0 + l) * a.MR + a.dst[r]] = a.keep < a.n ? make_int2(a.keep, a.n) : make_int2(0, 0);
 }
 
+template <int D>
+static cudaError_t launch_evict(Kv4EvictArgs a, bool in_place, cudaStream_t st, bool pdl) {
+  const dim3 grid(a.nh, a.rows, a.layers);
+  if (in_place) {
+    cudaError_t e = launch_kernel(k_kv4_evict<D, true>, grid, dim3(kEvictThreads), 0, st, pdl, a);
+    if (e == cudaSuccess) {
+      k_kv4_hole<<<a.layers, kKv4MaxRows, 0, st>>>(a);
+      e = cudaGetLastError();
+    }
+    return e;
+  }
+  cudaError_t e = launch_kernel(k_kv4_evict<32, false>, grid, dim3(kEvictThreads), 0, st, pdl, a);
+  const int per = 8 * kEvictPer;
+  if (e == cudaSuccess && a.keep)
+    e = launch_kernel(k_kv4_move<D>, dim3((a.keep + per - 1) / per, a.rows * a.nh, a.layers), dim3(256), 0, st, true, a);
+  return e;
+}
+
 cudaError_t launch_kv4_evict(const Kv4EvictArgs& args, cudaStream_t st, bool pdl) {
   Kv4EvictArgs a = args;
-  a.in_place = 0;
-  for (int i = 0; i < a.rows; ++i) a.in_place |= a.src[i] == a.dst[i];
+  bool in_place = false;
+  for (int i = 0; i < a.rows; ++i) in_place = in_place || a.src[i] == a.dst[i];
   a.wide = ((uintptr_t)a.k_val | (uintptr_t)a.v_val) % 16 == 0;
-  const dim3 grid(a.nh, a.rows, a.layers);
-  cudaError_t e = cudaErrorInvalidValue;
-  switch (a.D) {
-    case 32: e = launch_kernel(k_kv4_evict<32>, grid, dim3(kEvictThreads), 0, st, pdl, a); break;
-    case 64: e = launch_kernel(k_kv4_evict<64>, grid, dim3(kEvictThreads), 0, st, pdl, a); break;
-    case 128: e = launch_kernel(k_kv4_evict<128>, grid, dim3(kEvictThreads), 0, st, pdl, a); break;
-    case 256: e = launch_kernel(k_kv4_evict<256>, grid, dim3(kEvictThreads), 0, st, pdl, a); break;
+  // the list holds list_cap slots: as many layers at a time
+  const size_t per_layer = (size_t)a.rows * a.nh * (a.keep ? a.keep : 1);
+  int group = (int)(a.list_cap / per_layer < (size_t)a.layers ? a.list_cap / per_layer : (size_t)a.layers);
+  if (in_place || group < 1) group = a.layers;
+  if (!in_place && per_layer > a.list_cap) return cudaErrorInvalidValue;
+  cudaError_t e = cudaSuccess;
+  for (int l = 0; l < args.layers && e == cudaSuccess; l += group) {
+    a.layer0 = args.layer0 + l;
+    a.layers = args.layers - l < group ? args.layers - l : group;
+    a.kept = args.kept ? args.kept + l * per_layer : nullptr;
+    a.k_val = args.k_val ? args.k_val + l * per_layer * a.D : nullptr;
+    a.v_val = args.v_val ? args.v_val + l * per_layer * a.D : nullptr;
+    switch (a.D) {
+      case 32: e = launch_evict<32>(a, in_place, st, pdl); break;
+      case 64: e = launch_evict<64>(a, in_place, st, pdl); break;
+      case 128: e = launch_evict<128>(a, in_place, st, pdl); break;
+      case 256: e = launch_evict<256>(a, in_place, st, pdl); break;
+      default: e = cudaErrorInvalidValue;
+    }
   }
-  if (e != cudaSuccess || !a.in_place) return e;
-  k_kv4_hole<<<a.layers, kKv4MaxRows, 0, st>>>(a);
-  return cudaGetLastError();
+  return e;
 }
 
 cudaError_t init_kv4_attributes() {
