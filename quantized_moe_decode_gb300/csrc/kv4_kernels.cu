@@ -1398,23 +1398,20 @@ cudaError_t launch_kv4_attn(const Kv4AttnArgs& a, int tokens, cudaStream_t st, b
 }
 
 // ------------------------------------------------------------------ eviction
-// Eight or four fp16 values, in one store where the address allows.
-__device__ __forceinline__ void store16(__half* p, int wide, uint4 v) {
+// N packed words (2 N fp16 values), 16 or 8 bytes at a time where the address allows.
+template <int N>
+__device__ __forceinline__ void store_words(__half* p, int wide, const uint32_t (&w)[N]) {
   if (wide) {
-    *reinterpret_cast<uint4*>(p) = v;
-  } else {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    if constexpr (N % 4 == 0) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) p[j] = __ushort_as_half((unsigned short)(w[j >> 1] >> (16 * (j & 1))));
-  }
-}
-__device__ __forceinline__ void store8(__half* p, int wide, uint2 v) {
-  if (wide) {
-    *reinterpret_cast<uint2*>(p) = v;
-  } else {
-    const uint32_t w[2] = {v.x, v.y};
+      for (int j = 0; j < N; j += 4) reinterpret_cast<uint4*>(p)[j / 4] = make_uint4(w[j], w[j + 1], w[j + 2], w[j + 3]);
+    } else {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) p[j] = __ushort_as_half((unsigned short)(w[j >> 1] >> (16 * (j & 1))));
+      for (int j = 0; j < N; j += 2) reinterpret_cast<uint2*>(p)[j / 2] = make_uint2(w[j], w[j + 1]);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 2 * N; ++j) p[j] = __ushort_as_half((unsigned short)(w[j >> 1] >> (16 * (j & 1))));
   }
 }
 
@@ -1436,79 +1433,181 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 // 16-byte pieces of its tile) and the writes.
 constexpr int kEvictThreads = 512;
 constexpr int kEvictKeys = 4096;  // weights kept in shared memory between the passes
-constexpr int kEvictPer = 4;      // entries of a warp in flight
+constexpr int kEvictPer = 8;      // entries of a moving warp
 
-// An entry in a warp's registers, and the places of a lane's pieces: an entry's
-// pieces lie at a place of its slot plus a place of the piece.
+// Four entries in a warp's registers: lane 8 e + i holds dimensions
+// [i D/8, (i+1) D/8) of entry e (for head_dim 32, keys: eight dimensions in each
+// of four lanes), all of one group.
 template <int D>
-struct Kv4Entry {
-  static constexpr int VQ = D == 256 ? 2 : 1, NG = D / kKv4Group;
-  uint32_t kw, kpar;
-  uint16_t vq[VQ], vpar;
-  struct At {
-    int k, v[VQ], vp;
-    __device__ explicit At(int lane) {
-      k = lane < D / 8 ? kv4_k_word(D, 0, lane) : 0;
-#pragma unroll
-      for (int h = 0; h < VQ; ++h) v[h] = lane + 32 * h < D / 4 ? kv4_v_quad(D, 0, lane + 32 * h) : 0;
-      vp = kv4_v_param(D, 0, lane >> 1, lane & 1) - kv4_v_param(D, 0, 0, 0);
-    }
-  };
-  __device__ __forceinline__ void load(const uint8_t* keys, size_t voff, int slot, const At& at, int lane) {
+struct Kv4Four {
+  static constexpr int KL = D == 32 ? 4 : 8;   // lanes of an entry's keys
+  static constexpr int KW = D / 8 / KL;        // words of eight key codes
+  static constexpr int VW = D / 32;            // tile words that hold a lane's values (of a slot pair)
+  static constexpr int VN = VW < 2 ? 1 : VW / 2;  // words of eight value codes
+  uint32_t k[KW], v[VN], kpar, vpar;  // parameters: scale | minimum << 16
+
+  __device__ __forceinline__ void load(const uint8_t* keys, size_t voff, int slot, int i) {
     const int s = slot & 15;
     const uint8_t* kp = keys + (size_t)(slot >> 4) * kv4_tile_bytes(D);
     const uint8_t* vp = kp + voff;
-    if (lane < D / 8) kw = *reinterpret_cast<const uint32_t*>(kp + kv4_k_word(D, s, 0) + at.k);
-    if (lane < NG) kpar = *reinterpret_cast<const uint32_t*>(kp + kv4_k_param(D, s, 0) + lane * 8);
+    const uint8_t* ka = kp + kv4_k_word(D, s, 0) + (D == 32 ? i * 8 : kv4_stream(D, i >> 1, (i & 1) * (D / 16)));
+    const uint8_t* va = vp + kv4_v_quad(D, s & ~1, 0) + kv4_stream(D, 4 * i, 0);
+    if (KL == 8 || i < KL) load_words(ka, k);
+    uint32_t w[VW];
+    if constexpr (VW == 8) {
+      uint32_t a[4], b[4];
+      load_words(va, a);
+      load_words(va + 512, b);
 #pragma unroll
-    for (int h = 0; h < VQ; ++h)
-      if (lane < D / 4) vq[h] = *reinterpret_cast<const uint16_t*>(vp + kv4_v_quad(D, s, 0) + at.v[h]);
-    if (lane < 2 * NG) vpar = *reinterpret_cast<const uint16_t*>(vp + kv4_v_param(D, s, 0, 0) + at.vp);
+      for (int j = 0; j < 4; ++j) w[j] = a[j], w[4 + j] = b[j];
+    } else {
+      load_words(va, w);
+    }
+    const int kg = D == 32 ? 0 : i * D / 256;
+    kpar = *reinterpret_cast<const uint32_t*>(kp + kv4_k_param(D, s, kg));
+    vpar = (uint32_t)*reinterpret_cast<const uint16_t*>(vp + kv4_v_param(D, s, kg, 0)) |
+           (uint32_t)*reinterpret_cast<const uint16_t*>(vp + kv4_v_param(D, s, kg, 1)) << 16;
+    // this slot's halves of the pair's words
+    const uint32_t sel = (s & 1) ? 0x7632u : 0x5410u;
+    if constexpr (VW == 1) {
+      v[0] = __byte_perm(w[0], 0, (s & 1) ? 0x4432u : 0x4410u);
+    } else {
+#pragma unroll
+      for (int j = 0; j < VN; ++j) v[j] = __byte_perm(w[2 * j], w[2 * j + 1], sel);
+    }
   }
-  __device__ __forceinline__ void store(uint8_t* keys, size_t voff, int slot, const At& at, int lane) const {
-    const int s = slot & 15;
+  // To slots c .. c+3 (c a multiple of 4), `n` of them; the whole warp.
+  __device__ __forceinline__ void store(uint8_t* keys, size_t voff, int c, int n, int lane) const {
+    const int e = lane >> 3, i = lane & 7, slot = c + e, s = slot & 15;
     uint8_t* kp = keys + (size_t)(slot >> 4) * kv4_tile_bytes(D);
     uint8_t* vp = kp + voff;
-    if (lane < D / 8) *reinterpret_cast<uint32_t*>(kp + kv4_k_word(D, s, 0) + at.k) = kw;
-    if (lane < NG) *reinterpret_cast<uint32_t*>(kp + kv4_k_param(D, s, 0) + lane * 8) = kpar;
+    const bool odd = e & 1, pair = (e | 1) < n;
+    // the words of a slot pair hold both slots: one lane of the pair writes the
+    // first half of them, the other the second
+    uint32_t w[VW < 2 ? 1 : VW / 2];
+    if constexpr (VW == 1) {
+      const uint32_t o = __shfl_xor_sync(0xffffffffu, v[0], 8);
+      w[0] = v[0] | o << 16;
+    } else if constexpr (VW == 2) {
+      const uint32_t o = __shfl_xor_sync(0xffffffffu, v[0], 8);
+      w[0] = odd ? __byte_perm(o, v[0], 0x7632) : __byte_perm(v[0], o, 0x5410);
+    } else {
 #pragma unroll
-    for (int h = 0; h < VQ; ++h)
-      if (lane < D / 4) *reinterpret_cast<uint16_t*>(vp + kv4_v_quad(D, s, 0) + at.v[h]) = vq[h];
-    if (lane < 2 * NG) *reinterpret_cast<uint16_t*>(vp + kv4_v_param(D, s, 0, 0) + at.vp) = vpar;
-  }
-  // the values, to [D] arrays (whole warp)
-  __device__ __forceinline__ void values(__half* k_val, __half* v_val, int wide, int lane) const {
-    if (k_val) {  // word w belongs to group w / 4
-      const uint32_t p = __shfl_sync(0xffffffffu, kpar, lane >> 2);
-      uint32_t x[4];
-      dequant8(kw, __byte_perm(p, 0, 0x1010), __byte_perm(p, 0, 0x3232), x);
-      if (lane < D / 8) store16(k_val + 8 * lane, wide, make_uint4(x[0], x[1], x[2], x[3]));
-    }
-    if (v_val) {  // quad i belongs to group i / 8
-#pragma unroll
-      for (int h = 0; h < VQ; ++h) {
-        const int grp = (lane + 32 * h) >> 3;
-        const uint32_t sc = __shfl_sync(0xffffffffu, (uint32_t)vpar, 2 * grp) * 0x10001u;
-        const uint32_t lo = __shfl_sync(0xffffffffu, (uint32_t)vpar, 2 * grp + 1) * 0x10001u;
-        const uint32_t q = vq[h];
-        // nibbles 0 | 1 to bits 0-3 of the halves, 2 | 3 to bits 4-7
-        const uint32_t w = (q & 0xFu) | ((q & 0xF0u) << 12) | ((q & 0xF00u) >> 4) | ((q & 0xF000u) << 8);
-        const uint32_t x0 = hfma2u(sc, hsub2u(lop_and_or(w, 0x000F000Fu, 0x64006400u), 0x64006400u), lo);
-        const uint32_t x1 = hfma2u(sc, hsub2u(lop_and_or(w, 0x00F000F0u, 0x54005400u), 0x54005400u), lo);
-        if (lane < D / 4) store8(v_val + 4 * (lane + 32 * h), wide, make_uint2(x0, x1));
+      for (int j = 0; j < VW / 4; ++j) {
+        const uint32_t mine = odd ? v[VW / 4 + j] : v[j];
+        const uint32_t o = __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[VW / 4 + j], 8);
+        const uint32_t x = odd ? o : mine, y = odd ? mine : o;
+        w[2 * j] = __byte_perm(x, y, 0x5410);
+        w[2 * j + 1] = __byte_perm(x, y, 0x7632);
       }
     }
+    if (e >= n) return;
+    if (KL == 8 || i < KL)
+      store_raw(kp + kv4_k_word(D, s, 0) + (D == 32 ? i * 8 : kv4_stream(D, i >> 1, (i & 1) * (D / 16))), k);
+    if (pair) {
+      uint8_t* va = vp + kv4_v_quad(D, s & ~1, 0) + kv4_stream(D, 4 * i, 0);
+      if constexpr (VW == 1) {
+        if (!odd) store_raw(va, w);
+      } else {
+        store_raw(va + (odd ? (VW == 8 ? 512 : 2 * VW) : 0), w);
+      }
+    } else {  // the last slot, alone: its halves only
+#pragma unroll
+      for (int j = 0; j < VW; ++j)
+        *reinterpret_cast<uint16_t*>(vp + kv4_v_quad(D, s, i * VW + j)) = (uint16_t)(v[j / 2] >> (16 * (j & 1)));
+    }
+    constexpr int LG = D == 32 ? 8 : 256 / D;  // lanes of a group
+    if (i % LG == 0) {
+      const int grp = i / LG;
+      *reinterpret_cast<uint32_t*>(kp + kv4_k_param(D, s, grp)) = kpar;
+      *reinterpret_cast<uint16_t*>(vp + kv4_v_param(D, s, grp, 0)) = (uint16_t)vpar;
+      *reinterpret_cast<uint16_t*>(vp + kv4_v_param(D, s, grp, 1)) = (uint16_t)(vpar >> 16);
+    }
+  }
+  // The values of entry e, to [D] arrays.
+  __device__ __forceinline__ void values(__half* k_val, __half* v_val, int wide, int i) const {
+    if (k_val && (KL == 8 || i < KL)) {
+      const uint32_t sc = __byte_perm(kpar, 0, 0x1010), lo = __byte_perm(kpar, 0, 0x3232);
+      uint32_t x[KW * 4];
+#pragma unroll
+      for (int j = 0; j < KW; ++j) {
+        uint32_t y[4];
+        dequant8(k[j], sc, lo, y);
+#pragma unroll
+        for (int m = 0; m < 4; ++m) x[4 * j + m] = y[m];
+      }
+      store_words(k_val + i * (KW * 8), wide, x);
+    }
+    if (v_val) {
+      const uint32_t sc = __byte_perm(vpar, 0, 0x1010), lo = __byte_perm(vpar, 0, 0x3232);
+      uint32_t x[VW * 2];
+#pragma unroll
+      for (int j = 0; j < VW * 2; ++j) {
+        // a byte in both halves: its low nibble over 1024, its high one over 64
+        const uint32_t b = __byte_perm(v[j / 4], 0, 0x4040 + 0x101 * (j & 3));
+        x[j] = hfma2u(sc, hsub2u(lop_and_or(b, 0x00F0000Fu, 0x54006400u), 0x54006400u), lo);
+      }
+      store_words(v_val + i * (D / 8), wide, x);
+    }
+  }
+
+ private:
+  template <int N>
+  static __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
+    if constexpr (N == 4) {
+      const uint4 u = *reinterpret_cast<const uint4*>(p);
+      w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+    } else if constexpr (N == 2) {
+      const uint2 u = *reinterpret_cast<const uint2*>(p);
+      w[0] = u.x, w[1] = u.y;
+    } else {
+      w[0] = *reinterpret_cast<const uint32_t*>(p);
+    }
+  }
+  template <int N>
+  static __device__ __forceinline__ void store_raw(uint8_t* p, const uint32_t (&w)[N]) {
+    if constexpr (N == 4)
+      *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    else if constexpr (N == 2)
+      *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+    else
+      *reinterpret_cast<uint32_t*>(p) = w[0];
   }
 };
+
+// Counts before this thread's and in all, over a CTA of kEvictThreads.
+__device__ __forceinline__ int block_scan(int mine, int* s_warp, int& all) {
+  constexpr int NW = kEvictThreads / 32;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int up = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, up, o);
+    if (lane >= o) up += v;
+  }
+  if (lane == 31) s_warp[warp] = up;
+  __syncthreads();
+  int w = lane < NW ? s_warp[lane] : 0;
+#pragma unroll
+  for (int o = 1; o < NW; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, w, o);
+    if (lane >= o) w += v;
+  }
+  all = __shfl_sync(0xffffffffu, w, NW - 1);
+  const int before = __shfl_sync(0xffffffffu, w, warp ? warp - 1 : 0);
+  __syncthreads();  // s_warp may be written again
+  return up - mine + (warp ? before : 0);
+}
 
 // MOVE: compact here (a row may be its own source); else list the kept slots.
 template <int D, bool MOVE>
 __global__ void __launch_bounds__(kEvictThreads) k_kv4_evict(const Kv4EvictArgs a) {
-  constexpr int T = kEvictThreads, NW = T / 32, E = kEvictPer, TB = kv4_tile_bytes(D);
+  constexpr int T = kEvictThreads, NW = T / 32, TB = kv4_tile_bytes(D);
+  constexpr int PER = 4, BLOCK = T * PER;  // live entries of a thread and of the CTA at a time
   __shared__ uint32_t s_key[kEvictKeys];
   __shared__ int s_hist[2048];
-  __shared__ int s_warp[2][NW];
-  __shared__ int s_kept[MOVE ? T : 1];
+  __shared__ int s_warp[NW];
+  __shared__ int s_kept[MOVE ? BLOCK : 1];
   __shared__ uint32_t s_prefix;
   __shared__ int s_need;
   const int head = blockIdx.x, r = blockIdx.y, l = blockIdx.z;
@@ -1545,19 +1644,10 @@ __global__ void __launch_bounds__(kEvictThreads) k_kv4_evict(const Kv4EvictArgs 
     }
     __syncthreads();
     // thread t holds the four bins below 2048 - 4t: counts of everything above them
-    int c[4], sum = 0;
+    int c[4], sum = 0, all;
 #pragma unroll
     for (int j = 0; j < 4; ++j) sum += c[j] = s_hist[2047 - 4 * tid - j];
-    int up = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, up, o);
-      if (lane >= o) up += v;
-    }
-    if (lane == 31) s_warp[0][warp] = up;
-    __syncthreads();
-    int above = up - sum;
-    for (int w = 0; w < warp; ++w) above += s_warp[0][w];
+    int above = block_scan(sum, s_warp, all);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {  // the bin that holds the need-th largest
       if (above < need && above + c[j] >= need) {
@@ -1577,66 +1667,65 @@ __global__ void __launch_bounds__(kEvictThreads) k_kv4_evict(const Kv4EvictArgs 
   uint8_t* const base = a.kv4 + ((size_t)layer * a.MR * 2 * a.nh + head) * a.tiles * TB;
   const size_t row_bytes = (size_t)2 * a.nh * a.tiles * TB, voff = row_bytes / 2;
   const size_t out0 = (((size_t)l * a.rows + r) * a.nh + head) * a.keep;
-  const typename Kv4Entry<D>::At at_lane(lane);
   int done = 0, tied = 0;
-  for (int i0 = 0; i0 < live && done < a.keep; i0 += T) {
-    const int i = i0 + tid;
-    bool eq = false, keep = false;
-    if (i < live) {
+  for (int i0 = 0; i0 < live && done < a.keep; i0 += BLOCK) {
+    int eqs = 0, keeps = 0;  // bits of this thread's entries
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      const int i = i0 + tid * PER + j;
+      if (i >= live) continue;
       if (i < a.protect) {
-        keep = true;
+        keeps |= 1 << j;
       } else if (some) {
         const uint32_t k = key_of(i);
-        eq = k == kth;
-        keep = k > kth;
+        if (k == kth) eqs |= 1 << j;
+        if (k > kth) keeps |= 1 << j;
       }
     }
-    const uint32_t below = (1u << lane) - 1u;
-    const uint32_t eqs = __ballot_sync(0xffffffffu, eq);
-    if (lane == 0) s_warp[0][warp] = __popc(eqs);
-    __syncthreads();
-    int before = tied + __popc(eqs & below);
-    for (int w = 0; w < NW; ++w) {
-      if (w < warp) before += s_warp[0][w];
-      tied += s_warp[0][w];
-    }
-    keep = keep || (eq && before < ties);
-    const uint32_t keeps = __ballot_sync(0xffffffffu, keep);
-    if (lane == 0) s_warp[1][warp] = __popc(keeps);
-    __syncthreads();
-    int at = __popc(keeps & below), count = 0;
-    for (int w = 0; w < NW; ++w) {
-      if (w < warp) at += s_warp[1][w];
-      count += s_warp[1][w];
-    }
-    if constexpr (!MOVE) {
-      if (keep) a.list[out0 + done + at] = slot_of(i);
-    } else {
-      if (keep) s_kept[at] = slot_of(i);
-      __syncthreads();
-      for (int c0 = 0; c0 < count; c0 += NW * E) {
-        Kv4Entry<D> x[E];
-        float wt[E];
+    int all, count;
+    int before = tied + block_scan(__popc(eqs), s_warp, all);
+    tied += all;
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const int c = c0 + e * NW + warp;
-          if (c < count) {
-            x[e].load(base + rs * row_bytes, voff, s_kept[c], at_lane, lane);
-            if (lane == 0) wt[e] = ws[s_kept[c]];
-          }
+    for (int j = 0; j < PER; ++j)
+      if (eqs >> j & 1)
+        if (before++ < ties) keeps |= 1 << j;
+    int at = block_scan(__popc(keeps), s_warp, count);
+#pragma unroll
+    for (int j = 0; j < PER; ++j)
+      if (keeps >> j & 1) {
+        const int slot = slot_of(i0 + tid * PER + j);
+        if constexpr (MOVE)
+          s_kept[at++] = slot;
+        else
+          a.list[out0 + done + at++] = slot;
+      }
+    if constexpr (MOVE) {
+      __syncthreads();
+      // kept entry x goes to slot done + x; a warp takes whole groups of four slots
+      const int base0 = done & ~3;
+      for (int c0 = base0; c0 < done + count; c0 += NW * 4) {
+        const int c = c0 + warp * 4, e = lane >> 3;  // slots c .. c+3
+        const int x = c + e - done;
+        const bool in = x >= 0 && x < count;
+        const int slot = in ? s_kept[x] : 0;
+        Kv4Four<D> f;
+        float wt = 0.f;
+        if (in) {
+          f.load(base + rs * row_bytes, voff, slot, lane & 7);
+          wt = ws[slot];
+        } else if (c + e < done) {  // placed by the block before: the pair's words hold it too
+          f.load(base + rd * row_bytes, voff, c + e, lane & 7);
+          wt = wd[c + e];
         }
         __syncthreads();  // the chunk is in registers
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const int c = c0 + e * NW + warp;
-          if (c < count) {
-            const int ds = done + c;
-            x[e].store(base + rd * row_bytes, voff, ds, at_lane, lane);
-            x[e].values(a.k_val ? a.k_val + (out0 + ds) * D : nullptr, a.v_val ? a.v_val + (out0 + ds) * D : nullptr, a.wide,
-                        lane);
-            if (lane == 0) {
-              wd[ds] = wt[e];
-              if (a.kept) a.kept[out0 + ds] = s_kept[c];
+        if (c < done + count) {
+          f.store(base + rd * row_bytes, voff, c, min(4, done + count - c), lane);
+          if (in) {
+            const size_t o = out0 + done + x;
+            f.values(a.k_val ? a.k_val + o * D : nullptr, a.v_val ? a.v_val + o * D : nullptr, a.wide, lane & 7);
+            if ((lane & 7) == 0) {
+              wd[done + x] = wt;
+              if (a.kept) a.kept[o] = slot;
             }
           }
         }
@@ -1650,39 +1739,41 @@ __global__ void __launch_bounds__(kEvictThreads) k_kv4_evict(const Kv4EvictArgs 
     a.hole[(size_t)layer * a.MR + rd] = a.keep < a.n ? make_int2(a.keep, a.n) : make_int2(0, 0);
 }
 
-// Move the listed entries between rows: a warp takes kEvictPer of them.
+// Move the listed entries between rows: a warp takes kEvictPer of them, four at a
+// time, and has all loads of one round in flight before its stores.
 template <int D>
 __global__ void __launch_bounds__(256) k_kv4_move(const Kv4EvictArgs a) {
-  constexpr int E = kEvictPer, TB = kv4_tile_bytes(D);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int F = kEvictPer / 4, TB = kv4_tile_bytes(D);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, e = lane >> 3, i = lane & 7;
   const int head = blockIdx.y % a.nh, r = blockIdx.y / a.nh, l = blockIdx.z, layer = a.layer0 + l;
   const size_t SLt = (size_t)a.tiles * kKv4Slots, out0 = (((size_t)l * a.rows + r) * a.nh + head) * a.keep;
   uint8_t* const base = a.kv4 + ((size_t)layer * a.MR * 2 * a.nh + head) * a.tiles * TB;
   const size_t row_bytes = (size_t)2 * a.nh * a.tiles * TB, voff = row_bytes / 2;
   const float* ws = a.wts + (((size_t)layer * a.MR + a.src[r]) * a.nh + head) * SLt;
   float* wd = a.wts + (((size_t)layer * a.MR + a.dst[r]) * a.nh + head) * SLt;
-  const typename Kv4Entry<D>::At at(lane);
-  const int c0 = (blockIdx.x * 8 + warp) * E;
+  const int c0 = (blockIdx.x * 8 + warp) * kEvictPer;
   pdl_launch_dependents();
   pdl_wait();
   if (c0 >= a.keep) return;
-  int slot = lane < E && c0 + lane < a.keep ? a.list[out0 + c0 + lane] : 0;
-  Kv4Entry<D> x[E];
+  const int mine = c0 + lane < a.keep && lane < kEvictPer ? a.list[out0 + c0 + lane] : 0;
+  Kv4Four<D> x[F];
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    const int ss = __shfl_sync(0xffffffffu, slot, e);
-    if (c0 + e < a.keep) x[e].load(base + a.src[r] * row_bytes, voff, ss, at, lane);
+  for (int f = 0; f < F; ++f) {
+    const int slot = __shfl_sync(0xffffffffu, mine, 4 * f + e);
+    if (c0 + 4 * f + e < a.keep) x[f].load(base + a.src[r] * row_bytes, voff, slot, i);
   }
-  if (lane < E && c0 + lane < a.keep) {
-    wd[c0 + lane] = ws[slot];
-    if (a.kept) a.kept[out0 + c0 + lane] = slot;
+  if (lane < kEvictPer && c0 + lane < a.keep) {
+    wd[c0 + lane] = ws[mine];
+    if (a.kept) a.kept[out0 + c0 + lane] = mine;
   }
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    const int ds = c0 + e;
-    if (ds < a.keep) {
-      x[e].store(base + a.dst[r] * row_bytes, voff, ds, at, lane);
-      x[e].values(a.k_val ? a.k_val + (out0 + ds) * D : nullptr, a.v_val ? a.v_val + (out0 + ds) * D : nullptr, a.wide, lane);
+  for (int f = 0; f < F; ++f) {
+    const int c = c0 + 4 * f;
+    if (c >= a.keep) break;
+    x[f].store(base + a.dst[r] * row_bytes, voff, c, min(4, a.keep - c), lane);
+    if (c + e < a.keep) {
+      const size_t o = out0 + c + e;
+      x[f].values(a.k_val ? a.k_val + o * D : nullptr, a.v_val ? a.v_val + o * D : nullptr, a.wide, i);
     }
   }
 }
