@@ -9,6 +9,28 @@
 
 namespace uocr {
 
+// One exponential; the argument is in units of log2.
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t hfma2u(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+__device__ __forceinline__ uint32_t hsub2u(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+
 // ------------------------------------------------------------------ append
 // cos and sin of a in double: a is reduced by the nearest multiple of pi/2 in
 // two steps and the remainder, at most pi/4, goes through the Taylor series up
@@ -88,12 +110,28 @@ __device__ __forceinline__ void load8(const void* p, long long at, float (&x)[8]
 // read neighbouring entries.
 __device__ __forceinline__ int turn_at(int j) { return (j & 7) * 17 + (j >> 3); }
 
-// Dimensions d .. d+7 of a vector at `base`, rotated: (x, y) -> (x c - y s,
-// y c + x s), the products and the sum each rounded to fp32.
+// Dimensions d .. d+7 of a vector at `base`, and their partners in the rotation
+// where those are not among them.
 template <int DT, bool VEC>
-__device__ __forceinline__ void load8_rotated(const void* p, long long base, int d, const Kv4AppendArgs& a,
-                                              const float2* cs, float (&x)[8]) {
+__device__ __forceinline__ void load8_pairs(const void* p, long long base, int d, const Kv4AppendArgs& a, float (&x)[8],
+                                            float (&y)[8]) {
   load8<DT, VEC>(p, base + d, x);
+  const int rd = a.rope_dims, half = rd >> 1;
+  if (a.rope_layout == 1 || d >= rd) return;
+  if ((half & 7) == 0) {  // the partners are eight neighbours too
+    load8<DT, VEC>(p, base + (d < half ? d + half : d - half), y);
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int i = d + j;
+    y[j] = i < rd ? load_elem(p, DT, base + (i < half ? i + half : i - half)) : 0.f;
+  }
+}
+
+// The rotation: (x, y) -> (x c - y s, y c + x s), the products and the sum each
+// rounded to fp32.
+__device__ __forceinline__ void rotate8(int d, const Kv4AppendArgs& a, const float2* cs, float (&x)[8], const float (&y)[8]) {
   const int rd = a.rope_dims, half = rd >> 1;
   if (d >= rd) return;
   if (a.rope_layout == 1) {
@@ -107,16 +145,14 @@ __device__ __forceinline__ void load8_rotated(const void* p, long long base, int
       }
     return;
   }
-  if ((half & 7) == 0) {  // the partners are eight neighbours too
+  if ((half & 7) == 0) {
     const bool lo = d < half;
-    const int o = lo ? d + half : d - half, c = lo ? d : d - half;
-    float y[8];
-    load8<DT, VEC>(p, base + o, y);
+    const int c = lo ? d : d - half;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const float2 r = cs[turn_at(c + j)];
-      const float u = __fmul_rn(x[j], r.x), v = __fmul_rn(y[j], r.y);
-      x[j] = lo ? __fsub_rn(u, v) : __fadd_rn(u, v);
+      const float v = __fmul_rn(y[j], r.y);
+      x[j] = __fadd_rn(__fmul_rn(x[j], r.x), lo ? -v : v);
     }
     return;
   }
@@ -126,18 +162,38 @@ __device__ __forceinline__ void load8_rotated(const void* p, long long base, int
     if (i >= rd) break;
     const bool lo = i < half;
     const float2 r = cs[turn_at(lo ? i : i - half)];
-    const float u = __fmul_rn(x[j], r.x), v = __fmul_rn(load_elem(p, DT, base + (lo ? i + half : i - half)), r.y);
-    x[j] = lo ? __fsub_rn(u, v) : __fadd_rn(u, v);
+    const float v = __fmul_rn(y[j], r.y);
+    x[j] = __fadd_rn(__fmul_rn(x[j], r.x), lo ? -v : v);
   }
+}
+
+// clamp(rint((x - m) / s), 0, 15) of eight values, in the low bits of c.  The
+// quotient is taken as a product with 1/s: it is off by a few units of 2^-23 of
+// at most 15, so only a quotient that close to a half can round another way, and
+// those are divided.
+__device__ __forceinline__ void codes8(const float (&x)[8], float s, float m, uint32_t (&c)[8]) {
+  constexpr float kRound = 12582912.f;  // 1.5 2^23: adding it rounds to an integer, in the low bits
+  const float r = s > 0.f ? 1.0f / s : 0.f;
+  float far = 0.f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float t = fminf(fmaxf((x[j] - m) * r, 0.f), 15.f);
+    const float u = t + kRound;
+    far = fmaxf(far, fabsf(t - (u - kRound)));
+    c[j] = __float_as_uint(u) & 15u;
+  }
+  if (far > 0.4999f)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) c[j] = kv4_code(x[j], s, m);
 }
 
 // One CTA per token; a thread takes eight dimensions of a key, value or query
 // vector, four neighbouring lanes a group of 32.  What it cannot do without is
 // reading the projections once and writing queries and entries; the rest is
-// arithmetic per element (rotation, two divisions' worth of quantising), so the
-// loads are 16 bytes wide where the addresses allow (VEC).  Double precision
-// runs at 1/64 of the fp32 rate here: a chunk takes its angles from the
-// context's two tables with four operations per pair instead of some forty.
+// arithmetic per element (rotation, quantising), so the loads are 16 bytes wide
+// where the addresses allow (VEC).  Double precision runs at 1/64 of the fp32
+// rate here: a chunk takes its angles from the context's two tables with four
+// operations per pair instead of some forty.
 template <int DT, bool VEC>
 __global__ void __launch_bounds__(1024) k_kv4_append(const Kv4AppendArgs a) {
   __shared__ float2 s_cs[8 * 17];
@@ -171,7 +227,6 @@ __global__ void __launch_bounds__(1024) k_kv4_append(const Kv4AppendArgs a) {
       }
       s_cs[turn_at(j)] = make_float2((float)(a.amp * cs), (float)(a.amp * sn));
     }
-    __syncthreads();
   }
   const int wpv = D >> 3, lw = 31 - __clz(wpv);  // words per vector, a power of two
   uint8_t* row4 = a.kv4 + (size_t)row * 2 * a.nh * a.tiles * kv4_tile_bytes(D);
@@ -180,62 +235,56 @@ __global__ void __launch_bounds__(1024) k_kv4_append(const Kv4AppendArgs a) {
   for (int i0 = 0; i0 < total; i0 += blockDim.x) {
     const int i = i0 + threadIdx.x;
     const int vec = i >> lw, w = i & (wpv - 1);
-    float x[8];
-    if (i >= kv_items) {
-      if (i < total) {
-        const int h = vec - 2 * a.nh;
-        load8_rotated<DT, VEC>(a.q, t * a.ldq + (long long)h * D, 8 * w, a, s_cs, x);
-        float4* o = reinterpret_cast<float4*>(a.q_out + ((size_t)t * a.q_heads + h) * D + 8 * w);
-        if (VEC) {
-          o[0] = make_float4(x[0], x[1], x[2], x[3]);
-          o[1] = make_float4(x[4], x[5], x[6], x[7]);
-        } else {
+    const bool is_q = i >= kv_items, is_v = !is_q && vec >= a.nh, turn = a.rotate && !is_v;
+    const int head = is_q ? vec - 2 * a.nh : is_v ? vec - a.nh : vec;
+    float x[8], y[8];
+    if (i < total) {
+      const void* src = is_q ? a.q : is_v ? a.v : a.k;
+      const long long base = is_q ? t * a.ldq + (long long)head * D : is_v ? t * a.ldv + head * a.lhk : t * a.ldk + head * a.lhk;
+      if (turn)
+        load8_pairs<DT, VEC>(src, base, 8 * w, a, x, y);
+      else
+        load8<DT, VEC>(src, base + 8 * w, x);
+    }
+    if (i0 == 0) __syncthreads();  // the angles (the loads are under way)
+    if (i < total && turn) rotate8(8 * w, a, s_cs, x, y);
+    if (is_q && i < total) {
+      float4* o = reinterpret_cast<float4*>(a.q_out + ((size_t)t * a.q_heads + head) * D + 8 * w);
+      if (VEC) {
+        o[0] = make_float4(x[0], x[1], x[2], x[3]);
+        o[1] = make_float4(x[4], x[5], x[6], x[7]);
+      } else {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) reinterpret_cast<float*>(o)[j] = x[j];
-        }
+        for (int j = 0; j < 8; ++j) reinterpret_cast<float*>(o)[j] = x[j];
       }
     }
-    const bool in = i < kv_items;
-    if (!__any_sync(0xffffffffu, in)) continue;
-    const int kv = vec >= a.nh, head = kv ? vec - a.nh : vec;
-    float mn = INFINITY, mx = -INFINITY;
-    bool ok = true;
-    if (in) {
-      if (kv)
-        load8<DT, VEC>(a.v, t * a.ldv + head * a.lhk + 8 * w, x);
-      else if (a.rotate)
-        load8_rotated<DT, VEC>(a.k, t * a.ldk + head * a.lhk, 8 * w, a, s_cs, x);
-      else
-        load8<DT, VEC>(a.k, t * a.ldk + head * a.lhk + 8 * w, x);
+    if (!__any_sync(0xffffffffu, !is_q)) continue;
+    float mn = x[0], mx = x[0], z = 0.f;  // z: NaN if any value is one, or infinite
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        mn = fminf(mn, x[j]);
-        mx = fmaxf(mx, x[j]);
-        ok = ok && fabsf(x[j]) <= 65504.f;
-      }
+    for (int j = 0; j < 8; ++j) {
+      mn = fminf(mn, x[j]);
+      mx = fmaxf(mx, x[j]);
+      z = fmaf(x[j], 0.f, z);
     }
 #pragma unroll
     for (int o = 1; o < 4; o <<= 1) {
       mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-      ok = __shfl_xor_sync(0xffffffffu, (int)ok, o) && ok;
+      z += __shfl_xor_sync(0xffffffffu, z, o);
     }
-    if (!in) continue;
+    if (is_q) continue;
     __half sc, lo;
-    kv4_params(mn, mx, ok, sc, lo);
-    const float sf = __half2float(sc), mf = __half2float(lo);
+    kv4_params(mn, mx, z == 0.f && mn >= -65504.f && mx <= 65504.f, sc, lo);
     uint32_t c[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) c[j] = kv4_code(x[j], sf, mf);
-    __half* val = kv ? a.v_val : a.k_val;
+    codes8(x, __half2float(sc), __half2float(lo), c);
+    __half* val = is_v ? a.v_val : a.k_val;
     if (val) {
       val += ((size_t)t * a.nh + head) * D + 8 * w;
       uint32_t v[4];
+      const uint32_t s2 = __half_as_ushort(sc) * 0x10001u, m2 = __half_as_ushort(lo) * 0x10001u;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const __half2 h = __halves2half2(kv4_value(c[2 * j], sc, lo), kv4_value(c[2 * j + 1], sc, lo));
-        v[j] = *reinterpret_cast<const uint32_t*>(&h);
-      }
+      for (int j = 0; j < 4; ++j)  // codes to fp16 over the mantissa of 1024
+        v[j] = hfma2u(s2, hsub2u(0x64006400u | c[2 * j] | (c[2 * j + 1] << 16), 0x64006400u), m2);
       if (VEC) {
         *reinterpret_cast<uint4*>(val) = make_uint4(v[0], v[1], v[2], v[3]);
       } else {
@@ -244,9 +293,9 @@ __global__ void __launch_bounds__(1024) k_kv4_append(const Kv4AppendArgs a) {
       }
     }
     if (!write) continue;
-    uint8_t* tp = row4 + ((size_t)(kv * a.nh + head) * a.tiles + tile) * kv4_tile_bytes(D);
+    uint8_t* tp = row4 + ((size_t)vec * a.tiles + tile) * kv4_tile_bytes(D);
     const int grp = w >> 2;
-    if (!kv) {
+    if (!is_v) {
       uint32_t word = 0;
 #pragma unroll
       for (int j = 0; j < 8; ++j) word |= c[j] << (4 * ((j >> 1) + 4 * (j & 1)));
@@ -274,9 +323,12 @@ cudaError_t launch_kv4_append(const Kv4AppendArgs& a, int tokens, cudaStream_t s
   auto wide = [&](const void* p, long long ld) { return ((uintptr_t)p | (uintptr_t)(ld * e)) % 16 == 0; };
   const bool vec = wide(a.q, a.ldq) && wide(a.k, a.ldk) && wide(a.v, a.ldv) && a.lhk * e % 16 == 0 &&
                    ((uintptr_t)a.q_out | (uintptr_t)a.k_val | (uintptr_t)a.v_val) % 16 == 0;
-  // few tokens: one round of threads over the vectors, so that a step waits for one load
+  // rounds of at most 256 threads over a token's vectors, evenly filled; few
+  // tokens take one round, so that a step waits for one load
   const int items = (2 * a.nh + a.q_heads) * (a.D / 8);
-  const int threads = tokens >= a.n_sm || items <= 256 ? 256 : items <= 512 ? 512 : 1024;
+  const int most = tokens >= a.n_sm ? 256 : 1024;
+  const int rounds = (items + most - 1) / most;
+  const int threads = ((items + rounds - 1) / rounds + 31) / 32 * 32;
 #define UOCR_APPEND(DT_)                                                                                       \
   return vec ? launch_kernel(k_kv4_append<DT_, true>, dim3(tokens), dim3(threads), 0, st, pdl, a)              \
              : launch_kernel(k_kv4_append<DT_, false>, dim3(tokens), dim3(threads), 0, st, pdl, a);
@@ -486,28 +538,6 @@ struct Attn4 {
   static constexpr bool QREG = D * NT <= 256;  // query fragments in registers, else in shared memory
   static constexpr int QB = QREG ? 0 : NT * (D / 16) * 32 * 8;
 };
-
-// One exponential; the argument is in units of log2.
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ uint32_t hfma2u(uint32_t a, uint32_t b, uint32_t c) {
-  uint32_t d;
-  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
-  return d;
-}
-__device__ __forceinline__ uint32_t hsub2u(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  uint32_t d;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-  return d;
-}
 
 // Four pairs of codes of a word (nibbles 0|4, 1|5, 2|6, 3|7) as fp16 values
 // s q + m: the code is or'ed into the mantissa of 1024 (bits 0-3) or 64 (bits
