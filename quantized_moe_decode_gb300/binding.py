@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+from array import array
 
 import numpy as np
 
@@ -277,8 +278,9 @@ class Context:
         count = len(src_rows)
         if count != len(dst_rows):
             raise ValueError("uocr_kv_evict: src_rows and dst_rows have different lengths")
-        rows = (C.c_int32 * (2 * count + 1))(*src_rows, *dst_rows)
-        at = C.addressof(rows)
+        rows = array("i", src_rows)
+        rows.extend(dst_rows)
+        at = rows.buffer_info()[0]
         self._ck(self.lib.uocr_kv_evict(self.h, layer, count, at, at + 4 * count, n, keep, protect, kept_ptr or None,
                                         k_val_ptr or None, v_val_ptr or None))
 

@@ -191,11 +191,13 @@ __device__ __forceinline__ void codes8(const float (&x)[8], float s, float m, ui
 // vector, four neighbouring lanes a group of 32.  What it cannot do without is
 // reading the projections once and writing queries and entries; the rest is
 // arithmetic per element (rotation, quantising), so the loads are 16 bytes wide
-// where the addresses allow (VEC).  Double precision runs at 1/64 of the fp32
+// where the addresses allow (VEC), and many tokens run five CTAs on an SM (48
+// registers; 2048 tokens of 10 heads: 15.8 us, with four CTAs 17.1, with eight
+// and spills 16.0).  Double precision runs at 1/64 of the fp32
 // rate here: a chunk takes its angles from the context's two tables with four
 // operations per pair instead of some forty.
-template <int DT, bool VEC>
-__global__ void __launch_bounds__(1024) k_kv4_append(const Kv4AppendArgs a) {
+template <int DT, bool VEC, bool MANY>
+__global__ void __launch_bounds__(MANY ? 256 : 1024, MANY ? 5 : 1) k_kv4_append(const Kv4AppendArgs a) {
   __shared__ float2 s_cs[8 * 17];
   pdl_launch_dependents();
   pdl_wait();
@@ -326,17 +328,20 @@ cudaError_t launch_kv4_append(const Kv4AppendArgs& a, int tokens, cudaStream_t s
   // rounds of at most 256 threads over a token's vectors, evenly filled; few
   // tokens take one round, so that a step waits for one load
   const int items = (2 * a.nh + a.q_heads) * (a.D / 8);
-  const int most = tokens >= a.n_sm ? 256 : 1024;
+  const bool many = tokens >= a.n_sm;
+  const int most = many ? 256 : 1024;
   const int rounds = (items + most - 1) / most;
   const int threads = ((items + rounds - 1) / rounds + 31) / 32 * 32;
-#define UOCR_APPEND(DT_)                                                                                       \
-  return vec ? launch_kernel(k_kv4_append<DT_, true>, dim3(tokens), dim3(threads), 0, st, pdl, a)              \
-             : launch_kernel(k_kv4_append<DT_, false>, dim3(tokens), dim3(threads), 0, st, pdl, a);
+#define UOCR_LAUNCH(...) launch_kernel(k_kv4_append<__VA_ARGS__>, dim3(tokens), dim3(threads), 0, st, pdl, a)
+#define UOCR_APPEND(DT_)                                                                                     \
+  return many ? (vec ? UOCR_LAUNCH(DT_, true, true) : UOCR_LAUNCH(DT_, false, true))                         \
+              : (vec ? UOCR_LAUNCH(DT_, true, false) : UOCR_LAUNCH(DT_, false, false));
   switch (a.dtype) {
     case 0: UOCR_APPEND(0)
     case 1: UOCR_APPEND(1)
     case 2: UOCR_APPEND(2)
   }
+#undef UOCR_LAUNCH
 #undef UOCR_APPEND
   return cudaErrorInvalidValue;
 }
@@ -519,21 +524,9 @@ struct Attn4 {
   static constexpr int TILE = 20 * D;             // K codes, V codes, K parameters, V parameters
   // tiles of a warp's step (two independent product chains where the registers
   // allow), steps in its ring, CTAs per SM
-#ifdef A4U
-  static constexpr int U = D * NT <= 128 ? A4U : 1;
-#else
   static constexpr int U = D * NT <= 128 ? 2 : 1;
-#endif
-#ifdef A4S
-  static constexpr int ST = D * NT <= 128 ? A4S : 3;
-#else
   static constexpr int ST = U == 2 || D == 256 ? 3 : 4;
-#endif
-#ifdef A4C
-  static constexpr int CPS = D * NT <= 64 ? A4C + 1 : D * NT <= 128 ? A4C : 2;
-#else
   static constexpr int CPS = D * NT <= 64 ? 4 : D * NT <= 128 ? 3 : 2;
-#endif
   static constexpr int RING = ST * U * TILE;
   static constexpr bool QREG = D * NT <= 256;  // query fragments in registers, else in shared memory
   static constexpr int QB = QREG ? 0 : NT * (D / 16) * 32 * 8;
