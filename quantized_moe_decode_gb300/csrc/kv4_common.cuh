@@ -92,6 +92,31 @@ __device__ __forceinline__ void store_elem(void* p, int dtype, long long i, floa
   }
 }
 
+// 32 neighbouring elements (fp32 bit patterns) from element i of an array, 16
+// bytes at a time where it is aligned (wide) and i is a multiple of 8.
+__device__ __forceinline__ void store32(void* p, int dtype, int wide, long long i, const uint32_t (&x)[32]) {
+  if (!wide) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) store_elem(p, dtype, i + j, __uint_as_float(x[j]));
+  } else if (dtype == 0) {
+    uint4* o = reinterpret_cast<uint4*>(reinterpret_cast<float*>(p) + i);
+#pragma unroll
+    for (int j = 0; j < 32; j += 4) o[j / 4] = make_uint4(x[j], x[j + 1], x[j + 2], x[j + 3]);
+  } else {
+    uint4* o = reinterpret_cast<uint4*>(reinterpret_cast<unsigned short*>(p) + i);
+    uint32_t w[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      unsigned short h[2];
+      store_elem(h, dtype, 0, __uint_as_float(x[2 * j]));
+      store_elem(h, dtype, 1, __uint_as_float(x[2 * j + 1]));
+      w[j] = h[0] | ((uint32_t)h[1] << 16);
+    }
+#pragma unroll
+    for (int j = 0; j < 16; j += 4) o[j / 4] = make_uint4(w[j], w[j + 1], w[j + 2], w[j + 3]);
+  }
+}
+
 // ---- launch arguments
 // Rotate (operator form) and append key / value vectors.
 struct Kv4AppendArgs {
@@ -123,7 +148,7 @@ cudaError_t launch_kv4_append(const Kv4AppendArgs& a, int tokens, cudaStream_t s
 // Zero the entries and weights of slots [slot0, slot0 + n) of a row.
 cudaError_t launch_kv4_zero(const Kv4AppendArgs& a, int row, int slot0, int n, cudaStream_t st);
 
-constexpr int kAttn4MaxParts = 16384;  // (runs that the attention's tiles are cut into) x queries, at most
+constexpr int kAttn4MaxParts = 20480;  // (runs that the attention's tiles are cut into) x queries, at most
 constexpr int kAttn4PartHead = 4;      // floats before a partial's values: maximum, sum
 constexpr int kKv4MaxRows = 64;
 struct Kv4AttnArgs {
@@ -140,7 +165,7 @@ struct Kv4AttnArgs {
   float2* lse;                 // scratch: [tokens][q_heads] (maximum, 1 / sum)
   float* parts;                // scratch: [runs][2][queries][kAttn4PartHead + D]
   int n_runs;                  // set by the launcher; 0: one item per CTA
-  int q_wide;                  // set by the launcher: q is 16-byte aligned
+  int q_wide, out_wide;        // set by the launcher: q and out are 16-byte aligned
   int q_heads, nh, D, P, R, tiles;
   int kv_row0, kv_rstep;       // kv_rstep 0: every token belongs to cache row kv_row0
   int n_sm;
@@ -148,6 +173,10 @@ struct Kv4AttnArgs {
   int* status;
 };
 cudaError_t launch_kv4_attn(const Kv4AttnArgs& a, int tokens, cudaStream_t st, bool pdl);
+// The same for a chunk of many queries per cache head, head_dim up to 128.
+constexpr int kPromptMinQueries = 64;
+cudaError_t launch_kv4_prompt(const Kv4AttnArgs& a, int tokens, cudaStream_t st, bool pdl);
+cudaError_t init_kv4_prompt_attributes();
 
 // Host-visible entries: codes one per byte [nh][n][D], scales and minima
 // [nh][n][D/32], for K and V of one (layer, row).

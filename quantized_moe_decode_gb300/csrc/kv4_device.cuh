@@ -1,0 +1,82 @@
+// Arithmetic that the kernels of the 4-bit cache share: codes to fp16 values, the
+// tiles that a query reads, and how a call's tiles are dealt out.
+#pragma once
+#include <math.h>
+
+#include "kv4_common.cuh"
+
+namespace uocr {
+
+// One exponential; the argument is in units of log2.
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t hfma2u(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+__device__ __forceinline__ uint32_t hsub2u(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+
+// Four pairs of codes of a word (nibbles 0|4, 1|5, 2|6, 3|7) as fp16 values
+// s q + m: the code is or'ed into the mantissa of 1024 (bits 0-3) or 64 (bits
+// 4-7), which is subtracted again, exactly.
+__device__ __forceinline__ void dequant8(uint32_t w, uint32_t s, uint32_t m, uint32_t (&x)[4]) {
+  const uint32_t h = w >> 8;
+  x[0] = hfma2u(s, hsub2u(lop_and_or(w, 0x000F000Fu, 0x64006400u), 0x64006400u), m);
+  x[1] = hfma2u(s, hsub2u(lop_and_or(w, 0x00F000F0u, 0x54005400u), 0x54005400u), m);
+  x[2] = hfma2u(s, hsub2u(lop_and_or(h, 0x000F000Fu, 0x64006400u), 0x64006400u), m);
+  x[3] = hfma2u(s, hsub2u(lop_and_or(h, 0x00F000F0u, 0x54005400u), 0x54005400u), m);
+}
+
+// The slots that queries up to `lim` read, as whole tiles: those of [0, x) and of
+// [y, lim).
+struct TileList {
+  int ta, tb, count;
+  TileList() = default;
+  __device__ TileList(int lim, int2 hole) {
+    const int x = min(hole.x, lim);
+    const bool gap = hole.y > hole.x && lim > hole.x;
+    ta = ((gap ? x : lim) + 15) >> 4;
+    tb = gap ? max(ta, hole.y >> 4) : ta;
+    count = ta + (gap && lim > hole.y ? max(((lim + 15) >> 4) - tb, 0) : 0);
+  }
+  __device__ int operator()(int j) const { return j < ta ? j : tb + (j - ta); }
+};
+
+// How a call's tiles are dealt out: item i has tiles [start(i), start(i) + tiles)
+// of the list, run c the tiles [c per, (c + 1) per).  32 bits hold them: a tile
+// is 640 bytes of cache at least, and a chunk has few items where it has runs.
+struct Attn4Runs {
+  const int* cum;  // [rows + 1] tiles of one head in the rows before (rows), shared memory
+  int nh, uniform, per;
+  __device__ int tiles(int z) const { return cum ? cum[z + 1] - cum[z] : uniform; }
+  __device__ int start(int z, int head) const { return cum ? cum[z] * nh + head * tiles(z) : (z * nh + head) * uniform; }
+};
+
+// Position, and from it the limit, of token t; an invalid one is reported.
+__device__ __forceinline__ int token_limit(const Kv4AttnArgs& a, int t, int2 hole, bool report) {
+  int p = a.pos ? a.pos[t] : a.pos0 + t;
+  if (p < 0 || (hole.y > hole.x && p < hole.y)) {
+    if (report) atomicOr(a.status, kStatusPosition);
+    p = max(p, 0);
+  }
+  return kv_limit(p, a.P, a.R);
+}
+
+// The running maximum before any score: low enough that the first one raises it,
+// and finite, so that masked scores (-infinity) weigh nothing under it.
+constexpr float kNoMax = -1e30f;
+
+}  // namespace uocr

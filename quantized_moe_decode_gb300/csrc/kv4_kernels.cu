@@ -4,32 +4,10 @@
 
 #include <type_traits>
 
-#include "kv4_common.cuh"
+#include "kv4_device.cuh"
 #include "launch.h"
 
 namespace uocr {
-
-// One exponential; the argument is in units of log2.
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ uint32_t hfma2u(uint32_t a, uint32_t b, uint32_t c) {
-  uint32_t d;
-  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
-  return d;
-}
-__device__ __forceinline__ uint32_t hsub2u(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  uint32_t d;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-  return d;
-}
 
 // ------------------------------------------------------------------ append
 // cos and sin of a in double: a is reduced by the nearest multiple of pi/2 in
@@ -532,52 +510,6 @@ struct Attn4 {
   static constexpr int QB = QREG ? 0 : NT * (D / 16) * 32 * 8;
 };
 
-// Four pairs of codes of a word (nibbles 0|4, 1|5, 2|6, 3|7) as fp16 values
-// s q + m: the code is or'ed into the mantissa of 1024 (bits 0-3) or 64 (bits
-// 4-7), which is subtracted again, exactly.
-__device__ __forceinline__ void dequant8(uint32_t w, uint32_t s, uint32_t m, uint32_t (&x)[4]) {
-  const uint32_t h = w >> 8;
-  x[0] = hfma2u(s, hsub2u(lop_and_or(w, 0x000F000Fu, 0x64006400u), 0x64006400u), m);
-  x[1] = hfma2u(s, hsub2u(lop_and_or(w, 0x00F000F0u, 0x54005400u), 0x54005400u), m);
-  x[2] = hfma2u(s, hsub2u(lop_and_or(h, 0x000F000Fu, 0x64006400u), 0x64006400u), m);
-  x[3] = hfma2u(s, hsub2u(lop_and_or(h, 0x00F000F0u, 0x54005400u), 0x54005400u), m);
-}
-
-// The slots that queries up to `lim` read, as whole tiles: those of [0, x) and of
-// [y, lim).
-struct TileList {
-  int ta, tb, count;
-  TileList() = default;
-  __device__ TileList(int lim, int2 hole) {
-    const int x = min(hole.x, lim);
-    const bool gap = hole.y > hole.x && lim > hole.x;
-    ta = ((gap ? x : lim) + 15) >> 4;
-    tb = gap ? max(ta, hole.y >> 4) : ta;
-    count = ta + (gap && lim > hole.y ? max(((lim + 15) >> 4) - tb, 0) : 0);
-  }
-  __device__ int operator()(int j) const { return j < ta ? j : tb + (j - ta); }
-};
-
-// How a call's tiles are dealt out: item i has tiles [start(i), start(i) + tiles)
-// of the list, run c the tiles [c per, (c + 1) per).  32 bits hold them: a tile
-// is 640 bytes of cache at least, and a chunk has few items where it has runs.
-struct Attn4Runs {
-  const int* cum;  // [rows + 1] tiles of one head in the rows before (rows), shared memory
-  int nh, uniform, per;
-  __device__ int tiles(int z) const { return cum ? cum[z + 1] - cum[z] : uniform; }
-  __device__ int start(int z, int head) const { return cum ? cum[z] * nh + head * tiles(z) : (z * nh + head) * uniform; }
-};
-
-// Position, and from it the limit, of token t; an invalid one is reported.
-__device__ __forceinline__ int token_limit(const Kv4AttnArgs& a, int t, int2 hole, bool report) {
-  int p = a.pos ? a.pos[t] : a.pos0 + t;
-  if (p < 0 || (hole.y > hole.x && p < hole.y)) {
-    if (report) atomicOr(a.status, kStatusPosition);
-    p = max(p, 0);
-  }
-  return kv_limit(p, a.P, a.R);
-}
-
 // What the rows of a call read, for the CTAs that share it out.
 struct Attn4Rows {
   int cum[kKv4MaxRows + 1];  // tiles of one head in the rows before
@@ -627,10 +559,6 @@ __device__ __forceinline__ int attn4_runs(const Kv4AttnArgs& a, int tokens, int 
   r.per = max((int)(((unsigned)total + a.n_runs - 1) / (unsigned)a.n_runs), 4);
   return total;
 }
-
-// The running maximum before any score: low enough that the first one raises it,
-// and finite, so that masked scores (-infinity) weigh nothing under it.
-constexpr float kNoMax = -1e30f;
 
 __device__ __forceinline__ void cp_async16u(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -1401,23 +1329,29 @@ static cudaError_t launch_attn4(const Kv4AttnArgs& args, int tokens, cudaStream_
   if (e == cudaSuccess && a.n_runs)
     e = launch_kernel(k_kv4_merge, dim3((unsigned)items, a.kv_rstep ? a.q_heads / a.nh : 4 * NT), dim3(256), 0, st, true,
                       a, tokens, n_z, 4 * NT);
-  if (e == cudaSuccess && a.wts && !a.kv_rstep)
-    e = launch_kernel(k_kv4_track, dim3((a.P + a.R + 127) / 128, a.nh), dim3(128), 0, st, true, a, tokens);
   return e;
 }
 
 cudaError_t launch_kv4_attn(const Kv4AttnArgs& a, int tokens, cudaStream_t st, bool pdl) {
   if (tokens <= 0) return cudaSuccess;
   const int G = a.q_heads / a.nh;
+  // a chunk of many queries: a block dequantised once for 128 of them
+  const bool prompt = !a.kv_rstep && a.D <= 128 && (long long)tokens * G >= kPromptMinQueries;
   // a second group of four queries costs registers: only where they exist
   const bool two = (a.kv_rstep ? G : tokens * G) > 4;
-  switch (a.D) {
-    case 32: return two ? launch_attn4<32, 2>(a, tokens, st, pdl) : launch_attn4<32, 1>(a, tokens, st, pdl);
-    case 64: return two ? launch_attn4<64, 2>(a, tokens, st, pdl) : launch_attn4<64, 1>(a, tokens, st, pdl);
-    case 128: return two ? launch_attn4<128, 2>(a, tokens, st, pdl) : launch_attn4<128, 1>(a, tokens, st, pdl);
-    case 256: return two ? launch_attn4<256, 2>(a, tokens, st, pdl) : launch_attn4<256, 1>(a, tokens, st, pdl);
-  }
-  return cudaErrorInvalidValue;
+  cudaError_t e = cudaErrorInvalidValue;
+#define UOCR_ATTN(D_)                                                                             \
+  case D_:                                                                                        \
+    e = two ? launch_attn4<D_, 2>(a, tokens, st, pdl) : launch_attn4<D_, 1>(a, tokens, st, pdl); \
+    break;
+  if (prompt)
+    e = launch_kv4_prompt(a, tokens, st, pdl);
+  else
+    switch (a.D) { UOCR_ATTN(32) UOCR_ATTN(64) UOCR_ATTN(128) UOCR_ATTN(256) }
+#undef UOCR_ATTN
+  if (e == cudaSuccess && a.wts && !a.kv_rstep)
+    e = launch_kernel(k_kv4_track, dim3((a.P + a.R + 127) / 128, a.nh), dim3(128), 0, st, true, a, tokens);
+  return e;
 }
 
 // ------------------------------------------------------------------ eviction
@@ -1861,6 +1795,7 @@ cudaError_t init_kv4_attributes() {
   if (e == cudaSuccess) e = allow_max_dyn_smem(k_kv4_attn<D_, 2>);
   UOCR_A(32) UOCR_A(64) UOCR_A(128) UOCR_A(256)
 #undef UOCR_A
+  if (e == cudaSuccess) e = init_kv4_prompt_attributes();
   return e;
 }
 

@@ -747,3 +747,89 @@ def test_buffers_aligned_to_their_elements_only(cuda, dim):
             ctx.close()
         for u, v in zip(*got):
             assert torch.equal(u, v) and u.float().abs().sum() > 0
+
+
+def _chunk_reference(q, K, V, start, P, R, hole=(0, 0), sinks=None):
+    """oracle.attend_kv4 of one row's chunk, by whole products: K, V [nh, slots, D]; (out, weights)."""
+    n, qh, D = q.shape
+    nh, SL, _ = K.shape
+    G = qh // nh
+    out, w = np.zeros((n, qh, D)), np.zeros((nh, SL))
+    slots = np.arange(SL)
+    lim = np.array([p + 1 if p < P else P + min(p - P + 1, R) for p in range(start, start + n)])
+    live = (slots[None] < lim[:, None]) & ~((slots >= hole[0]) & (slots < hole[1]))[None]
+    for h in range(qh):
+        s = np.where(live, np.where(live, q[:, h].astype(np.float64) @ np.nan_to_num(K[h // G]).T, 0) / np.sqrt(D), -np.inf)
+        top = s.max(1, keepdims=True)
+        if sinks is not None:
+            top = np.maximum(top, sinks[h // G])
+        e = np.exp(s - top)
+        z = e.sum(1, keepdims=True) + (0 if sinks is None else np.exp(sinks[h // G] - top))
+        out[:, h] = (e / z) @ np.nan_to_num(V[h // G])
+        w[h // G] += (e / z).sum(0)
+    return out, w
+
+
+@pytest.mark.parametrize("dim,nh,n,start,group,P,R,sink,dtype,track,keep", [
+    (32, 16, 500, 0, 1, 700, 20, True, 0, 0, None), (64, 10, 250, 131, 3, 380, 9, False, 0, 1, None),
+    (128, 8, 1000, 0, 1, 1000, 16, False, 0, 0, None), (128, 12, 641, 333, 1, 900, 128, True, 1, 1, 77),
+    (64, 20, 130, 1500, 3, 1600, 40, False, 2, 0, 5), (256, 8, 960, 5, 1, 970, 30, True, 0, 0, None),
+    (32, 40, 64, 800, 3, 860, 10, False, 0, 1, 0), (128, 3, 343, 0, 8, 343, 1, False, 0, 0, None)])
+def test_attend_long_chunks(cuda, dim, nh, n, start, group, P, R, sink, dtype, track, keep):
+    """Enough queries for the kernel that dequantises a block once for 64 of them."""
+    torch = cuda
+    rng = np.random.default_rng(dim + n)
+    cfg = _cfg(head_dim=dim, n_heads=nh, prefix_len=P, ring_len=R, max_rows=1, use_sink=int(sink),
+               kv_track=int(track or keep is not None))
+    ctx = binding.Context(cfg, max_rows=1)
+    nh = cfg.n_heads
+    vals = _fill(ctx, cfg, rng)[0]
+    sinks = rng.standard_normal((1, nh)).astype(np.float32) if sink else None
+    if sink:
+        ctx.uocr_set_sinks(sinks)
+    hole = (0, 0)
+    if keep is not None:
+        w = rng.random((1, nh, P + R)).astype(np.float32)
+        _put_weights(torch, ctx, w)
+        evicted = max(1, start - 10)
+        kept, k, v = _evict(torch, ctx, cfg, 0, [0], [0], evicted, keep, 0)
+        vals[0, 0, :, :keep], vals[0, 1, :, :keep] = k[0, 0], v[0, 0]
+        hole = (keep, evicted)
+        _put_weights(torch, ctx, np.zeros((1, nh, P + R)))
+    q = rng.standard_normal((n, nh * group, dim)).astype(np.float32) * 2
+    want, add = _chunk_reference(q, vals[0, 0], vals[0, 1], start, P, R, hole, None if sinks is None else sinks[0].astype(np.float64))
+    _close(_attend(torch, ctx, cfg, q, chunk=(0, start), dtype=dtype), want, dtype)
+    if cfg.kv_track:
+        _close(_weights(torch, ctx, cfg)[0], add, 0)
+    ctx.close()
+
+
+@pytest.mark.parametrize("dim,nh,n", [(32, 16, 500), (128, 8, 1000), (256, 8, 960)])
+def test_long_chunk_never_sees_later_tokens(cuda, dim, nh, n):
+    torch = cuda
+    rng = np.random.default_rng(dim)
+    cfg = _cfg(head_dim=dim, n_heads=nh, prefix_len=n, ring_len=30, max_rows=1)
+    ctx = binding.Context(cfg, max_rows=1)
+    vals = _fill(ctx, cfg, rng)[0]
+    bad = n - 150  # entries from here on: groups that are NaN, infinite or as before
+    c, s, m = _entries(rng, (nh, n + 30 - bad, dim))
+    m[:, 0::3], s[:, 1::3] = np.nan, np.inf
+    ctx.uocr_kv_write_i4(0, 0, bad, c, s, m, c, s, m)
+    q = rng.standard_normal((n, nh, dim)).astype(np.float32)
+    want, _ = _chunk_reference(q, vals[0, 0], vals[0, 1], 0, n, 30)
+    got = _attend(torch, ctx, cfg, q, chunk=(0, 0))
+    _close(got[:bad], want[:bad], 0)
+    assert np.all(np.isnan(got[bad:]))
+    # one dimension group of one value only: the rest of the output stays as it was
+    ctx.close()
+    ctx = binding.Context(cfg, max_rows=1)
+    vals = _fill(ctx, cfg, rng)[0]
+    k, ks, km, v, vs, vm = (x.copy() for x in _read(ctx, cfg, 0))
+    vm[1, n - 40, 0] = np.nan
+    ctx.uocr_kv_write_i4(0, 0, 0, k, ks, km, v, vs, vm)
+    want, _ = _chunk_reference(q, vals[0, 0], vals[0, 1], 0, n, 30)
+    got = _attend(torch, ctx, cfg, q, chunk=(0, 0))
+    assert np.all(np.isnan(got[n - 40:, 1, :32]))
+    got[n - 40:, 1, :32] = want[n - 40:, 1, :32]
+    _close(got, want, 0)
+    ctx.close()
