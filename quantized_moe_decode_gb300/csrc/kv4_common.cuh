@@ -92,28 +92,23 @@ __device__ __forceinline__ void store_elem(void* p, int dtype, long long i, floa
   }
 }
 
-// 32 neighbouring elements (fp32 bit patterns) from element i of an array, 16
-// bytes at a time where it is aligned (wide) and i is a multiple of 8.
-__device__ __forceinline__ void store32(void* p, int dtype, int wide, long long i, const uint32_t (&x)[32]) {
+// Elements i .. i + 3, i a multiple of 4, in one store where the array is 16-byte
+// aligned (wide).
+__device__ __forceinline__ void store4(void* p, int dtype, int wide, long long i, float4 v) {
   if (!wide) {
-#pragma unroll
-    for (int j = 0; j < 32; ++j) store_elem(p, dtype, i + j, __uint_as_float(x[j]));
+    store_elem(p, dtype, i, v.x);
+    store_elem(p, dtype, i + 1, v.y);
+    store_elem(p, dtype, i + 2, v.z);
+    store_elem(p, dtype, i + 3, v.w);
   } else if (dtype == 0) {
-    uint4* o = reinterpret_cast<uint4*>(reinterpret_cast<float*>(p) + i);
-#pragma unroll
-    for (int j = 0; j < 32; j += 4) o[j / 4] = make_uint4(x[j], x[j + 1], x[j + 2], x[j + 3]);
+    *reinterpret_cast<float4*>(reinterpret_cast<float*>(p) + i) = v;
   } else {
-    uint4* o = reinterpret_cast<uint4*>(reinterpret_cast<unsigned short*>(p) + i);
-    uint32_t w[16];
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      unsigned short h[2];
-      store_elem(h, dtype, 0, __uint_as_float(x[2 * j]));
-      store_elem(h, dtype, 1, __uint_as_float(x[2 * j + 1]));
-      w[j] = h[0] | ((uint32_t)h[1] << 16);
-    }
-#pragma unroll
-    for (int j = 0; j < 16; j += 4) o[j / 4] = make_uint4(w[j], w[j + 1], w[j + 2], w[j + 3]);
+    uint2 h, b;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h.x) : "f"(v.y), "f"(v.x));
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h.y) : "f"(v.w), "f"(v.z));
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(b.x) : "f"(v.y), "f"(v.x));
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(b.y) : "f"(v.w), "f"(v.z));
+    *reinterpret_cast<uint2*>(reinterpret_cast<unsigned short*>(p) + i) = dtype == 1 ? h : b;
   }
 }
 
@@ -173,8 +168,13 @@ struct Kv4AttnArgs {
   int* status;
 };
 cudaError_t launch_kv4_attn(const Kv4AttnArgs& a, int tokens, cudaStream_t st, bool pdl);
-// The same for a chunk of many queries per cache head, head_dim up to 128.
-constexpr int kPromptMinQueries = 64;
+// The same for a chunk of many queries per cache head, head_dim up to 128: from 128
+// queries on, where an item of 128 is full.  This kernel and the other one, in us, 128
+// dimensions, a query per token and cache head: 2048 tokens from 0, ten heads, 43 and
+// 145; 256 from 1792 23 and 44; 128 from 1920 22.9 and 29.3, from 0 15.0 and 14.3; 128
+// from 59872, two heads, 64 and 82; half an item: 64 tokens from 1984, ten heads, 22.1
+// and 23.8, from 0 11.2 and 12.2, but from 59936, two heads, 63 and 48.
+constexpr int kPromptMinQueries = 128;
 cudaError_t launch_kv4_prompt(const Kv4AttnArgs& a, int tokens, cudaStream_t st, bool pdl);
 cudaError_t init_kv4_prompt_attributes();
 

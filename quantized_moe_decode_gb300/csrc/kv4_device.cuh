@@ -79,4 +79,21 @@ __device__ __forceinline__ int token_limit(const Kv4AttnArgs& a, int t, int2 hol
 // and finite, so that masked scores (-infinity) weigh nothing under it.
 constexpr float kNoMax = -1e30f;
 
+// Copies and loads by 32-bit shared-memory address.
+__device__ __forceinline__ void cp_async16u(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async8u(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async4u(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void lds128u(uint32_t p, uint32_t& x, uint32_t& y, uint32_t& z, uint32_t& w) {
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(x), "=r"(y), "=r"(z), "=r"(w) : "r"(p) : "memory");
+}
+__device__ __forceinline__ void lds64u(uint32_t p, uint32_t& x, uint32_t& y) {
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(x), "=r"(y) : "r"(p) : "memory");
+}
+
 }  // namespace uocr

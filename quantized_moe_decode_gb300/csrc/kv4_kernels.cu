@@ -560,19 +560,6 @@ __device__ __forceinline__ int attn4_runs(const Kv4AttnArgs& a, int tokens, int 
   return total;
 }
 
-__device__ __forceinline__ void cp_async16u(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async8u(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void lds128u(uint32_t p, uint32_t& x, uint32_t& y, uint32_t& z, uint32_t& w) {
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(x), "=r"(y), "=r"(z), "=r"(w) : "r"(p) : "memory");
-}
-__device__ __forceinline__ void lds64u(uint32_t p, uint32_t& x, uint32_t& y) {
-  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(x), "=r"(y) : "r"(p) : "memory");
-}
-
 // Add the softmax weights that a row's queries gave to a head's slots, query by
 // query: four slots for every thread of `from, from + stride, ..`.
 __device__ __forceinline__ void add_weights(const Kv4AttnArgs& a, int z, int head, int row, const TileList& tiles, int nq,

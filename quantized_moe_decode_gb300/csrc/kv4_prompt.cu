@@ -3,52 +3,70 @@
 //
 // An item is 128 queries of one head (tokens times the heads that share the cache
 // head); it goes through the slots in blocks of four 16-slot tiles, each
-// dequantised once for all of them:
-//   four warps dequantise a block into the K-major operands of shared memory,
-//     keys [64 slots][D] and values transposed [D][64 slots] (a tile's words hold
-//     eight dimensions of a slot, or one dimension of a slot pair, side by side);
-//   one thread issues S = Q K^T (M 128, N 64) and O += P V (M 128, N D) into
-//     tensor memory, S twice buffered;
-//   eight warps, two threads per query with half of the block's scores each, read
-//     S, keep the softmax (the pair exchanges its maxima), write P to shared
-//     memory, and rescale O in tensor memory when the maximum has grown by 2^8,
+// dequantised once for all of them.  The warps of a CTA have roles, which go through
+// the CTA's items each at its own pace and meet in barriers only:
+//   four warps dequantise a block's keys, four its values, into the K-major operands
+//     of shared memory, keys [64 slots][D] and values transposed [D][64 slots] (a
+//     tile's words hold eight dimensions of a slot, or one dimension of a slot pair,
+//     side by side); at an item's end they put the next item's queries into tensor
+//     memory, so that shared memory feeds the products one operand only;
+//   one warp issues S = Q K^T (M 128, N 64), two blocks ahead, and O += P V (M 128,
+//     N D);
+//   eight warps, a thread per query, in two groups that take the blocks in turn, so
+//     that one's exponentials run while the other waits: a pass over S for the maximum
+//     (the reference goes on from group to group), a pass that writes P into tensor
+//     memory in place of S; O is rescaled there when the maximum has grown by 2^8,
 //     which almost never happens.
 // As in the decode kernel queries and weights are pairs of fp16 numbers (value and
 // remainder), here as two products, which keeps about 22 bits; sums are fp32.
 // The call's blocks are cut into equal runs, one per SM, an item's start counting
 // as kPromptStart blocks; an item that several runs share leaves partials, which a
 // second kernel merges.
-// What it cannot do without are those products (4 M N K of them per block and
-// pass); the softmax of 64 x 128 scores takes about as long on the other pipes.
+// What it cannot do without are those products, 4 M N K of them per block and pass:
+// about 1050 cycles of the tensor pipe for a block of 128 dimensions.  Measured (2048
+// tokens from position 0, ten heads of 128 dimensions: 18 blocks an SM): 43 us with the
+// merge, about 1700 cycles a block (the issuing warp's waits between the products),
+// 7000 until an item's first scores are there, 6000 to 8000 from one item to the next.
 #include "kv4_device.cuh"
 #include "launch.h"
 #include "tc_common.cuh"
 
 namespace uocr {
 
-constexpr int kPromptThreads = 416;  // warps 0-7 softmax, 8-11 dequantising, 12 issues
-constexpr int kPromptStart = 4;      // what an item's start and end take, in blocks
+constexpr int kPromptThreads = 544;  // warps 0-7 softmax, 8-11 keys, 12-15 values, 16 issues
+constexpr int kPromptStart = 4;      // what an item's start and end take, in blocks (3 and 6: 46 and 44.5 us where 4 gives 43)
 constexpr int kPromptMaxZ = 2048;    // query tiles of a call that is cut into runs
 
 template <int D>
 struct Prompt4 {
   static constexpr int M = 128, N = 64;
-  static constexpr int QL = 128, QS = D / 8 * 128;        // bytes between core matrices along K and M/N: queries,
-  static constexpr int KL = 144, KS = D / 8 * KL;         // keys (padded: two bank passes instead of four),
-  static constexpr int VL = 128, VS = N / 8 * 128 + 16;   // values (padded likewise),
-  static constexpr int PL = 128, PS = N / 8 * 128;        // weights
-  static constexpr int QB = M / 8 * QS, KB = N / 8 * KS, VB = D / 8 * VS, PB = M / 8 * PS;
-  static constexpr int Q = 0, K = 2 * QB, V = K + 2 * KB, P = V + 2 * VB, SMEM = P + 2 * PB;
-  static constexpr int COLS = 128 + D <= 256 ? 256 : 512;  // tensor memory columns: S, S, O
-  static constexpr int O = 128;
+  static constexpr int KL = 144, KS = D / 8 * KL;        // bytes between core matrices along K and N: keys
+  static constexpr int VL = 128, VS = N / 8 * 128 + 16;  // (padded for the stores), values (likewise)
+  static constexpr int KB = N / 8 * KS, VB = D / 8 * VS;
+  // a dequantising warp's tiles under way, as they lie in the cache
+  static constexpr int RT = 10 * D, RS = 4, RB = RS * RT;
+  static constexpr int QL = 4 * D + 16;              // bytes between the next item's queries,
+  static constexpr int OW = D < 64 ? D : 64;         // and between pieces of OW dimensions of results
+  static constexpr int OL = 4 * OW + 16;
+  static constexpr int K = 0, V = 2 * KB, R = V + 2 * VB, Q = R + 8 * RB, OUT = Q + M * QL,
+                       SMEM = OUT + M * OL;
+  // tensor memory columns: four blocks' scores, then weights (value, remainder; a tile's
+  // weights in place of its scores), O, queries (value, remainder)
+  static constexpr int COLS = 512, O = 256, TQ = 384;
 };
 
+// Matrix descriptor (smem_desc) of an operand at 16 addr16.
+__device__ __forceinline__ uint64_t operand(uint32_t addr16, uint32_t lbo, uint32_t sbo) {
+  return (uint64_t)(1u << 14 | sbo >> 4) << 32 | (addr16 | lbo >> 4 << 16);
+}
+
 struct PromptBars {
-  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full, pv_done, all_done;
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[4], p_full[4], pv_done[4], q_full[2], q_land[4], all_done;
 };
 
 // Bounded wait: gives up after kSpinLimit polls, or when another role has.
 __device__ __forceinline__ bool prompt_wait(uint64_t* bar, uint32_t parity, volatile int* dead) {
+#pragma unroll 1
   for (uint32_t i = 0; i < kSpinLimit; ++i) {
     if (mbar_try_wait(bar, parity)) return true;
     if ((i & 63u) == 63u && *dead) return false;
@@ -57,39 +75,104 @@ __device__ __forceinline__ bool prompt_wait(uint64_t* bar, uint32_t parity, vola
   return false;
 }
 
-__device__ __forceinline__ void tc_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+// D[tmem] (+)= A[tmem] * B[smem]^T: row r of A in lane r, two numbers to a column.
+__device__ __forceinline__ void tc_mma_f16_t(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                             uint32_t accumulate) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
-      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+// One lane of a warp that is together.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+  return p != 0;
+}
+// Thread t of the warp writes 8 consecutive 32-bit columns of TMEM lane (lane field of taddr) + t.
+__device__ __forceinline__ void tc_st8(uint32_t taddr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+__device__ __forceinline__ void tc_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
 }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// Blocks of query tile z of a chunk (positions rise and do not wrap, so that a
-// query at position p reads p + 1 slots but the evicted ones).
-__device__ __forceinline__ int prompt_blocks(const Kv4AttnArgs& a, int z, int n_queries, int G, int2 hole) {
-  const int last = min((z + 1) * 128, n_queries) - 1;
-  return (TileList(token_limit(a, last / G, hole, false), hole).count + 3) >> 2;
+// u / G: exact while u G < 2^32.
+__device__ __forceinline__ uint32_t over(int G) { return 0xFFFFFFFFu / (uint32_t)G + 1; }
+__device__ __forceinline__ int div_by(int u, int G, uint32_t over_g) { return G == 1 ? u : (int)__umulhi((uint32_t)u, over_g); }
+
+// Blocks of a query tile whose last token is tok (positions rise and do not wrap,
+// so that a query at position p reads p + 1 slots but the evicted ones).
+__device__ __forceinline__ int prompt_blocks(int lim, int2 hole) { return (TileList(lim, hole).count + 3) >> 2; }
+
+// Barriers of the two softmax warps that have the same 32 queries: for both, and
+// from one group of warps to the other.
+__device__ __forceinline__ void pair_sync(int pair) { asm volatile("bar.sync %0, 64;" ::"r"(9 + pair) : "memory"); }
+__device__ __forceinline__ void pair_give(int to, int pair) {
+  asm volatile("bar.arrive %0, 64;" ::"r"(1 + to * 4 + pair) : "memory");
+}
+__device__ __forceinline__ void pair_take(int group, int pair) {
+  asm volatile("bar.sync %0, 64;" ::"r"(1 + group * 4 + pair) : "memory");
 }
 
-// A thread waits at a barrier of the softmax warps.
-__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+// Two numbers as a pair of fp16 values and the pair of their remainders.
+__device__ __forceinline__ void split2(float x, float y, uint32_t& h, uint32_t& e) {
+  h = pack2(x, y);
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+  e = pack2(x - f.x, y - f.y);
+}
+
+// The low n of a tile's 16 bits, n of any sign.
+__device__ __forceinline__ unsigned low_bits(int n) { return (1u << min(max(n, 0), 16)) - 1u; }
+
+// One item's part in a run: blocks [b0, b1) of query tile z of a head.
+struct PromptItem {
+  int z, head, b0, b1, nq;
+  int lim_lo, lim_hi;  // slots that its first and last query read
+  bool inside, whole;  // the item begins inside the run (its second partial); the run has all of it
+};
+
+// Places among all queries of a tile's row, and of the rows every `step` further.
+struct RowWalk {
+  long long off, by, wrap;
+  int rem, G, drem;
+  __device__ RowWalk(const Kv4AttnArgs& a, const PromptItem& x, int row, int step, int G, uint32_t over_g) : G(G) {
+    const int u = x.z * 128 + row, tok = div_by(u, G, over_g), dtok = div_by(step, G, over_g);
+    rem = u - tok * G;
+    drem = step - dtok * G;
+    off = (long long)tok * a.q_heads + x.head * G + rem;
+    by = (long long)dtok * a.q_heads + drem;
+    wrap = a.q_heads - G;
+  }
+  __device__ void next() {
+    off += by;
+    rem += drem;
+    if (rem >= G) {
+      rem -= G;
+      off += wrap;
+    }
+  }
+};
 
 // Cumulated blocks of the query tiles, kPromptStart more for each, for the runs
 // (every thread of a CTA).  An item's blocks follow its start in the list.
 __device__ __forceinline__ int prompt_runs(const Kv4AttnArgs& a, int n_queries, int n_z, int* cum, Attn4Runs& r) {
   const int2 hole = a.hole[a.kv_row0];
   const int G = a.q_heads / a.nh, lane = threadIdx.x & 31;
+  const uint32_t over_g = over(G);
   if (threadIdx.x < 32) {
     int before = 0;
     if (lane == 0) cum[0] = 0;
+#pragma unroll 1
     for (int z0 = 0; z0 < n_z; z0 += 32) {
-      const int z = z0 + lane;
-      int up = z < n_z ? prompt_blocks(a, z, n_queries, G, hole) + kPromptStart : 0;
+      const int z = z0 + lane, last = div_by(min((z + 1) * 128, n_queries) - 1, G, over_g);
+      int up = z < n_z ? prompt_blocks(token_limit(a, last, hole, false), hole) + kPromptStart : 0;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int v = __shfl_up_sync(0xffffffffu, up, o);
@@ -119,25 +202,33 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(const Kv4AttnA
   __shared__ volatile int s_dead;
   __shared__ unsigned s_bad[2][4][8];  // by block parity, tile, chunk of dimensions: slots whose group is not finite
   __shared__ int s_cum[kPromptMaxZ + 1];
-  __shared__ float s_cq[128];
-  __shared__ float s_pair[2][2][128];  // the pair's maxima, by block parity; its sums and NaN masks at the end
+  __shared__ float s_cq[2][128];  // by round parity: a query's factor of its products
+  // by group: the reference of a query's weights, their sum, its NaN chunks
+  __shared__ float s_ref[2][128], s_sum[2][128];
+  __shared__ unsigned s_nan[2][128];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int G = a.q_heads / a.nh, row = a.kv_row0;
+  const uint32_t over_g = over(G);
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars.k_full[i], 4);
       mbar_init(&bars.v_full[i], 4);
       mbar_init(&bars.k_empty[i], 1);
       mbar_init(&bars.v_empty[i], 1);
-      mbar_init(&bars.s_full[i], 1);
+      mbar_init(&bars.q_full[i], 8);
     }
-    mbar_init(&bars.p_full, 8);
-    mbar_init(&bars.pv_done, 1);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&bars.s_full[i], 1);
+      mbar_init(&bars.p_full[i], 4);
+      mbar_init(&bars.pv_done[i], 1);
+      mbar_init(&bars.q_land[i], 1);
+    }
     mbar_init(&bars.all_done, 1);
     fence_mbar_init();
     s_dead = 0;
   }
-  if (warp == 12) {
+  pdl_wait();  // before tensor memory is taken: kernels before may wait for theirs
+  if (warp == 16) {
     tmem_alloc(&s_tmem, C::COLS);
     tmem_relinquish();
   }
@@ -145,8 +236,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(const Kv4AttnA
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
-
-  pdl_wait();
   pdl_launch_dependents();
   const int2 hole = a.hole[row];
   Attn4Runs runs;
@@ -168,374 +257,485 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(const Kv4AttnA
   }
   const size_t v_off = (size_t)a.nh * a.tiles * kv4_tile_bytes(D);
 
-  int it = 0;  // blocks so far: the buffers' and barriers' phases
+  // the next item with blocks in the run
   const int run0 = at;
-  while (at < end) {
-    const int u0 = z * 128, nq = min(128, n_queries - u0);
-    const int lim_lo = token_limit(a, u0 / G, hole, false), lim_hi = token_limit(a, (u0 + nq - 1) / G, hole, false);
-    const TileList tiles(lim_hi, hole);
-    const int blocks = (tiles.count + 3) >> 2;
-    int b0 = 0, b1 = blocks;
-    bool inside = false;  // the item begins inside the run: the run's second partial
-    if (a.n_runs) {
-      const int s = runs.start(z, head) + kPromptStart;
-      b0 = max(at - s, 0);
-      b1 = max(min(end - s, blocks), 0);
-      inside = s > run0;
-      at = s + b1 < end && b1 == blocks ? s + b1 : end;
-    } else {
-      at = end;
-    }
-    if (b0 >= b1) {  // the start only: the blocks are the next run's
+  auto take = [&](PromptItem& x) {
+    while (at < end) {
+      x.z = z, x.head = head;
+      x.nq = min(128, n_queries - z * 128);
+      x.lim_lo = token_limit(a, div_by(z * 128, G, over_g), hole, false);
+      x.lim_hi = token_limit(a, div_by(z * 128 + x.nq - 1, G, over_g), hole, false);
+      const int blocks = prompt_blocks(x.lim_hi, hole);
+      x.b0 = 0, x.b1 = blocks, x.inside = false;
+      if (a.n_runs) {
+        const int s = runs.start(z, head) + kPromptStart;
+        x.b0 = max(at - s, 0);
+        x.b1 = max(min(end - s, blocks), 0);
+        x.inside = s > run0;
+        at = min(s + blocks, end);
+      } else {
+        at = end;
+      }
+      x.whole = x.b0 == 0 && x.b1 == blocks;
       if (++head == a.nh) {
         head = 0;
         ++z;
       }
-      continue;
+      if (x.b0 < x.b1) return true;  // else the start only: the blocks are the next run's
     }
-    const bool whole = b0 == 0 && b1 == blocks;
-    auto first_slot = [&](int j) { return j < tiles.count ? tiles(j) * 16 : 0x7FFFFF00; };
-    auto is_full = [&](int s) { return s + 16 <= lim_lo && (hole.y <= hole.x || s + 16 <= hole.x || s >= hole.y); };
+    return false;
+  };
 
-    // ---- queries: D / 4 lanes to a row, four dimensions each (the last item's
-    // products are done)
-    if (warp < 8) {
-      constexpr int LR = D / 4, RW = 32 / LR, PASSES = 16 / RW;  // lanes of a row, rows of a warp's pass
-      const int c = (lane % LR) * 4;
-      float4 q[PASSES];
-      int tok = (u0 + warp * 16 + lane / LR) / G, rem = u0 + warp * 16 + lane / LR - tok * G;
-#pragma unroll
-      for (int i = 0; i < PASSES; ++i) {
-        q[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (warp * 16 + i * RW + lane / LR < nq) {
-          const float* p = a.q + ((size_t)tok * a.q_heads + head * G + rem) * D + c;
-          q[i] = a.q_wide ? *reinterpret_cast<const float4*>(p) : make_float4(p[0], p[1], p[2], p[3]);
-        }
-        rem += RW;
-        while (rem >= G) {
-          rem -= G;
-          ++tok;
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < PASSES; ++i) {
-        const int r = warp * 16 + i * RW + lane / LR;
-        float4 x = q[i];
-        float mx = fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w)));
-#pragma unroll
-        for (int o = 1; o < LR; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        // 2^-e with e the exponent of the largest magnitude (0 and infinities stay)
-        const int e = mx > 0.f && mx < INFINITY ? min(max((int)(__float_as_uint(mx) >> 23) - 127, -100), 100) : 0;
-        const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-        if (c == 0) s_cq[r] = a.scale * 1.4426950408889634f * __uint_as_float((uint32_t)(127 + e) << 23);
-        x.x *= down, x.y *= down, x.z *= down, x.w *= down;
-        const uint32_t h0 = pack2(x.x, x.y), h1 = pack2(x.z, x.w);
-        const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&h0));
-        const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&h1));
-        unsigned char* o = smem + C::Q + (r >> 3) * C::QS + (c >> 3) * C::QL + (r & 7) * 16 + (c & 7) * 2;
-        *reinterpret_cast<uint2*>(o) = make_uint2(h0, h1);
-        *reinterpret_cast<uint2*>(o + C::QB) = make_uint2(pack2(x.x - f0.x, x.y - f0.y), pack2(x.z - f1.x, x.w - f1.y));
-      }
-      fence_proxy_async_smem();
-    }
-    __syncthreads();
-
-    if (warp >= 8 && warp < 12) {  // ---------------- dequantise: tile n of every block
-      const int n = warp - 8;
-      const uint8_t* kt = a.kv4 + ((size_t)row * 2 * a.nh + head) * a.tiles * kv4_tile_bytes(D);
-      const int kp_off = 8 * D + (g * W + t * W / 4) * 8;
-      const int vp_off = 8 * D + ((g * D / 256) * 4 + t) * 16;
-      uint32_t kc[2 * W], vc[2 * W];
-      uint2 kpar = make_uint2(0u, 0u);
-      uint4 vpar = make_uint4(0u, 0u, 0u, 0u);
-      auto load_codes = [&](const uint8_t* p, uint32_t (&w)[2 * W]) {
-        if constexpr (D == 32) {
-          const uint2 u = *reinterpret_cast<const uint2*>(p + lane * 8);
-          w[0] = u.x, w[1] = u.y;
-        } else {
-#pragma unroll
-          for (int i = 0; i < W / 2; ++i) {
-            const uint4 u = *reinterpret_cast<const uint4*>(p + i * 512 + lane * 16);
-            w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
-          }
-        }
-      };
-      auto fetch = [&](int b) {
-        const int j = b * 4 + n;
-        if (j >= tiles.count) {  // a missing tile: zeros, under weights of zero
-#pragma unroll
-          for (int i = 0; i < 2 * W; ++i) kc[i] = vc[i] = 0u;
-          kpar = make_uint2(0u, 0u);
-          vpar = make_uint4(0u, 0u, 0u, 0u);
-          return;
-        }
-        const uint8_t* k = kt + (size_t)tiles(j) * kv4_tile_bytes(D);
-        load_codes(k, kc);
-        load_codes(k + v_off, vc);
-        kpar = *reinterpret_cast<const uint2*>(k + kp_off);
-        vpar = *reinterpret_cast<const uint4*>(k + v_off + vp_off);
-      };
-      fetch(b0);
-      for (int b = b0, i = it; b < b1; ++b, ++i) {
-        const int s = i & 1;
-        const uint32_t free_parity = (uint32_t)(((i >> 1) - 1) & 1);
-        if (i >= 2 && !prompt_wait(&bars.k_empty[s], free_parity, &s_dead)) break;
-        {  // slot g of the tile's first half, dimensions t D/4 + 8 w .. + 7; g + 8 of the second
-          unsigned char* o = smem + C::K + s * C::KB + 2 * n * C::KS + t * W * C::KL + g * 16;
-          const uint32_t s0 = __byte_perm(kpar.x, 0, 0x1010), m0 = __byte_perm(kpar.x, 0, 0x3232);
-          const uint32_t s1 = __byte_perm(kpar.y, 0, 0x1010), m1 = __byte_perm(kpar.y, 0, 0x3232);
-#pragma unroll
-          for (int w = 0; w < W; ++w) {
-            uint32_t x[4];
-            dequant8(kc[w], s0, m0, x);
-            *reinterpret_cast<uint4*>(o + w * C::KL) = make_uint4(x[0], x[1], x[2], x[3]);
-            dequant8(kc[W + w], s1, m1, x);
-            *reinterpret_cast<uint4*>(o + C::KS + w * C::KL) = make_uint4(x[0], x[1], x[2], x[3]);
-          }
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars.k_full[s]);
-
-        if (i >= 2 && !prompt_wait(&bars.v_empty[s], free_parity, &s_dead)) break;
-        uint32_t bad = 0;
-        const int slot0 = first_slot(b * 4 + n);
-        if (!is_full(slot0) && slot0 < lim_hi) {
-          // slots that no query reads become zeros, and so does a group that is not
-          // finite: the queries that do read it get NaN there
-          const int x = slot0 + 2 * t;
-          auto live = [&](int x) { return x < lim_hi && !(x >= hole.x && x < hole.y); };
-          uint32_t k0 = (live(x) ? 0xFFFFu : 0u) | (live(x + 1) ? 0xFFFF0000u : 0u);
-          uint32_t k1 = (live(x + 8) ? 0xFFFFu : 0u) | (live(x + 9) ? 0xFFFF0000u : 0u);
-          vpar.x &= k0, vpar.y &= k0, vpar.z &= k1, vpar.w &= k1;
-          auto odd = [](uint32_t s, uint32_t m) {
-            return (((s & 0x7C00u) == 0x7C00u || (m & 0x7C00u) == 0x7C00u) ? 1u : 0u) |
-                   (((s & 0x7C000000u) == 0x7C000000u || (m & 0x7C000000u) == 0x7C000000u) ? 2u : 0u);
-          };
-          const uint32_t o0 = odd(vpar.x, vpar.y), o1 = odd(vpar.z, vpar.w);
-          k0 = (o0 & 1 ? 0u : 0xFFFFu) | (o0 & 2 ? 0u : 0xFFFF0000u);
-          k1 = (o1 & 1 ? 0u : 0xFFFFu) | (o1 & 2 ? 0u : 0xFFFF0000u);
-          vpar.x &= k0, vpar.y &= k0, vpar.z &= k1, vpar.w &= k1;
-          bad = (o0 << (2 * t)) | (o1 << (2 * t + 8));
-        }
-        bad |= __shfl_xor_sync(0xffffffffu, bad, 1);
-        bad |= __shfl_xor_sync(0xffffffffu, bad, 2);
-        if (t == 0) s_bad[s][n][g] = bad;
-        {  // dimension g D/8 + 4 q + j of slots 2t, 2t+1 (first half of the tile), 2t+8, 2t+9 (second)
-          unsigned char* o = smem + C::V + s * C::VB + 2 * n * C::VL + t * 4;
-#pragma unroll
-          for (int q = 0; q < W; ++q) {
-            uint32_t x[4], y[4];
-            dequant8(vc[q], vpar.x, vpar.y, x);
-            dequant8(vc[W + q], vpar.z, vpar.w, y);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int d = g * (D / 8) + 4 * q + j;
-              unsigned char* p = o + (d >> 3) * C::VS + (d & 7) * 16;
-              *reinterpret_cast<uint32_t*>(p) = x[j];
-              *reinterpret_cast<uint32_t*>(p + C::VL) = y[j];
-            }
-          }
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars.v_full[s]);
-        if (b + 1 < b1) fetch(b + 1);
-      }
-    } else if (warp == 12) {  // ---------------- issue the products
-      if (lane == 0) {
-        auto scores = [&](int i) {
-          const int s = i & 1;
-          if (!prompt_wait(&bars.k_full[s], (uint32_t)((i >> 1) & 1), &s_dead)) return false;
-          tc_fence_after();
-          const unsigned char* k = smem + C::K + s * C::KB;
-#pragma unroll
-          for (int pass = 0; pass < 2; ++pass)
-#pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks)
-              tc_mma_f16(tmem + s * 64, smem_desc(smem + C::Q + pass * C::QB + ks * 2 * C::QL, C::QL, C::QS),
-                         smem_desc(k + ks * 2 * C::KL, C::KL, C::KS), IDESC_S, (pass | ks) != 0);
-          tc_commit(&bars.s_full[s]);
-          tc_commit(&bars.k_empty[s]);
-          return true;
-        };
-        bool ok = b0 < b1 && scores(it);
-        for (int b = b0, i = it; b < b1 && ok; ++b, ++i) {
-          const int s = i & 1;
-          if (b + 1 < b1) ok = scores(i + 1);
-          ok = ok && prompt_wait(&bars.v_full[s], (uint32_t)((i >> 1) & 1), &s_dead) &&
-               prompt_wait(&bars.p_full, (uint32_t)(i & 1), &s_dead);
-          if (!ok) break;
-          tc_fence_after();
-          const unsigned char* v = smem + C::V + s * C::VB;
-#pragma unroll
-          for (int pass = 0; pass < 2; ++pass)
-#pragma unroll
-            for (int ks = 0; ks < C::N / 16; ++ks)
-              tc_mma_f16(tmem + C::O, smem_desc(smem + C::P + pass * C::PB + ks * 2 * C::PL, C::PL, C::PS),
-                         smem_desc(v + ks * 2 * C::VL, C::VL, C::VS), IDESC_O, b > b0 || (pass | ks) != 0);
-          tc_commit(&bars.pv_done);
-          tc_commit(&bars.v_empty[s]);
-        }
-      }
-    } else {  // ---------------- softmax: two threads per query
-      const int half = warp >> 2, r = (warp & 3) * 32 + lane, u = u0 + r;
-      const bool have = r < nq;
-      const int tok = u / G;
-      const size_t qi = (size_t)tok * a.q_heads + head * G + (u - tok * G);
-      const int lim = have ? token_limit(a, tok, hole, false) : 0;
-      const float cq = s_cq[r];
-      const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-      float m_ref = kNoMax, l = 0.f;
-      unsigned nan_chunks = 0;  // chunks of D/8 dimensions
-      bool ok = true;           // a failed wait: the warp goes on to the barriers only
-      for (int b = b0, i = it; b < b1; ++b, ++i) {
-        const int s = i & 1, j0 = b * 4 + 2 * half;  // this thread's tiles: j0, j0 + 1
-        ok = ok && __all_sync(0xffffffffu, lane != 0 || prompt_wait(&bars.s_full[s], (uint32_t)((i >> 1) & 1), &s_dead));
-        float x[32], mx = kNoMax;
-        const int slot0[2] = {first_slot(j0), first_slot(j0 + 1)};
-        const bool full = is_full(slot0[0]) && is_full(slot0[1]);
-        if (ok) {
-          tc_fence_after();
-          uint32_t raw[32];
-          tc_ld32(lanes + s * 64 + half * 32, raw);
-          tc_wait_ld();
-#pragma unroll
-          for (int j = 0; j < 32; ++j) x[j] = __uint_as_float(raw[j]) * cq;
-          if (!full) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              const int p = slot0[j >> 4] + (j & 15);
-              if (p >= lim || (p >= hole.x && p < hole.y)) x[j] = -INFINITY;
-            }
-          }
-#pragma unroll
-          for (int j = 0; j < 32; ++j) mx = fmaxf(mx, x[j]);
-          if (a.scores && have) {
-            float* so = a.scores + qi * a.tiles * kKv4Slots;
-#pragma unroll
-            for (int j = 0; j < 32; j += 4)
-              if (j0 + (j >> 4) < tiles.count)
-                *reinterpret_cast<float4*>(so + slot0[j >> 4] + (j & 15)) = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
-          }
-        }
-        s_pair[i & 1][half][r] = mx;
-        softmax_sync();
-        mx = fmaxf(mx, s_pair[i & 1][half ^ 1][r]);
-        const bool raise = mx > m_ref + 8.f;
-        const float corr = raise ? ex2(m_ref - mx) : 1.f;
-        if (raise) {
-          m_ref = mx;
-          l *= corr;
-        }
-        // the products that read the last weights and wrote O are done
-        if (i > 0)
-          ok = ok && __all_sync(0xffffffffu, lane != 0 || prompt_wait(&bars.pv_done, (uint32_t)((i - 1) & 1), &s_dead));
-        if (!ok) continue;
-        tc_fence_after();
-        if (b > b0 && __any_sync(0xffffffffu, raise)) {  // O: the thread's pair takes every other 32 columns
+  // Every role goes through the same items at its own pace; the softmax warps load an
+  // item's queries one ahead, so that the first round has no item yet.
+  PromptItem cur, next;
+  cur.z = cur.head = cur.b0 = cur.b1 = cur.nq = cur.lim_lo = cur.lim_hi = 0;
+  cur.inside = cur.whole = false;
+  int it = 0;      // blocks so far: the buffers' and barriers' phases
+  bool ok = true;  // a failed wait: the role does no more (softmax warps go on to their barriers)
+  // By whole warps.  The first try is every lane's and apart from the loop: a wait that
+  // is over takes 90 cycles so, and 320 where lane 0 polls for the others.
+  auto wait = [&](uint64_t* bar, int phase) {
+    if (!__all_sync(0xffffffffu, mbar_try_wait(bar, (uint32_t)(phase & 1))))
+      ok = __all_sync(0xffffffffu, prompt_wait(bar, (uint32_t)(phase & 1), &s_dead)) && ok;
+  };
 #pragma unroll 1
-          for (int c = half * 32; c < D; c += 64) {
-            uint32_t o[32];
-            tc_ld32(lanes + C::O + c, o);
-            tc_wait_ld();
+  for (int round = 0;; ++round) {
+    const bool more = take(next);
+    const TileList tiles(cur.lim_hi, hole);
+    if (warp >= 8 && warp < 16) {  // ---------------- dequantise: the keys, or the values, of tile n of every block
+      const int n = warp & 3;
+      const bool keys = warp < 12;
+      const uint32_t ring = smem_u32(smem + C::R + (warp - 8) * C::RB);
+      unsigned char* const qrow = smem + C::Q + (n * 32 + lane) * C::QL;
+      // copies of codes run three blocks ahead, a group each; an item's first ones start with the item before
+      auto fetch = [&](const PromptItem& x, const TileList& list, int b) {
+        const int j = b * 4 + n;
+        if (b < x.b1 && j < list.count) {
+          const uint8_t* k = a.kv4 + ((size_t)row * 2 * a.nh + x.head) * a.tiles * kv4_tile_bytes(D) + (keys ? 0 : v_off) +
+                             (size_t)list(j) * kv4_tile_bytes(D) + lane * 16;
+          const uint32_t d = ring + (b & (C::RS - 1)) * C::RT + lane * 16;
 #pragma unroll
-            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * corr);
-            tc_st32(lanes + C::O + c, o);
-          }
-          tc_wait_st();
+          for (int p = 0; p < C::RT; p += 512)
+            if (p + lane * 16 < C::RT) cp_async16u(d + p, k + p);
         }
-        unsigned char* po = smem + C::P + (r >> 3) * C::PS + (r & 7) * 16 + half * 4 * C::PL;
-        float sum = 0.f;
+        cp_commit();
+      };
+      if (ok && cur.b0 < cur.b1) {
+        auto load_codes = [&](uint32_t p, uint32_t (&w)[4]) {
+          if constexpr (D == 32)
+            lds64u(p, w[0], w[1]);
+          else
+            lds128u(p, w[0], w[1], w[2], w[3]);
+        };
+        for (int b = cur.b0, i = it; b < cur.b1; ++b, ++i) {
+          cp_wait<C::RS - 2>();
+          __syncwarp();  // every lane's copies have landed, and the last block's slot is read
+          fetch(cur, tiles, b + C::RS - 1);
+          const bool missing = b * 4 + n >= tiles.count;  // such a tile: zeros, under weights of zero
+          const uint32_t raw = ring + (b & (C::RS - 1)) * C::RT, codes = raw + lane * (D == 32 ? 8 : 16);
+          const int s = i & 1;
+          if (i >= 2) wait(keys ? &bars.k_empty[s] : &bars.v_empty[s], (i >> 1) - 1);
+          if (!ok) break;
+          if (keys) {
+            uint2 kpar = make_uint2(0u, 0u);
+            if (!missing) lds64u(raw + 8 * D + (g * W + t * W / 4) * 8, kpar.x, kpar.y);
+            // slot g of the tile's first half, dimensions t D/4 + 8 w .. + 7; g + 8 of the second
+            if constexpr (W == 4) {  // a load has a half's words; half the lanes store theirs in another
+                                     // order, so that a store's eight lanes of a pass meet in no bank
+#pragma unroll 1
+              for (int half = 0; half < 2; ++half) {
+                uint32_t w[4], x[4];
+                load_codes(codes + half * 512, w);
+                const uint32_t par = half ? kpar.y : kpar.x;
+                const uint32_t s0 = __byte_perm(par, 0, 0x1010), m0 = __byte_perm(par, 0, 0x3232);
+                unsigned char* o = smem + C::K + s * C::KB + (2 * n + half) * C::KS + t * W * C::KL + g * 16;
+                const int turn = t & 2;
 #pragma unroll
-        for (int j = 0; j < 32; j += 8) {
-          uint32_t h[4], e[4];
+                for (int q = 0; q < 4; ++q) {
+                  dequant8(turn ? w[q ^ 2] : w[q], s0, m0, x);
+                  *reinterpret_cast<uint4*>(o + (q ^ turn) * C::KL) = make_uint4(x[0], x[1], x[2], x[3]);
+                }
+              }
+            } else {  // one load has both halves' words
+              uint32_t w[4], x[4];
+              load_codes(codes, w);
+              unsigned char* o = smem + C::K + s * C::KB + 2 * n * C::KS + t * W * C::KL + g * 16;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float v0 = ex2(x[j + 2 * k] - m_ref), v1 = ex2(x[j + 2 * k + 1] - m_ref);
-            sum += v0 + v1;
-            h[k] = pack2(v0, v1);
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[k]));
-            e[k] = pack2(v0 - f.x, v1 - f.y);
+              for (int q = 0; q < 2 * W; ++q) {
+                const uint32_t par = q < W ? kpar.x : kpar.y;
+                dequant8(w[q], __byte_perm(par, 0, 0x1010), __byte_perm(par, 0, 0x3232), x);
+                *reinterpret_cast<uint4*>(o + (q / W) * C::KS + (q % W) * C::KL) = make_uint4(x[0], x[1], x[2], x[3]);
+              }
+            }
+          } else {
+            uint4 vpar = make_uint4(0u, 0u, 0u, 0u);
+            if (!missing) lds128u(raw + 8 * D + ((g * D / 256) * 4 + t) * 16, vpar.x, vpar.y, vpar.z, vpar.w);
+            uint32_t bad = 0;
+            const int slot0 = missing ? 0x7FFFFF00 : tiles(b * 4 + n) * 16;
+            const bool is_full = slot0 + 16 <= cur.lim_lo && (hole.y <= hole.x || slot0 + 16 <= hole.x || slot0 >= hole.y);
+            if (!is_full && slot0 < cur.lim_hi) {
+              // slots that no query reads become zeros, and so does a group that is not
+              // finite: the queries that do read it get NaN there
+              const int x = slot0 + 2 * t;
+              auto live = [&](int x) { return x < cur.lim_hi && !(x >= hole.x && x < hole.y); };
+              uint32_t k0 = (live(x) ? 0xFFFFu : 0u) | (live(x + 1) ? 0xFFFF0000u : 0u);
+              uint32_t k1 = (live(x + 8) ? 0xFFFFu : 0u) | (live(x + 9) ? 0xFFFF0000u : 0u);
+              vpar.x &= k0, vpar.y &= k0, vpar.z &= k1, vpar.w &= k1;
+              auto odd = [](uint32_t s, uint32_t m) {
+                return (((s & 0x7C00u) == 0x7C00u || (m & 0x7C00u) == 0x7C00u) ? 1u : 0u) |
+                       (((s & 0x7C000000u) == 0x7C000000u || (m & 0x7C000000u) == 0x7C000000u) ? 2u : 0u);
+              };
+              const uint32_t o0 = odd(vpar.x, vpar.y), o1 = odd(vpar.z, vpar.w);
+              k0 = (o0 & 1 ? 0u : 0xFFFFu) | (o0 & 2 ? 0u : 0xFFFF0000u);
+              k1 = (o1 & 1 ? 0u : 0xFFFFu) | (o1 & 2 ? 0u : 0xFFFF0000u);
+              vpar.x &= k0, vpar.y &= k0, vpar.z &= k1, vpar.w &= k1;
+              bad = (o0 << (2 * t)) | (o1 << (2 * t + 8));
+            }
+            bad |= __shfl_xor_sync(0xffffffffu, bad, 1);
+            bad |= __shfl_xor_sync(0xffffffffu, bad, 2);
+            if (t == 0) s_bad[s][n][g] = bad;
+            // dimension g D/8 + 4 q + j of slots 2t, 2t+1 (first half of the tile), 2t+8, 2t+9 (second);
+            // where g and g + 4 would meet in a bank, one takes the pairs of a word's nibbles the other way round
+            const int turn = D == 128 ? g >> 2 : 0;
+#pragma unroll 1
+            for (int half = 0; half < (W == 4 ? 2 : 1); ++half) {
+              uint32_t w[4], x[4];
+              load_codes(codes + half * 512, w);
+              unsigned char* o = smem + C::V + s * C::VB + 2 * n * C::VL + t * 4;
+              if (half) vpar.x = vpar.z, vpar.y = vpar.w, o += C::VL;
+#pragma unroll
+              for (int q = 0; q < (W == 4 ? 4 : 2 * W); ++q) {
+                if (W < 4 && q == W) vpar.x = vpar.z, vpar.y = vpar.w, o += C::VL;
+                const uint32_t c = turn ? ((w[q] >> 4) & 0x0F0F0F0Fu) | ((w[q] & 0x0F0F0F0Fu) << 4) : w[q];
+                dequant8(c, vpar.x, vpar.y, x);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  const int d = g * (D / 8) + 4 * (q % W) + j;
+                  *reinterpret_cast<uint32_t*>(o + (d >> 3) * C::VS + (d & 7) * 16 + (j & 1 ? -16 : 16) * turn) = x[j];
+                }
+              }
+            }
           }
-          *reinterpret_cast<uint4*>(po + (j >> 3) * C::PL) = make_uint4(h[0], h[1], h[2], h[3]);
-          *reinterpret_cast<uint4*>(po + C::PB + (j >> 3) * C::PL) = make_uint4(e[0], e[1], e[2], e[3]);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(keys ? &bars.k_full[s] : &bars.v_full[s]);
         }
-        l += sum;
-        if (!full) {  // groups that are not finite, once the block's values (and s_bad) are written
-          ok = __all_sync(0xffffffffu, lane != 0 || prompt_wait(&bars.v_full[s], (uint32_t)((i >> 1) & 1), &s_dead));
-          if (!ok) continue;
+      }
+      if (keys && more) {  // the next item's queries n * 32 .. + 31 into shared memory, a row to a lane
+        const int r = n * 32 + lane, rows = min(max(next.nq - n * 32, 0), 32);
+        const float* p = a.q + RowWalk(a, next, r, 1, G, over_g).off * D;
+        if (round) wait(&bars.q_full[(round - 1) & 1], (round - 1) >> 1);  // the last ones are read
+        if (a.q_wide) {
+          fence_proxy_async_smem();
+          if (lane == 0) mbar_expect_tx(&bars.q_land[n], rows * D * 4);
+          __syncwarp();
+          if (lane < rows) bulk_g2s(qrow, p, D * 4, &bars.q_land[n]);
+        } else {
+          if (lane < rows)
+#pragma unroll 4
+            for (int k = 0; k < D; ++k) cp_async4u(smem_u32(qrow) + 4 * k, p + k);
+          cp_commit();
+          cp_wait<0>();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars.q_land[n]);
+        }
+      }
+      if (more) {
+        cp_wait<0>();
+        __syncwarp();  // the ring is the next item's
+        const TileList list(next.lim_hi, hole);
+#pragma unroll 1
+        for (int k = 0; k < C::RS - 1; ++k) fetch(next, list, next.b0 + k);
+      }
+      if (more) {
+        // Scaled to a magnitude about 1, as pairs of fp16 numbers, into tensor memory once the
+        // last products with this item's are done; half of the dimensions each, keys' and values' warps.
+        wait(&bars.q_land[n], round);
+        const bool have = n * 32 + lane < next.nq;
+        float4 top = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int k = 0; k < D / 4; ++k) {
+          const float4 v = *reinterpret_cast<const float4*>(qrow + k * 16);
+          top.x = fmaxf(top.x, fabsf(v.x)), top.y = fmaxf(top.y, fabsf(v.y));
+          top.z = fmaxf(top.z, fabsf(v.z)), top.w = fmaxf(top.w, fabsf(v.w));
+        }
+        const float mx = fmaxf(fmaxf(top.x, top.y), fmaxf(top.z, top.w));
+        // 2^-e with e the exponent of the largest magnitude (0 and infinities stay)
+        const int e = have && mx > 0.f && mx < INFINITY ? min(max((int)(__float_as_uint(mx) >> 23) - 127, -100), 100) : 0;
+        const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+        const int done = it + cur.b1 - cur.b0 - 1;
+        if (cur.b0 < cur.b1) wait(&bars.s_full[done & 3], done >> 2);
+        tc_fence_after();
+        // (the factor before the last one is read: this item's products wait for the weights of the one before)
+        if (keys) s_cq[round & 1][n * 32 + lane] = a.scale * 1.4426950408889634f * __uint_as_float((uint32_t)(127 + e) << 23);
+        const uint32_t tq = tmem + ((uint32_t)(n * 32) << 16) + C::TQ + (keys ? 0 : D / 4);
+        const unsigned char* mine = qrow + (keys ? 0 : D * 2);
+#pragma unroll 1
+        for (int k = 0; k < D / 32; ++k) {  // 16 dimensions: 8 columns
+          uint32_t h[8], l[8];
 #pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            const int c = min(max(lim - slot0[n], 0), 16);  // the query reads the tile's first c slots
-            const unsigned read = (1u << c) - 1u;
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              if (s_bad[s][2 * half + n][k] & read) nan_chunks |= 1u << k;
+          for (int j = 0; j < 4; ++j) {
+            float4 v = *reinterpret_cast<const float4*>(mine + (k * 4 + j) * 16);
+            if (!have) v = make_float4(0.f, 0.f, 0.f, 0.f);
+            split2(v.x * down, v.y * down, h[2 * j], l[2 * j]);
+            split2(v.z * down, v.w * down, h[2 * j + 1], l[2 * j + 1]);
           }
+          tc_st8(tq + k * 8, h);
+          tc_st8(tq + D / 2 + k * 8, l);
         }
-        fence_proxy_async_smem();
+        tc_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars.p_full);
+        if (lane == 0) mbar_arrive(&bars.q_full[round & 1]);
       }
-      // ---- the item's end: the pair's sums together, every other 32 columns each
-      const int n_it = b1 - b0;
-      ok = ok && __all_sync(0xffffffffu, lane != 0 || prompt_wait(&bars.pv_done, (uint32_t)((it + n_it - 1) & 1), &s_dead));
-      softmax_sync();  // the last maxima are read
-      s_pair[0][half][r] = l;
-      s_pair[1][half][r] = __uint_as_float(nan_chunks);
-      softmax_sync();
-      l = s_pair[0][0][r] + s_pair[0][1][r];
-      nan_chunks |= __float_as_uint(s_pair[1][half ^ 1][r]);
-      tc_fence_after();
-      if (ok) {
-        const float sink = whole && a.sink ? a.sink[head] * 1.4426950408889634f : -INFINITY;
-        const float Mx = fmaxf(m_ref, sink), f = ex2(m_ref - Mx);
-        const float L = l * f + (whole && a.sink ? ex2(sink - Mx) : 0.f);
-        const float inv = L == 0.f ? 0.f : 1.f / L, c = whole ? f * inv : 1.f;
-        float* part = a.parts + (((size_t)blockIdx.x * 2 + inside) * 128 + r) * (D + kAttn4PartHead);
-        if (have && half == 0) {
-          if (!whole)
-            *reinterpret_cast<float2*>(part) = make_float2(m_ref, l);
+    } else if (warp == 16) {  // ---------------- issue the products
+      auto same = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };  // known to be the same in every lane
+      const uint32_t tm = same(tmem), kd = same((int)smem_u32(smem + C::K) >> 4), vd = same((int)smem_u32(smem + C::V) >> 4);
+      const int b0 = same(cur.b0), b1 = same(cur.b1);
+      if (b0 < b1) wait(&bars.q_full[(round - 1) & 1], (round - 1) >> 1);
+#pragma unroll 1
+      for (int b = b0 - 2, i = same(it) - 2; b < b1 && ok; ++b, ++i) {  // scores of block b + 2, then values of block b
+        if (b + 2 < b1) {
+          const int s = i & 1, n = (i + 2) & 3;
+          // Block i + 2's scores take the place of the weights of block i - 2, which are used:
+          // block i's values replaced those that they were used with.  (Before an item's
+          // first blocks it is the last item's last values that say so.)
+          if (b >= b0) wait(&bars.v_full[s], i >> 1);
+          wait(&bars.k_full[s], (i + 2) >> 1);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t d = kd + s * (C::KB >> 4), acc = tm + n * 64;
+          if (elect_one()) {
+#pragma unroll
+            for (int pass = 0; pass < 2; ++pass)
+#pragma unroll
+              for (int ks = 0; ks < D / 16; ++ks)
+                tc_mma_f16_t(acc, tm + C::TQ + pass * (D / 2) + ks * 8, operand(d + (ks * 2 * C::KL >> 4), C::KL, C::KS), IDESC_S,
+                             (pass | ks) != 0);
+            tc_commit(&bars.s_full[n]);
+            tc_commit(&bars.k_empty[s]);
+          }
+          __syncwarp();
+        }
+        if (b >= b0) {
+          const int s = i & 1, n = i & 3;
+          if (b + 2 >= b1) wait(&bars.v_full[s], i >> 1);
+          wait(&bars.p_full[n], i >> 2);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t d = vd + s * (C::VB >> 4), p = tm + n * 64, first = b > b0;
+          if (elect_one()) {
+#pragma unroll
+            for (int pass = 0; pass < 2; ++pass)
+#pragma unroll
+              for (int ks = 0; ks < C::N / 16; ++ks)
+                tc_mma_f16_t(tm + C::O, p + ks * 16 + pass * 8, operand(d + (ks * 2 * C::VL >> 4), C::VL, C::VS), IDESC_O,
+                             (pass | ks) != 0 ? 1u : first);
+            tc_commit(&bars.pv_done[n]);
+            tc_commit(&bars.v_empty[s]);
+          }
+          __syncwarp();
+        }
+      }
+    } else {  // ---------------- softmax: a thread per query and block, two groups of warps take the blocks in turn
+      const int group = warp >> 2, pair = warp & 3, r = pair * 32 + lane;
+      const uint32_t lanes = tmem + ((uint32_t)(pair * 32) << 16);
+      const int b0 = cur.b0, b1 = cur.b1;
+      const bool have = r < cur.nq;
+      auto first_slot = [&](int j) { return j < tiles.count ? tiles(j) * 16 : 0x7FFFFF00; };
+      const long long qi = RowWalk(a, cur, r, 1, G, over_g).off;
+      const int lim = have ? token_limit(a, div_by(cur.z * 128 + r, G, over_g), hole, false) : 0;
+      float cq = 0.f, m_ref = kNoMax, l = 0.f;
+      if (b0 < b1) {
+        wait(&bars.q_full[(round - 1) & 1], (round - 1) >> 1);
+        cq = s_cq[(round - 1) & 1][r];
+      }
+      unsigned nan_chunks = 0;  // chunks of D/8 dimensions
+      for (int b = b0 + ((it ^ group) & 1); b < b1; b += 2) {
+        const int i = it + b - b0;  // i & 1 == group
+        const uint32_t sp = lanes + (i & 3) * 64;
+        wait(&bars.s_full[i & 3], i >> 2);
+        // A pass for the maximum and one for the weights, a tile's slots at a time in
+        // short loops: the roles' loops together stay in the instruction caches.
+        float mx = kNoMax;
+        const int slot_lo = first_slot(b * 4), slot_hi = first_slot(b * 4 + 3) + 16;
+        const bool full = slot_hi > 0 && slot_hi <= cur.lim_lo && (hole.y <= hole.x || slot_hi <= hole.x || slot_lo >= hole.y);
+        auto load = [&](int n, float (&x)[16]) {  // products of tile n, in units of 1 / cq
+          uint32_t raw[16];
+          tc_ld16(sp + n * 16, raw);
+          tc_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 16; ++j) x[j] = __uint_as_float(raw[j]);
+          if (!full) {
+            const int s0 = first_slot(b * 4 + n);
+            const unsigned read = low_bits(lim - s0) & (hole.y > hole.x ? low_bits(hole.x - s0) | ~low_bits(hole.y - s0) : ~0u);
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              if (!(read >> j & 1u)) x[j] = -INFINITY;
+          }
+        };
+        if (ok) {
+          tc_fence_after();
+#pragma unroll 1
+          for (int n = 0; n < 4; ++n) {
+            float x[16];
+            load(n, x);
+            float top[4] = {x[0], x[1], x[2], x[3]};  // four chains
+#pragma unroll
+            for (int j = 4; j < 16; ++j) top[j & 3] = fmaxf(top[j & 3], x[j]);
+            mx = fmaxf(mx, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * cq);
+            if (a.scores && have && b * 4 + n < tiles.count) {
+              float* so = a.scores + qi * a.tiles * kKv4Slots + first_slot(b * 4 + n);
+#pragma unroll
+              for (int j = 0; j < 16; j += 4)
+                *reinterpret_cast<float4*>(so + j) = make_float4(x[j] * cq, x[j + 1] * cq, x[j + 2] * cq, x[j + 3] * cq);
+            }
+          }
+        }
+        // the reference goes from block to block, and with it from group to group
+        float ref = kNoMax;
+        if (b > b0) {
+          pair_take(group, pair);
+          ref = s_ref[group ^ 1][r];
+        }
+        const bool raise = mx > ref + 8.f;
+        const float before = ref;
+        if (raise) ref = mx;
+        if (b + 1 < b1) {
+          s_ref[group][r] = ref;
+          pair_give(group ^ 1, pair);
+        }
+        l *= ex2(m_ref - ref);
+        m_ref = ref;
+        // before O changes, the last products with it are done
+        const bool any = b > b0 && __any_sync(0xffffffffu, raise);
+        if (any) wait(&bars.pv_done[(i - 1) & 3], (i - 1) >> 2);
+        if (!ok) continue;
+        if (any) {
+          tc_fence_after();
+          const float corr = ex2(before - ref);
+#pragma unroll 1
+          for (int c = 0; c < D; c += 8) {
+            uint32_t o[8];
+            tc_ld8(lanes + C::O + c, o);
+            tc_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 8; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * corr);
+            tc_st8(lanes + C::O + c, o);
+          }
+        }
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+        for (int n = 0; n < 4; ++n) {
+          float x[16];
+          uint32_t h[8], e[8];
+          load(n, x);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float v0 = ex2(fmaf(x[2 * j], cq, -ref)), v1 = ex2(fmaf(x[2 * j + 1], cq, -ref));
+            sum[j & 3] += v0 + v1;
+            split2(v0, v1, h[j], e[j]);
+          }
+          tc_st8(sp + n * 16, h);
+          tc_st8(sp + n * 16 + 8, e);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        if (!full) {  // groups that are not finite, once the block's values (and s_bad) are written
+          wait(&bars.v_full[group], i >> 1);
+          if (!ok) continue;
+#pragma unroll 1
+          for (int n = 0; n < 4; ++n) {
+            const unsigned read = low_bits(lim - first_slot(b * 4 + n));
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              if (s_bad[group][n][k] & read) nan_chunks |= 1u << k;
+          }
+        }
+        tc_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.p_full[i & 3]);
+      }
+
+      const int done = it + b1 - b0 - 1;  // the item's last block
+      if (b0 < b1) {  // ---- the item's end: the groups' sums together, every other 32 columns each
+        wait(&bars.pv_done[done & 3], done >> 2);
+        pair_sync(pair);  // the last reference is read
+        s_ref[group][r] = m_ref;
+        s_sum[group][r] = l;
+        s_nan[group][r] = nan_chunks;
+        pair_sync(pair);
+        tc_fence_after();
+        const float m_end = s_ref[done & 1][r];
+        l = s_sum[0][r] * ex2(s_ref[0][r] - m_end) + s_sum[1][r] * ex2(s_ref[1][r] - m_end);
+        nan_chunks |= s_nan[group ^ 1][r];
+        const float sink = cur.whole && a.sink ? a.sink[cur.head] * 1.4426950408889634f : -INFINITY;
+        const float Mx = fmaxf(m_end, sink), f = ex2(m_end - Mx);
+        const float L = l * f + (cur.whole && a.sink ? ex2(sink - Mx) : 0.f);
+        const float inv = L == 0.f ? 0.f : 1.f / L, c = cur.whole ? f * inv : 1.f;
+        float* const part = a.parts + ((size_t)blockIdx.x * 2 + cur.inside) * 128 * (D + kAttn4PartHead);
+        if (ok && have && group == 0) {
+          if (!cur.whole)
+            *reinterpret_cast<float2*>(part + r * (D + kAttn4PartHead)) = make_float2(m_end, l);
           else if (a.lse)
             a.lse[qi] = make_float2(Mx, inv);
         }
+        // results go through shared memory, OW dimensions of the pair's rows at a time, so
+        // that neighbouring lanes store neighbouring pieces of a row
+        constexpr int LR = C::OW / 4, RW = 64 / LR;
+        const int c4 = (group * 32 + lane) % LR * 4, first = pair * 32 + (group * 32 + lane) / LR;
 #pragma unroll 1
-        for (int d0 = half * 32; d0 < D; d0 += 64) {
-          uint32_t o[32];
-          tc_ld32(lanes + C::O + d0, o);
-          tc_wait_ld();
-          if (!have) continue;
-#pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            float v = __uint_as_float(o[j]) * c;
-            if (nan_chunks >> ((d0 + j) / (D / 8)) & 1u) v = __int_as_float(0x7FFFFFFF);
-            o[j] = __float_as_uint(v);
-          }
-          if (whole) {
-            store32(a.out, a.out_dtype, a.out_wide, (long long)qi * D + d0, o);
-          } else {
+        for (int d0 = 0; d0 < D; d0 += C::OW) {
+          if (ok && group * 32 < C::OW) {
+            uint32_t o[32];
+            tc_ld32(lanes + C::O + d0 + group * 32, o);
+            tc_wait_ld();
+            float* w = reinterpret_cast<float*>(smem + C::OUT + r * C::OL) + group * 32;
 #pragma unroll
             for (int j = 0; j < 32; j += 4)
-              *reinterpret_cast<uint4*>(part + kAttn4PartHead + d0 + j) = make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+              *reinterpret_cast<float4*>(w + j) = make_float4(__uint_as_float(o[j]) * c, __uint_as_float(o[j + 1]) * c,
+                                                              __uint_as_float(o[j + 2]) * c, __uint_as_float(o[j + 3]) * c);
+            if (nan_chunks)
+#pragma unroll 1
+              for (int j = 0; j < 32; ++j)
+                if (nan_chunks >> ((d0 + group * 32 + j) / (D / 8)) & 1u) w[j] = __int_as_float(0x7FFFFFFF);
+            __syncwarp();
           }
+          tc_fence_before();
+          pair_sync(pair);  // rows are written, and at the end O is read
+          if (ok) {
+            constexpr int PASSES = 32 / RW;
+            float4 v[PASSES];
+            const float* w = reinterpret_cast<const float*>(smem + C::OUT + first * C::OL) + c4;
+#pragma unroll
+            for (int i = 0; i < PASSES; ++i) v[i] = *reinterpret_cast<const float4*>(w + i * RW * (C::OL / 4));
+            if (cur.whole) {
+              RowWalk at(a, cur, first, RW, G, over_g);
+#pragma unroll
+              for (int i = 0; i < PASSES; ++i, at.next())
+                if (first + i * RW < cur.nq) store4(a.out, a.out_dtype, a.out_wide, at.off * D + d0 + c4, v[i]);
+            } else {  // also rows past the last query, which nothing reads
+              float* p = part + first * (D + kAttn4PartHead) + kAttn4PartHead + d0 + c4;
+#pragma unroll
+              for (int i = 0; i < PASSES; ++i) *reinterpret_cast<float4*>(p + i * RW * (D + kAttn4PartHead)) = v[i];
+            }
+          }
+          pair_sync(pair);  // rows are stored
         }
       }
-      tc_fence_before();
     }
-    it += b1 - b0;
-    __syncthreads();
-    tc_fence_after();
-    if (s_dead) break;
-    if (++head == a.nh) {
-      head = 0;
-      ++z;
-    }
+    it += cur.b1 - cur.b0;
+    if (!more) break;
+    cur = next;
   }
+  cp_wait<0>();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
   // no product may still be running when the tensor memory is freed
-  if (warp == 12) {
-    if (lane == 0) {
+  if (warp == 16) {
+    if (elect_one()) {
       tc_commit(&bars.all_done);
       if (!mbar_wait(&bars.all_done, 0)) s_dead = 1;
     }
@@ -550,6 +750,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(const Kv4AttnA
 __global__ void __launch_bounds__(256) k_kv4_prompt_merge(const Kv4AttnArgs a, int n_queries, int n_z) {
   __shared__ int s_cum[kPromptMaxZ + 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, D = a.D, G = a.q_heads / a.nh;
+  const uint32_t over_g = over(G);
   const int z = blockIdx.x / a.nh, head = blockIdx.x % a.nh;
   Attn4Runs runs;
   prompt_runs(a, n_queries, n_z, s_cum, runs);  // positions and holes: written before the attention began
@@ -562,42 +763,32 @@ __global__ void __launch_bounds__(256) k_kv4_prompt_merge(const Kv4AttnArgs a, i
   const size_t step = (size_t)2 * 128 * (D + kAttn4PartHead);
   // a run's second partial is of an item that begins inside it: the first run's, if any
   const size_t shift = s > c0 * runs.per ? step / 2 : 0;
+#pragma unroll 1
   for (int r = blockIdx.y * 16 + warp; r < blockIdx.y * 16 + 16; r += 8) {
     const int u = z * 128 + r;
     if (u >= n_queries) break;
     const float* base = a.parts + c0 * step + (size_t)r * (D + kAttn4PartHead);
-    auto part = [&](int c) { return base + c * step + (c ? 0 : shift); };
-    float m = kNoMax, l = 0.f;
-    for (int c = lane; c < n; c += 32) {
-      const float2 p = *reinterpret_cast<const float2*>(part(c));
-      const float hi = fmaxf(m, p.x);
-      l = l * ex2(m - hi) + p.y * ex2(p.x - hi);
-      m = hi;
-    }
-    float M = m;
-#pragma unroll
-    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    M = fmaxf(M, sink);
-    float L = l * ex2(m - M);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-    if (a.sink) L += ex2(sink - M);
-    const float inv = L == 0.f ? 0.f : 1.f / L;
-    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    float m = kNoMax, L = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
     for (int c = 0; c < n; ++c) {
-      const float* p = part(c);
-      const float f = ex2(p[0] - M);
+      const float* p = base + c * step + (c ? 0 : shift);
+      const float2 head = *reinterpret_cast<const float2*>(p);
+      const float hi = fmaxf(m, head.x), down = ex2(m - hi), f = ex2(head.x - hi);
+      m = hi;
+      L = L * down + head.y * f;
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        if (32 * k < D) v[k] += p[kAttn4PartHead + lane + 32 * k] * f;
+        if (32 * k < D) v[k] = v[k] * down + p[kAttn4PartHead + lane + 32 * k] * f;
     }
-    const int tok = u / G;
+    const float M = fmaxf(m, sink), f = ex2(m - M);
+    L = L * f + (a.sink ? ex2(sink - M) : 0.f);
+    const float inv = L == 0.f ? 0.f : f / L, lse = L == 0.f ? 0.f : 1.f / L;
+    const int tok = div_by(u, G, over_g);
     const long long qi = (long long)tok * a.q_heads + head * G + (u - tok * G);
 #pragma unroll
     for (int k = 0; k < 4; ++k)
       if (32 * k < D) store_elem(a.out, a.out_dtype, qi * D + lane + 32 * k, v[k] * inv);
-    if (a.lse && lane == 0) a.lse[qi] = make_float2(M, inv);
+    if (a.lse && lane == 0) a.lse[qi] = make_float2(M, lse);
   }
 }
 

@@ -804,6 +804,21 @@ def test_attend_long_chunks(cuda, dim, nh, n, start, group, P, R, sink, dtype, t
     ctx.close()
 
 
+@pytest.mark.parametrize("dim,nh,n,start,group,P,R", [(32, 64, 640, 0, 1, 640, 20), (64, 48, 700, 9, 1, 720, 3),
+                                                      (128, 40, 650, 0, 1, 655, 1), (32, 32, 640, 0, 8, 640, 1)])
+def test_attend_chunk_of_many_items(cuda, dim, nh, n, start, group, P, R):
+    """More query tiles than SMs: several, some of them in part, to one CTA; last, so many that each has a CTA."""
+    torch = cuda
+    rng = np.random.default_rng(dim + nh)
+    cfg = _cfg(head_dim=dim, n_heads=nh, prefix_len=P, ring_len=R, max_rows=1)
+    ctx = binding.Context(cfg, max_rows=1)
+    vals = _fill(ctx, cfg, rng)[0]
+    q = rng.standard_normal((n, nh * group, dim)).astype(np.float32) * 2
+    want, _ = _chunk_reference(q, vals[0, 0], vals[0, 1], start, P, R)
+    _close(_attend(torch, ctx, cfg, q, chunk=(0, start)), want, 0)
+    ctx.close()
+
+
 @pytest.mark.parametrize("dim,nh,n", [(32, 16, 500), (128, 8, 1000), (256, 8, 960)])
 def test_long_chunk_never_sees_later_tokens(cuda, dim, nh, n):
     torch = cuda
