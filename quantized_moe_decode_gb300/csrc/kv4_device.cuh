@@ -56,8 +56,8 @@ struct TileList {
 };
 
 // How a call's tiles are dealt out: item i has tiles [start(i), start(i) + tiles)
-// of the list, run c the tiles [c per, (c + 1) per).  32 bits hold them: a tile
-// is 640 bytes of cache at least, and a chunk has few items where it has runs.
+// of the list, run c the tiles [c per, (c + 1) per).  32 bits hold them: a call
+// of 2^30 tiles or more has no runs.
 struct Attn4Runs {
   const int* cum;  // [rows + 1] tiles of one head in the rows before (rows), shared memory
   int nh, uniform, per;

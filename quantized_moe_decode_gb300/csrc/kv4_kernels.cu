@@ -1310,7 +1310,8 @@ static cudaError_t launch_attn4(const Kv4AttnArgs& args, int tokens, cudaStream_
   // last); else a run for every resident warp.
   int ctas = a.n_sm * C::CPS;
   if (ctas * kAttn4Warps * 4 * NT > kAttn4MaxParts) ctas = kAttn4MaxParts / (kAttn4Warps * 4 * NT);
-  a.n_runs = a.tiles <= 16 || (!a.kv_rstep && items >= 2LL * ctas) ? 0 : ctas * kAttn4Warps;
+  const bool countable = items * a.tiles < 1LL << 30;
+  a.n_runs = a.tiles <= 16 || (!a.kv_rstep && items >= 2LL * ctas) || !countable ? 0 : ctas * kAttn4Warps;
   cudaError_t e = launch_kernel(k_kv4_attn<D, NT>, dim3(a.n_runs ? ctas : (unsigned)items), dim3(kAttn4Warps * 32),
                                 (size_t)(part > ring ? part : ring), st, pdl, a, tokens, n_z);
   if (e == cudaSuccess && a.n_runs)

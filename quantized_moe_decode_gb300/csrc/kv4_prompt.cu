@@ -103,7 +103,7 @@ __device__ __forceinline__ void tc_ld8(uint32_t taddr, uint32_t (&r)[8]) {
 }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// u / G: exact while u G < 2^32.
+// u / G, exact for G up to 8 and u below 2^30.
 __device__ __forceinline__ uint32_t over(int G) { return 0xFFFFFFFFu / (uint32_t)G + 1; }
 __device__ __forceinline__ int div_by(int u, int G, uint32_t over_g) { return G == 1 ? u : (int)__umulhi((uint32_t)u, over_g); }
 
@@ -801,7 +801,8 @@ static cudaError_t launch_prompt4(const Kv4AttnArgs& args, int tokens, cudaStrea
   const long long items = (long long)n_z * a.nh;
   // one run per SM, unless there are so many items that their last wave does not show
   const int ctas = a.n_sm * 256 <= kAttn4MaxParts * 2 ? a.n_sm : kAttn4MaxParts * 2 / 256;
-  a.n_runs = items >= 8LL * ctas || n_z > kPromptMaxZ ? 0 : ctas;
+  const bool countable = items * ((a.tiles + 3) / 4 + kPromptStart) < 1LL << 30;
+  a.n_runs = items >= 8LL * ctas || n_z > kPromptMaxZ || !countable ? 0 : ctas;
   cudaError_t e = launch_kernel(k_kv4_prompt<D>, dim3(a.n_runs ? a.n_runs : (unsigned)items), dim3(kPromptThreads),
                                 (size_t)Prompt4<D>::SMEM, st, pdl, a, queries, n_z);
   if (e == cudaSuccess && a.n_runs)

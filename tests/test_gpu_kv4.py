@@ -819,6 +819,63 @@ def test_attend_chunk_of_many_items(cuda, dim, nh, n, start, group, P, R):
     ctx.close()
 
 
+@pytest.mark.parametrize("dim,nh,n,start,group", [(32, 2, 127, 0, 1), (64, 1, 128, 3, 1), (128, 1, 129, 0, 1),
+                                                  (64, 2, 40, 30, 5), (128, 2, 37, 0, 7), (32, 3, 86, 11, 3), (128, 1, 16, 200, 8),
+                                                  (64, 1, 65, 0, 2), (32, 2, 50, 0, 6), (128, 3, 32, 1, 4)])
+@pytest.mark.parametrize("dtype,shift", [(0, 0), (1, 1), (2, 1), (0, 1), (2, 0)])
+def test_attend_chunk_of_any_sharing(cuda, dim, nh, n, start, group, dtype, shift):
+    """Around 128 queries per cache head, any number of heads that share one, aligned and shifted pointers."""
+    torch = cuda
+    rng = np.random.default_rng(dim + n + group)
+    cfg = _cfg(head_dim=dim, n_heads=nh, prefix_len=230, ring_len=5, max_rows=1, use_sink=1)
+    nh = cfg.n_heads
+    ctx = binding.Context(cfg, max_rows=1)
+    vals = _fill(ctx, cfg, rng)[0]
+    sinks = rng.standard_normal((1, nh)).astype(np.float32)
+    ctx.uocr_set_sinks(sinks)
+    q = rng.standard_normal((n, nh * group, dim)).astype(np.float32) * 2
+    q[n // 2] *= 1e-20
+    want, _ = _chunk_reference(q, vals[0, 0], vals[0, 1], start, 230, 5, sinks=sinks[0].astype(np.float64))
+    qd = torch.zeros(q.size + 1, device="cuda")[shift:shift + q.size]
+    qd.copy_(torch.from_numpy(q).reshape(-1))
+    buf = torch.full((q.size + 2,), 7.0, dtype=_dt(torch, dtype), device="cuda")
+    out = buf[shift:shift + q.size]
+    ctx.uocr_attend_chunk(0, 0, start, n, nh * group, qd.data_ptr(), out.data_ptr(), dtype)
+    ctx.uocr_sync()
+    _close(out.double().cpu().numpy().reshape(q.shape), want, dtype)
+    assert torch.all(buf[shift + q.size:] == 7) and torch.all(buf[:shift] == 7)
+    ctx.close()
+
+
+@pytest.mark.parametrize("dim,nh,n,start,group,keep", [(32, 2, 300, 0, 1, None), (64, 2, 150, 160, 2, 9), (128, 2, 310, 0, 1, None),
+                                                       (128, 1, 70, 231, 3, 0)])
+def test_attend_chunk_tracked_on_many_rows(cuda, dim, nh, n, start, group, keep):
+    """A context of many rows accumulates the weights of many queries in one pass."""
+    torch = cuda
+    rng = np.random.default_rng(dim + n)
+    P, R = 310, 6
+    cfg = _cfg(head_dim=dim, n_heads=nh, prefix_len=P, ring_len=R, max_rows=24, kv_track=1)
+    nh = cfg.n_heads
+    ctx = binding.Context(cfg, max_rows=24)
+    vals = _fill(ctx, cfg, rng)[0]
+    hole = (0, 0)
+    w0 = np.zeros((24, nh, P + R), np.float32)
+    if keep is not None:
+        _put_weights(torch, ctx, rng.random((24, nh, P + R)).astype(np.float32))
+        _, k, v = _evict(torch, ctx, cfg, 0, [3], [3], start - 20, keep, 0)
+        vals[3, 0, :, :keep], vals[3, 1, :, :keep] = k[0, 0], v[0, 0]
+        hole = (keep, start - 20)
+        w0 = _weights(torch, ctx, cfg)
+    q = rng.standard_normal((n, nh * group, dim)).astype(np.float32) * 2
+    want, add = _chunk_reference(q, vals[3, 0], vals[3, 1], start, P, R, hole)
+    _close(_attend(torch, ctx, cfg, q, chunk=(3, start)), want, 0)
+    w = _weights(torch, ctx, cfg)
+    w0 = w0.astype(np.float64)
+    w0[3] += add
+    _close(w, w0, 0)
+    ctx.close()
+
+
 @pytest.mark.parametrize("dim,nh,n", [(32, 16, 500), (128, 8, 1000), (256, 8, 960)])
 def test_long_chunk_never_sees_later_tokens(cuda, dim, nh, n):
     torch = cuda
