@@ -245,7 +245,8 @@ typedef struct {
  * category before running). */
 typedef struct {
   uint64_t weights;      /* packed weights, norms, router, embedding, LM head  */
-  uint64_t kv_cache;     /* [layer][row][K|V][head][P+R][D] fp16               */
+  uint64_t kv_cache;     /* [layer][row][K|V][head][P+R][D] fp16, or the quantised entries with
+                            their scales (kv_int4: minima, evicted ranges and weights too) */
   uint64_t activations;  /* residual stream, q, attention partials, MLP/expert scratch */
   uint64_t routing;      /* router logits, top-k, counts, offsets, permutation */
   uint64_t logits;       /* [max_rows][vocab] fp32 readback buffer             */
@@ -320,8 +321,13 @@ UOCR_API uocr_status uocr_kv_write_i8(uocr_ctx* ctx, int32_t row, int32_t layer,
  * are the caller's.  A step or prefill of such a context runs the same
  * kernels.  Device pointers are aligned to their element.  Asynchronous unless
  * stated otherwise, enqueued on the caller's stream itself (in order with the
- * steps and the other calls), and can be captured into a graph of it.  uocr_kv_write_prefix / uocr_kv_write quantise the given
- * fp16 vectors and uocr_kv_read returns the entries' values.               */
+ * steps and the other calls), and can be captured into a graph of it.  The
+ * calls of one context share its workspaces: none may run on the GPU at the
+ * same time as another, or as a replayed graph that holds one.  What a call
+ * refuses because of evicted slots follows the evictions called so far, a
+ * captured one among them from its capture on; the device checks positions
+ * against those that have run.  uocr_kv_write_prefix / uocr_kv_write quantise
+ * the given fp16 vectors and uocr_kv_read returns the entries' values.      */
 
 /* Entries of slots [slot0, slot0+n) of one row and layer, exactly: codes one
  * per byte [n_heads][n][head_dim] (the low four bits count), scales and minima fp16
@@ -533,7 +539,8 @@ UOCR_API uocr_status uocr_debug_router_logits(uocr_ctx* ctx, int32_t layer, int3
  * CUDA graph and replayed 5 times, timed with CUDA events on the library
  * stream.  names[i] points into static storage.  n_inout: in = capacity, out
  * = number of classes.  The step mutates the KV cache like a real step (the
- * replays rewrite the current slot with the same values).                  */
+ * replays rewrite the current slot with the same values, and with kv_track
+ * add their weights again).                                                 */
 UOCR_API uocr_status uocr_profile(uocr_ctx* ctx, int32_t rows, int32_t input_kind,
                          const int32_t* token_ids, const uint16_t* x, const int32_t* positions,
                          const char** names, float* ms, int32_t* n_inout);

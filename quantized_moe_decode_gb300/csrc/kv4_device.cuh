@@ -32,12 +32,16 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 // Four pairs of codes of a word (nibbles 0|4, 1|5, 2|6, 3|7) as fp16 values
 // s q + m: the code is or'ed into the mantissa of 1024 (bits 0-3) or 64 (bits
 // 4-7), which is subtracted again, exactly.
-__device__ __forceinline__ void dequant8(uint32_t w, uint32_t s, uint32_t m, uint32_t (&x)[4]) {
+__device__ __forceinline__ void dequant8(uint32_t w, uint32_t s, uint32_t m, uint32_t mask0, uint32_t one0, uint32_t mask1,
+                                         uint32_t one1, uint32_t (&x)[4]) {
   const uint32_t h = w >> 8;
-  x[0] = hfma2u(s, hsub2u(lop_and_or(w, 0x000F000Fu, 0x64006400u), 0x64006400u), m);
-  x[1] = hfma2u(s, hsub2u(lop_and_or(w, 0x00F000F0u, 0x54005400u), 0x54005400u), m);
-  x[2] = hfma2u(s, hsub2u(lop_and_or(h, 0x000F000Fu, 0x64006400u), 0x64006400u), m);
-  x[3] = hfma2u(s, hsub2u(lop_and_or(h, 0x00F000F0u, 0x54005400u), 0x54005400u), m);
+  x[0] = hfma2u(s, hsub2u(lop_and_or(w, mask0, one0), one0), m);
+  x[1] = hfma2u(s, hsub2u(lop_and_or(w, mask1, one1), one1), m);
+  x[2] = hfma2u(s, hsub2u(lop_and_or(h, mask0, one0), one0), m);
+  x[3] = hfma2u(s, hsub2u(lop_and_or(h, mask1, one1), one1), m);
+}
+__device__ __forceinline__ void dequant8(uint32_t w, uint32_t s, uint32_t m, uint32_t (&x)[4]) {
+  dequant8(w, s, m, 0x000F000Fu, 0x64006400u, 0x00F000F0u, 0x54005400u, x);
 }
 
 // The slots that queries up to `lim` read, as whole tiles: those of [0, x) and of

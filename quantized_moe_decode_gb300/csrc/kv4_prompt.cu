@@ -10,8 +10,8 @@
 //     tile's words hold eight dimensions of a slot, or one dimension of a slot pair,
 //     side by side); at an item's end they put the next item's queries into tensor
 //     memory, so that shared memory feeds the products one operand only;
-//   one warp issues S = Q K^T (M 128, N 64), two blocks ahead, and O += P V (M 128,
-//     N D);
+//   one warp issues S = Q K^T (M 128, N 64), three blocks ahead, and O += P V (M 128,
+//     N D), in turns;
 //   eight warps, a thread per query, in two groups that take the blocks in turn, so
 //     that one's exponentials run while the other waits: a pass over S for the maximum
 //     (the reference goes on from group to group), a pass that writes P into tensor
@@ -23,10 +23,13 @@
 // as kPromptStart blocks; an item that several runs share leaves partials, which a
 // second kernel merges.
 // What it cannot do without are those products, 4 M N K of them per block and pass:
-// about 1050 cycles of the tensor pipe for a block of 128 dimensions.  Measured (2048
-// tokens from position 0, ten heads of 128 dimensions: 18 blocks an SM): 43 us with the
-// merge, about 1700 cycles a block (the issuing warp's waits between the products),
-// 7000 until an item's first scores are there, 6000 to 8000 from one item to the next.
+// about 1050 cycles of the tensor pipe for a block of 128 dimensions.  Measured, ten
+// heads of 128 dimensions, 2048 tokens from position 0 (18 blocks an SM): 41 us with
+// the merge, 7000 cycles until an item's first scores are there, 6000 to 8000 from one
+// item to the next; eight heads, 8192 tokens (219 blocks an SM): 258 us, 2200 cycles a
+// block.  There the roles wait for one another in turn: the values' warps take 1900 of
+// them, a softmax group 3300 for its two blocks, the issuing warp 1900; what they all
+// share is the SM's issue of instructions.
 #include "kv4_device.cuh"
 #include "launch.h"
 #include "tc_common.cuh"
@@ -34,7 +37,7 @@
 namespace uocr {
 
 constexpr int kPromptThreads = 544;  // warps 0-7 softmax, 8-11 keys, 12-15 values, 16 issues
-constexpr int kPromptStart = 4;      // what an item's start and end take, in blocks (3 and 6: 46 and 44.5 us where 4 gives 43)
+constexpr int kPromptStart = 4;      // what an item's start and end take, in blocks (3 and 6: 3 and 1 us more for 2048 tokens from 0 and ten heads)
 constexpr int kPromptMaxZ = 2048;    // query tiles of a call that is cut into runs
 
 template <int D>
@@ -126,6 +129,28 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t& h, uint32_t& 
   h = pack2(x, y);
   const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
   e = pack2(x - f.x, y - f.y);
+}
+
+// Two products or sums in one instruction, and the largest of three numbers.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n .reg .b64 a, b, c, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 c, {%6, %7};\n"
+      " fma.rn.f32x2 d, a, b, c;\n mov.b64 {%0, %1}, d;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n add.rn.f32x2 d, a, b;\n mov.b64 {%0, %1}, d;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 
 // The low n of a tile's 16 bits, n of any sign.
@@ -329,14 +354,15 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(const Kv4AttnA
             lds128u(p, w[0], w[1], w[2], w[3]);
         };
         for (int b = cur.b0, i = it; b < cur.b1; ++b, ++i) {
-          cp_wait<C::RS - 2>();
-          __syncwarp();  // every lane's copies have landed, and the last block's slot is read
-          fetch(cur, tiles, b + C::RS - 1);
           const bool missing = b * 4 + n >= tiles.count;  // such a tile: zeros, under weights of zero
           const uint32_t raw = ring + (b & (C::RS - 1)) * C::RT, codes = raw + lane * (D == 32 ? 8 : 16);
           const int s = i & 1;
           if (i >= 2) wait(keys ? &bars.k_empty[s] : &bars.v_empty[s], (i >> 1) - 1);
           if (!ok) break;
+          // (the copies behind the wait: in front of it they would hold it up by 600 cycles)
+          cp_wait<C::RS - 2>();
+          __syncwarp();  // every lane's copies have landed, and the last block's slot is read
+          fetch(cur, tiles, b + C::RS - 1);
           if (keys) {
             uint2 kpar = make_uint2(0u, 0u);
             if (!missing) lds64u(raw + 8 * D + (g * W + t * W / 4) * 8, kpar.x, kpar.y);
@@ -398,6 +424,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(const Kv4AttnA
             // dimension g D/8 + 4 q + j of slots 2t, 2t+1 (first half of the tile), 2t+8, 2t+9 (second);
             // where g and g + 4 would meet in a bank, one takes the pairs of a word's nibbles the other way round
             const int turn = D == 128 ? g >> 2 : 0;
+            const uint32_t mask0 = turn ? 0x00F000F0u : 0x000F000Fu, one0 = turn ? 0x54005400u : 0x64006400u;
+            const uint32_t mask1 = turn ? 0x000F000Fu : 0x00F000F0u, one1 = turn ? 0x64006400u : 0x54005400u;
 #pragma unroll 1
             for (int half = 0; half < (W == 4 ? 2 : 1); ++half) {
               uint32_t w[4], x[4];
@@ -407,8 +435,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(const Kv4AttnA
 #pragma unroll
               for (int q = 0; q < (W == 4 ? 4 : 2 * W); ++q) {
                 if (W < 4 && q == W) vpar.x = vpar.z, vpar.y = vpar.w, o += C::VL;
-                const uint32_t c = turn ? ((w[q] >> 4) & 0x0F0F0F0Fu) | ((w[q] & 0x0F0F0F0Fu) << 4) : w[q];
-                dequant8(c, vpar.x, vpar.y, x);
+                dequant8(w[q], vpar.x, vpar.y, mask0, one0, mask1, one1, x);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                   const int d = g * (D / 8) + 4 * (q % W) + j;
@@ -494,49 +521,62 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(const Kv4AttnA
       const uint32_t tm = same(tmem), kd = same((int)smem_u32(smem + C::K) >> 4), vd = same((int)smem_u32(smem + C::V) >> 4);
       const int b0 = same(cur.b0), b1 = same(cur.b1);
       if (b0 < b1) wait(&bars.q_full[(round - 1) & 1], (round - 1) >> 1);
+      // Products into one accumulator follow each other by 87 cycles, whatever N up to 128;
+      // so those of block b's values and of block b + 3's scores take turns.
 #pragma unroll 1
-      for (int b = b0 - 2, i = same(it) - 2; b < b1 && ok; ++b, ++i) {  // scores of block b + 2, then values of block b
-        if (b + 2 < b1) {
-          const int s = i & 1, n = (i + 2) & 3;
-          // Block i + 2's scores take the place of the weights of block i - 2, which are used:
-          // block i's values replaced those that they were used with.  (Before an item's
-          // first blocks it is the last item's last values that say so.)
-          if (b >= b0) wait(&bars.v_full[s], i >> 1);
-          wait(&bars.k_full[s], (i + 2) >> 1);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t d = kd + s * (C::KB >> 4), acc = tm + n * 64;
-          if (elect_one()) {
-#pragma unroll
-            for (int pass = 0; pass < 2; ++pass)
-#pragma unroll
-              for (int ks = 0; ks < D / 16; ++ks)
-                tc_mma_f16_t(acc, tm + C::TQ + pass * (D / 2) + ks * 8, operand(d + (ks * 2 * C::KL >> 4), C::KL, C::KS), IDESC_S,
-                             (pass | ks) != 0);
-            tc_commit(&bars.s_full[n]);
-            tc_commit(&bars.k_empty[s]);
-          }
-          __syncwarp();
+      for (int b = b0 - 3, i = same(it) - 3; b < b1 && ok; ++b, ++i) {
+        const bool score = b + 3 < b1, value = b >= b0;
+        const int j = i + 3;
+        // block j's scores take the place of the weights of block i - 1, which must be used;
+        // one trip to the barriers for all that are past already
+        bool ready = true;
+        if (score) ready = mbar_try_wait(&bars.k_full[j & 1], (uint32_t)(j >> 1) & 1u);
+        if (score && i > 0) ready = mbar_try_wait(&bars.pv_done[(i - 1) & 3], (uint32_t)((i - 1) >> 2) & 1u) && ready;
+        if (value) ready = mbar_try_wait(&bars.v_full[i & 1], (uint32_t)(i >> 1) & 1u) && ready;
+        if (value) ready = mbar_try_wait(&bars.p_full[i & 3], (uint32_t)(i >> 2) & 1u) && ready;
+        if (!__all_sync(0xffffffffu, ready)) {
+          if (score) wait(&bars.k_full[j & 1], j >> 1);
+          if (score && i > 0) wait(&bars.pv_done[(i - 1) & 3], (i - 1) >> 2);
+          if (value) wait(&bars.v_full[i & 1], i >> 1);
+          if (value) wait(&bars.p_full[i & 3], i >> 2);
         }
-        if (b >= b0) {
-          const int s = i & 1, n = i & 3;
-          if (b + 2 >= b1) wait(&bars.v_full[s], i >> 1);
-          wait(&bars.p_full[n], i >> 2);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t d = vd + s * (C::VB >> 4), p = tm + n * 64, first = b > b0;
-          if (elect_one()) {
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t k = kd + (j & 1) * (C::KB >> 4), acc = tm + (j & 3) * 64;
+        const uint32_t v = vd + (i & 1) * (C::VB >> 4), p = tm + (i & 3) * 64, first = b > b0;
+        auto scores = [&](int x) {  // of D / 8: two passes over the dimensions
+          const int pass = x / (D / 16), ks = x % (D / 16);
+          tc_mma_f16_t(acc, tm + C::TQ + pass * (D / 2) + ks * 8, operand(k + (ks * 2 * C::KL >> 4), C::KL, C::KS), IDESC_S, x != 0);
+        };
+        auto values = [&](int x) {  // of 8: two passes over the slots
+          const int pass = x >> 2, ks = x & 3;
+          tc_mma_f16_t(tm + C::O, p + ks * 16 + pass * 8, operand(v + (ks * 2 * C::VL >> 4), C::VL, C::VS), IDESC_O, x ? 1u : first);
+        };
+        if (elect_one()) {
+          if (score && value) {
 #pragma unroll
-            for (int pass = 0; pass < 2; ++pass)
+            for (int x = 0; x < 8; ++x) {
 #pragma unroll
-              for (int ks = 0; ks < C::N / 16; ++ks)
-                tc_mma_f16_t(tm + C::O, p + ks * 16 + pass * 8, operand(d + (ks * 2 * C::VL >> 4), C::VL, C::VS), IDESC_O,
-                             (pass | ks) != 0 ? 1u : first);
-            tc_commit(&bars.pv_done[n]);
-            tc_commit(&bars.v_empty[s]);
+              for (int y = x * D / 64; y < (x + 1) * D / 64; ++y) scores(y);
+              values(x);
+            }
+          } else if (score) {
+#pragma unroll
+            for (int y = 0; y < D / 8; ++y) scores(y);
+          } else if (value) {
+#pragma unroll
+            for (int x = 0; x < 8; ++x) values(x);
           }
-          __syncwarp();
+          if (score) {
+            tc_commit(&bars.s_full[j & 3]);
+            tc_commit(&bars.k_empty[j & 1]);
+          }
+          if (value) {
+            tc_commit(&bars.pv_done[i & 3]);
+            tc_commit(&bars.v_empty[i & 1]);
+          }
         }
+        __syncwarp();
       }
     } else {  // ---------------- softmax: a thread per query and block, two groups of warps take the blocks in turn
       const int group = warp >> 2, pair = warp & 3, r = pair * 32 + lane;
@@ -556,40 +596,54 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(const Kv4AttnA
         const int i = it + b - b0;  // i & 1 == group
         const uint32_t sp = lanes + (i & 3) * 64;
         wait(&bars.s_full[i & 3], i >> 2);
-        // A pass for the maximum and one for the weights, a tile's slots at a time in
+        // A pass for the maximum and one for the weights, two tiles' slots at a time in
         // short loops: the roles' loops together stay in the instruction caches.
         float mx = kNoMax;
         const int slot_lo = first_slot(b * 4), slot_hi = first_slot(b * 4 + 3) + 16;
         const bool full = slot_hi > 0 && slot_hi <= cur.lim_lo && (hole.y <= hole.x || slot_hi <= hole.x || slot_lo >= hole.y);
-        auto load = [&](int n, float (&x)[16]) {  // products of tile n, in units of 1 / cq
-          uint32_t raw[16];
-          tc_ld16(sp + n * 16, raw);
+        auto load = [&](int n, float (&x)[32]) {  // products of tiles n, n + 1, in units of 1 / cq
+          uint32_t raw[32];
+          tc_ld32(sp + n * 16, raw);
           tc_wait_ld();
 #pragma unroll
-          for (int j = 0; j < 16; ++j) x[j] = __uint_as_float(raw[j]);
+          for (int j = 0; j < 32; ++j) x[j] = __uint_as_float(raw[j]);
           if (!full) {
-            const int s0 = first_slot(b * 4 + n);
-            const unsigned read = low_bits(lim - s0) & (hole.y > hole.x ? low_bits(hole.x - s0) | ~low_bits(hole.y - s0) : ~0u);
+            unsigned read = 0;
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
+            for (int k = 0; k < 2; ++k) {
+              const int s0 = first_slot(b * 4 + n + k);
+              read |= (low_bits(lim - s0) & (hole.y > hole.x ? low_bits(hole.x - s0) | ~low_bits(hole.y - s0) : ~0u)) << (16 * k);
+            }
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
               if (!(read >> j & 1u)) x[j] = -INFINITY;
           }
         };
         if (ok) {
           tc_fence_after();
 #pragma unroll 1
-          for (int n = 0; n < 4; ++n) {
-            float x[16];
+          for (int n = 0; n < 4; n += 2) {
+            float x[32];
             load(n, x);
             float top[4] = {x[0], x[1], x[2], x[3]};  // four chains
 #pragma unroll
-            for (int j = 4; j < 16; ++j) top[j & 3] = fmaxf(top[j & 3], x[j]);
-            mx = fmaxf(mx, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * cq);
-            if (a.scores && have && b * 4 + n < tiles.count) {
-              float* so = a.scores + qi * a.tiles * kKv4Slots + first_slot(b * 4 + n);
+            for (int j = 4; j < 32; j += 8)
 #pragma unroll
-              for (int j = 0; j < 16; j += 4)
-                *reinterpret_cast<float4*>(so + j) = make_float4(x[j] * cq, x[j + 1] * cq, x[j + 2] * cq, x[j + 3] * cq);
+              for (int k = 0; k < 4; ++k) top[k] = j + 4 + k < 32 ? max3(top[k], x[j + k], x[(j + 4 + k) % 32]) : fmaxf(top[k], x[j + k]);
+            mx = fmaxf(mx, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * cq);
+            if (a.scores && have) {
+#pragma unroll 1
+              for (int k = 0; k < 2; ++k) {
+                if (b * 4 + n + k >= tiles.count) break;
+                float* so = a.scores + qi * a.tiles * kKv4Slots + first_slot(b * 4 + n + k);
+#pragma unroll
+                for (int j = 0; j < 16; j += 4) {
+                  const float4 lo = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
+                  const float4 hi = make_float4(x[16 + j], x[17 + j], x[18 + j], x[19 + j]);
+                  const float4 v = k ? hi : lo;
+                  *reinterpret_cast<float4*>(so + j) = make_float4(v.x * cq, v.y * cq, v.z * cq, v.w * cq);
+                }
+              }
             }
           }
         }
@@ -625,22 +679,30 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(const Kv4AttnA
             tc_st8(lanes + C::O + c, o);
           }
         }
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        const float2 cq2 = make_float2(cq, cq), ref2 = make_float2(-ref, -ref);
 #pragma unroll 1
-        for (int n = 0; n < 4; ++n) {
-          float x[16];
-          uint32_t h[8], e[8];
+        for (int n = 0; n < 4; n += 2) {
+          float x[32];
+          uint32_t h[16], e[16];
           load(n, x);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float v0 = ex2(fmaf(x[2 * j], cq, -ref)), v1 = ex2(fmaf(x[2 * j + 1], cq, -ref));
-            sum[j & 3] += v0 + v1;
-            split2(v0, v1, h[j], e[j]);
+          for (int j = 0; j < 16; ++j) {
+            const float2 v = fma2(make_float2(x[2 * j], x[2 * j + 1]), cq2, ref2);
+            const float2 w = make_float2(ex2(v.x), ex2(v.y));
+            sum[j & 1] = add2(sum[j & 1], w);
+            h[j] = pack2(w.x, w.y);
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
+            const float2 r = add2(w, make_float2(-f.x, -f.y));
+            e[j] = pack2(r.x, r.y);
           }
-          tc_st8(sp + n * 16, h);
-          tc_st8(sp + n * 16 + 8, e);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            tc_st8(sp + (n + k) * 16, h + 8 * k);
+            tc_st8(sp + (n + k) * 16 + 8, e + 8 * k);
+          }
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         if (!full) {  // groups that are not finite, once the block's values (and s_bad) are written
           wait(&bars.v_full[group], i >> 1);
           if (!ok) continue;
