@@ -168,13 +168,7 @@ struct Kv4AttnArgs {
   int* status;
 };
 cudaError_t launch_kv4_attn(const Kv4AttnArgs& a, int tokens, cudaStream_t st, bool pdl);
-// The same for a chunk of many queries per cache head, head_dim up to 128: from 128
-// queries on, where an item of 128 is full.  This kernel and the other one, in us, 128
-// dimensions, a query per token and cache head: 2048 tokens from 0, ten heads, 41 and
-// 145; 256 from 1792 22 and 44; 128 from 1920 22.3 and 29.3, from 0 14.7 and 14.3; 128
-// from 59872, two heads, 64 and 82; half an item: 64 tokens from 1984, ten heads, 22.1
-// and 23.8, from 0 11.2 and 12.2, but from 59936, two heads, 63 and 48.
-constexpr int kPromptMinQueries = 128;
+// The same for a chunk of much work, head_dim up to 128.
 cudaError_t launch_kv4_prompt(const Kv4AttnArgs& a, int tokens, cudaStream_t st, bool pdl);
 cudaError_t init_kv4_prompt_attributes();
 

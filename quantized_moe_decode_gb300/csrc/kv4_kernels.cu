@@ -1305,13 +1305,22 @@ static cudaError_t launch_attn4(const Kv4AttnArgs& args, int tokens, cudaStream_
   a.q_wide = (uintptr_t)a.q % 16 == 0;
   const int n_z = a.kv_rstep ? tokens : (tokens * (a.q_heads / a.nh) + 4 * NT - 1) / (4 * NT);
   const long long items = (long long)n_z * a.nh;
-  // One item per CTA where none can have more than 16 tiles, and in a chunk of two
-  // waves of items or more (its runs would take every item to be as long as the
-  // last); else a run for every resident warp.
   int ctas = a.n_sm * C::CPS;
   if (ctas * kAttn4Warps * 4 * NT > kAttn4MaxParts) ctas = kAttn4MaxParts / (kAttn4Warps * 4 * NT);
+  // An item a CTA, or a run a resident warp?  Runs take some 6 us more (a second kernel,
+  // and shared items), and gain what the last wave of an item a CTA leaves idle.
+  // Measured in us, items and runs, ten heads of 128 dimensions: 1 row of 1000 slots
+  // 9.8 and 13.0, of 2000 15.5 and 13.4; 24 rows of 1000 16.4 and 16.7, of 3000 40.6
+  // and 36.6; 64 rows of 1000 29.0 and 35.4, of 2000 48.7 and 52.5, of 6000 124 and 115;
+  // 64 tokens from 2000 22.1 and 22.9, from 6000 52 and 34.  The rule holds the time
+  // (a tile's grows with 64 + D) of the idle tiles against that, a wave that does not
+  // fill the GPU counting more the fuller it is; lengths of rows are known on the
+  // device only, so theirs count as the cache's.
+  const double tiles = a.pos ? a.tiles : (a.pos0 + tokens + kKv4Slots - 1) / kKv4Slots;
+  const double load = (double)items / ctas, waves = ceil(load);
+  const bool pays = tiles * (waves - load) * (load < 1. ? 1. + load : 1.) * (64 + D) > 18000.;
   const bool countable = items * a.tiles < 1LL << 30;
-  a.n_runs = a.tiles <= 16 || (!a.kv_rstep && items >= 2LL * ctas) || !countable ? 0 : ctas * kAttn4Warps;
+  a.n_runs = pays && countable ? ctas * kAttn4Warps : 0;
   cudaError_t e = launch_kernel(k_kv4_attn<D, NT>, dim3(a.n_runs ? ctas : (unsigned)items), dim3(kAttn4Warps * 32),
                                 (size_t)(part > ring ? part : ring), st, pdl, a, tokens, n_z);
   if (e == cudaSuccess && a.n_runs)
@@ -1320,11 +1329,28 @@ static cudaError_t launch_attn4(const Kv4AttnArgs& args, int tokens, cudaStream_
   return e;
 }
 
+// A chunk on the kernel that dequantises a block once for 128 queries (kv4_prompt.cu)
+// or on this one?  Both times in us, as measured: this kernel takes 4.5 for every
+// wave of items and 2.4 to 4.5 for 10^6 pairs of a query and a slot, that one 0.7 of
+// the latter and 5 more at its start, and more the longer its prefix is (partials to
+// merge).  This one and that one, ten heads of 128 dimensions, 192 tokens from 0 8.8
+// and 11.1, 512 24.6 and 16.9; 192 from 500 14.3 and 18.8, 256 23.4 and 18.2; 64 from
+// 2000 22.9 and 21.1, 128 29.6 and 21.8; 64 from 20000 74 and 40; ten of 64, 256 from
+// 500 12.9 and 16.6, 384 19.5 and 17.2; two of 128, 128 from 20000 35.5 and 49.5, 192
+// 48.8 and 39.9; 32 of 64, 256 from 0 19.3 and 11.4.
+static bool prompt_pays(const Kv4AttnArgs& a, int tokens) {
+  const double slots = a.pos ? a.tiles * kKv4Slots : a.pos0 + tokens;
+  const double pairs = 1e-6 * tokens * a.q_heads * slots;
+  const double each = a.D <= 64 ? 2.4 : 4.45;  // of 10^6 pairs here
+  const int resident = a.n_sm * (a.D <= 32 ? 4 : a.D <= 64 ? 3 : 2);
+  const double waves = ceil((double)tokens * a.q_heads / 8 / resident);
+  return pairs * (each - 0.7) + 4.5 * (waves - 1) > 5 + slots / 1300;
+}
+
 cudaError_t launch_kv4_attn(const Kv4AttnArgs& a, int tokens, cudaStream_t st, bool pdl) {
   if (tokens <= 0) return cudaSuccess;
   const int G = a.q_heads / a.nh;
-  // a chunk of many queries: a block dequantised once for 128 of them
-  const bool prompt = !a.kv_rstep && a.D <= 128 && (long long)tokens * G >= kPromptMinQueries;
+  const bool prompt = !a.kv_rstep && a.D <= 128 && prompt_pays(a, tokens);
   // a second group of four queries costs registers: only where they exist
   const bool two = (a.kv_rstep ? G : tokens * G) > 4;
   cudaError_t e = cudaErrorInvalidValue;

@@ -19,9 +19,9 @@
 //     which almost never happens.
 // As in the decode kernel queries and weights are pairs of fp16 numbers (value and
 // remainder), here as two products, which keeps about 22 bits; sums are fp32.
-// The call's blocks are cut into equal runs, one per SM, an item's start counting
-// as kPromptStart blocks; an item that several runs share leaves partials, which a
-// second kernel merges.
+// A CTA takes one item, or the call's blocks are cut into equal runs, one per SM, an
+// item's start counting as kPromptStart blocks; an item that several runs share leaves
+// partials, which a second kernel merges.
 // What it cannot do without are those products, 4 M N K of them per block and pass:
 // about 1050 cycles of the tensor pipe for a block of 128 dimensions.  Measured, ten
 // heads of 128 dimensions, 2048 tokens from position 0 (18 blocks an SM): 41 us with
@@ -861,10 +861,22 @@ static cudaError_t launch_prompt4(const Kv4AttnArgs& args, int tokens, cudaStrea
   a.out_wide = (uintptr_t)a.out % 16 == 0;
   const int queries = tokens * (a.q_heads / a.nh), n_z = (queries + 127) / 128;
   const long long items = (long long)n_z * a.nh;
-  // one run per SM, unless there are so many items that their last wave does not show
+  // A run an SM, or an item a CTA (the longest first)?  Runs take some 11 us more (the
+  // merge, the partials, more starts), about what 14 blocks take, and gain what the
+  // items leave idle: the longest item, or the first and shortest ones in the ragged
+  // last wave.  Measured in us, items and runs, 2048 tokens and ten heads of 64
+  // dimensions from 0 32.8 and 37.6, of 128 from 2000 84.7 and 72.5; 4096 tokens of 128
+  // from 0 94.4 and 97.9; 1024 tokens, 32 heads of 64, from 0 29.7 and 38.0, from 2000
+  // 78.4 and 79.6, from 20000 495 and 444; 128 tokens, ten heads of 128, from 0 10.2
+  // and 14.0, from 2000 41 and 22.
   const int ctas = a.n_sm * 256 <= kAttn4MaxParts * 2 ? a.n_sm : kAttn4MaxParts * 2 / 256;
+  const int pos0 = a.pos ? a.tiles * kKv4Slots - tokens : a.pos0;
+  auto blocks = [&](int before) { return (pos0 + before / (a.q_heads / a.nh) + 63) / 64 + kPromptStart; };
+  const double shortest = blocks(queries < 128 ? queries : 128), longest = blocks(queries);
+  const double load = (double)items / ctas, even = load * (shortest + longest) / 2, ragged = even + shortest * (ceil(load) - load);
+  const bool pays = (ragged > longest ? ragged : longest) - even > 14.;
   const bool countable = items * ((a.tiles + 3) / 4 + kPromptStart) < 1LL << 30;
-  a.n_runs = items >= 8LL * ctas || n_z > kPromptMaxZ || !countable ? 0 : ctas;
+  a.n_runs = pays && n_z <= kPromptMaxZ && countable ? ctas : 0;
   cudaError_t e = launch_kernel(k_kv4_prompt<D>, dim3(a.n_runs ? a.n_runs : (unsigned)items), dim3(kPromptThreads),
                                 (size_t)Prompt4<D>::SMEM, st, pdl, a, queries, n_z);
   if (e == cudaSuccess && a.n_runs)

@@ -847,6 +847,19 @@ def test_attend_chunk_of_any_sharing(cuda, dim, nh, n, start, group, dtype, shif
     ctx.close()
 
 
+@pytest.mark.parametrize("dim,nh,n,start,group", [(32, 64, 100, 130, 5), (64, 32, 90, 140, 7), (128, 16, 101, 97, 3), (32, 40, 150, 0, 8),
+                                                  (64, 40, 129, 60, 2), (128, 12, 77, 120, 6), (128, 30, 128, 99, 4), (64, 64, 127, 3, 1)])
+@pytest.mark.parametrize("dtype,shift", [(0, 1), (1, 0), (2, 1)])
+def test_attend_chunk_of_any_sharing_many_heads(cuda, dim, nh, n, start, group, dtype, shift):
+    """The same with enough heads for the kernel of long chunks."""
+    test_attend_chunk_of_any_sharing(cuda, dim, nh, n, start, group, dtype, shift)
+
+
+@pytest.mark.parametrize("dim,nh,n,start,group,keep", [(64, 32, 190, 40, 1, None), (32, 40, 64, 240, 3, 17), (128, 16, 96, 200, 2, 0)])
+def test_attend_chunk_tracked_on_many_rows_and_heads(cuda, dim, nh, n, start, group, keep):
+    test_attend_chunk_tracked_on_many_rows(cuda, dim, nh, n, start, group, keep)
+
+
 @pytest.mark.parametrize("dim,nh,n,start,group,keep", [(32, 2, 300, 0, 1, None), (64, 2, 150, 160, 2, 9), (128, 2, 310, 0, 1, None),
                                                        (128, 1, 70, 231, 3, 0)])
 def test_attend_chunk_tracked_on_many_rows(cuda, dim, nh, n, start, group, keep):
