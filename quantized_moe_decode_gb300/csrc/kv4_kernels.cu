@@ -303,10 +303,12 @@ cudaError_t launch_kv4_append(const Kv4AppendArgs& a, int tokens, cudaStream_t s
   auto wide = [&](const void* p, long long ld) { return ((uintptr_t)p | (uintptr_t)(ld * e)) % 16 == 0; };
   const bool vec = wide(a.q, a.ldq) && wide(a.k, a.ldk) && wide(a.v, a.ldv) && a.lhk * e % 16 == 0 &&
                    ((uintptr_t)a.q_out | (uintptr_t)a.k_val | (uintptr_t)a.v_val) % 16 == 0;
-  // rounds of at most 256 threads over a token's vectors, evenly filled; few
-  // tokens take one round, so that a step waits for one load
+  // rounds of at most 256 threads over a token's vectors, evenly filled; up to three
+  // tokens an SM take one round, so that a step waits for one load.  In us, one round
+  // and rounds, ten heads of 128 dimensions: 152 tokens 3.6 and 4.4, 304 4.2 and 6.6,
+  // 456 6.8 and 7.1, 608 7.3 and 7.2, 760 9.5 and 7.2, 2048 21.2 and 15.8.
   const int items = (2 * a.nh + a.q_heads) * (a.D / 8);
-  const bool many = tokens >= a.n_sm;
+  const bool many = tokens > 3 * a.n_sm;
   const int most = many ? 256 : 1024;
   const int rounds = (items + most - 1) / most;
   const int threads = ((items + rounds - 1) / rounds + 31) / 32 * 32;
@@ -464,7 +466,7 @@ cudaError_t launch_kv4_weights(const Kv4WeightsArgs& a, cudaStream_t st, bool pd
 }
 
 // ------------------------------------------------------------------ attention
-// softmax(q k / sqrt D) v over the live slots, split over a cluster of CTAs.
+// softmax(q k / sqrt D) v over the live slots.
 //
 // A CTA holds the queries that read one (row, head): the heads that share it,
 // or a tile of a chunk's tokens.  A warp takes 16-slot tiles in turn and keeps
@@ -485,14 +487,24 @@ cudaError_t launch_kv4_weights(const Kv4WeightsArgs& a, cudaStream_t st, bool pd
 // rescales the accumulators.
 //
 // The work of a call is the list of its items' tiles, an item being one (row,
-// head) or one (tile of a chunk's tokens, head).  It is cut into equal runs, one
-// for each warp that fits on the GPU at once, whatever the rows' lengths: a warp
-// goes through its run item by item and meets no barrier (but where one item
-// spans all four runs of a CTA, which then leave one partial).  It finishes an item
-// that lies in its run; of the first and the last, which it shares with its
-// neighbours, it leaves a partial (maximum, sum, weighted values), and a second,
-// small kernel merges those in order.  Items of a few tiles, and the many items
-// of a long chunk, are shared out one per CTA instead.
+// head) or one (tile of a chunk's tokens, head).  Either a CTA takes an item, its
+// warps the tiles in turn, and merges their parts in shared memory; or the list is
+// cut into equal runs, one for each warp that fits on the GPU at once, whatever the
+// rows' lengths: a warp goes through its run item by item and meets no barrier (but
+// where one item spans all four runs of a CTA, which then leave one partial).  It
+// finishes an item that lies in its run; of the first and the last, which it shares
+// with its neighbours, it leaves a partial (maximum, sum, weighted values), and a
+// second, small kernel merges those in order.
+//
+// What it cannot do without is the read of the entries (64 rows of 2176 slots, ten
+// heads of 128 dimensions: 223 MB, 33 us at the copy bandwidth).  Measured there,
+// device time of back-to-back calls: 48.7 us with an item a CTA, 52.5 with runs, of which
+// 6.5 pass before the first tiles are there (they are the first of the stream) and 5
+// from the last tile to the end of the merge; 57% of the issue slots and 59% of DRAM's
+// throughput over the whole launch.  More CTAs on an SM, deeper rings, other orders of
+// the rows and L2 hints changed nothing (at most 1 us).  Two rows of 60000 slots, 32
+// heads on four (77 MB, 11.3 us): 34 us, of which 8 are the merge and what starts and
+// ends; the rest is the arithmetic of eight queries, 440 instructions of a warp a tile.
 constexpr int kAttn4Warps = 4;
 
 template <int D, int NT>
@@ -1086,7 +1098,8 @@ __global__ void __launch_bounds__(kAttn4Warps * 32, Attn4<D, NT>::CPS) k_kv4_att
 
 // Merge the runs' partials: a CTA per (item, query of the item), which also adds
 // its share of the row's weights.  A trip to the L2 for all maxima and sums, one
-// for the values of the partials that hold any.
+// for the values of the partials that hold any.  Latency only: 2.5 us from the last
+// tile of the attention to its start, 1.5 to 2.5 more to its end.
 __global__ void __launch_bounds__(256) k_kv4_merge(const Kv4AttnArgs a, int tokens, int n_z, int nq_tile) {
   constexpr int T = 256, CAP = 1024;  // partials listed at a time
   __shared__ Attn4Rows s_rows;
@@ -1401,7 +1414,12 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 // are entries.  A row that is its own source is compacted by the selecting CTA
 // itself: a chunk is read into registers before any of it is written, and a kept
 // entry never moves up.  Bound by the scattered reads (a slot's values lie in
-// 16-byte pieces of its tile) and the writes.
+// 16-byte pieces of its tile, half of a 32-byte sector each) and the writes: 12
+// layers of 8 rows, 701 of 3000 entries with their values, 10 heads of 128
+// dimensions take 154 us, 34 to select (0.7 of the issue slots) and 118 to move,
+// whose 340 MB of reads and 401 of writes go at 6.2 TB/s.  Selecting and moving in
+// one kernel, so that the two overlap, took 156 to 170 us there and 50 to 64 where
+// the two take 46 (32 rows, one layer).
 constexpr int kEvictThreads = 512;
 constexpr int kEvictKeys = 4096;  // weights kept in shared memory between the passes
 constexpr int kEvictPer = 8;      // entries of a moving warp
