@@ -110,8 +110,8 @@ __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sy
 __device__ __forceinline__ uint32_t over(int G) { return 0xFFFFFFFFu / (uint32_t)G + 1; }
 __device__ __forceinline__ int div_by(int u, int G, uint32_t over_g) { return G == 1 ? u : (int)__umulhi((uint32_t)u, over_g); }
 
-// Blocks of a query tile whose last token is tok (positions rise and do not wrap,
-// so that a query at position p reads p + 1 slots but the evicted ones).
+// Blocks of a query tile whose last query reads up to slot lim (positions rise and do
+// not wrap, so that a query at position p reads p + 1 slots but the evicted ones).
 __device__ __forceinline__ int prompt_blocks(int lim, int2 hole) { return (TileList(lim, hole).count + 3) >> 2; }
 
 // Barriers of the two softmax warps that have the same 32 queries: for both, and
@@ -311,8 +311,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(const Kv4AttnA
     return false;
   };
 
-  // Every role goes through the same items at its own pace; the softmax warps load an
-  // item's queries one ahead, so that the first round has no item yet.
+  // Every role goes through the same items at its own pace; the dequantising warps
+  // load an item's queries one ahead, so that the first round has no item yet.
   PromptItem cur, next;
   cur.z = cur.head = cur.b0 = cur.b1 = cur.nq = cur.lim_lo = cur.lim_hi = 0;
   cur.inside = cur.whole = false;
@@ -478,7 +478,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_kv4_prompt(const Kv4AttnA
       if (more) {
         // Scaled to a magnitude about 1, as pairs of fp16 numbers, into tensor memory once the
         // last products with this item's are done; half of the dimensions each, keys' and values' warps.
-        wait(&bars.q_land[n], round);
+        if (!__all_sync(0xffffffffu, mbar_wait(&bars.q_land[n], (uint32_t)round & 1u))) {  // a copy: to its end
+          s_dead = 1;
+          ok = false;
+        }
         const bool have = n * 32 + lane < next.nq;
         float4 top = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
