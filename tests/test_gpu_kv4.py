@@ -819,6 +819,86 @@ def test_attend_chunk_of_many_items(cuda, dim, nh, n, start, group, P, R):
     ctx.close()
 
 
+@pytest.mark.parametrize("dim,nh,n,start,P,R,sink,keep", [(32, 64, 300, 1100, 1390, 20, True, None), (32, 64, 700, 1900, 2600, 1, False, 300),
+                                                          (128, 40, 520, 1400, 1900, 30, True, 11), (64, 64, 310, 1300, 1700, 9, False, None)])
+def test_attend_chunk_after_a_long_prefix(cuda, dim, nh, n, start, P, R, sink, keep):
+    """Long items, more of them than SMs: each SM has the end of one, whole ones and the start of another."""
+    test_attend_long_chunks(cuda, dim, nh, n, start, 1, P, R, sink, 0, 0, keep)
+
+
+@pytest.mark.parametrize("dim,nh,n,start", [(128, 16, 300, 0), (64, 16, 200, 1500), (32, 64, 300, 1100), (128, 2, 40, 0)])
+def test_captured_chunks_follow_their_inputs(cuda, dim, nh, n, start):
+    """A replayed attention of a chunk reads the queries and entries of its time, between other work of the stream."""
+    torch = cuda
+    rng = np.random.default_rng(dim + n)
+    s = torch.cuda.Stream()
+    cfg = _cfg(head_dim=dim, n_heads=nh, prefix_len=start + n, ring_len=4, max_rows=1)
+    ctx = binding.Context(cfg, max_rows=1, stream=s.cuda_stream)
+    nh = cfg.n_heads
+    with torch.cuda.stream(s):
+        q = torch.zeros(n, nh, dim, device="cuda")
+        out = torch.zeros(n, nh, dim, device="cuda")
+        twice = torch.zeros_like(out)
+        call = lambda: ctx.uocr_attend_chunk(0, 0, start, n, nh, q.data_ptr(), out.data_ptr(), 0)
+        vals = _fill(ctx, cfg, rng)[0]
+        call()
+        s.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            call()
+            twice.copy_(out)
+            twice.mul_(2)
+            call()
+        for _ in range(2):
+            x = rng.standard_normal((n, nh, dim)).astype(np.float32) * 2
+            q.copy_(torch.from_numpy(x))
+            g.replay()
+            g.replay()
+            s.synchronize()
+            want, _ = _chunk_reference(x, vals[0, 0], vals[0, 1], start, start + n, 4)
+            _close(out.double().cpu().numpy(), want, 0)
+            assert torch.equal(twice, 2 * out)
+            vals = _fill(ctx, cfg, rng)[0]
+            q.mul_(0.5)
+            g.replay()
+            want, _ = _chunk_reference(x * 0.5, vals[0, 0], vals[0, 1], start, start + n, 4)
+            s.synchronize()
+            _close(out.double().cpu().numpy(), want, 0)
+    ctx.uocr_sync()
+    ctx.close()
+
+
+def test_two_contexts_at_once(cuda):
+    """Long chunks and rows of two contexts on two streams, interleaved without a wait between them."""
+    torch = cuda
+    rng = np.random.default_rng(5)
+    todo = []
+    for dim, nh, n, start in ((128, 10, 400, 700), (64, 24, 300, 900)):
+        s = torch.cuda.Stream()
+        cfg = _cfg(head_dim=dim, n_heads=nh, prefix_len=start + n, ring_len=4, max_rows=1)
+        ctx = binding.Context(cfg, max_rows=1, stream=s.cuda_stream)
+        nh = cfg.n_heads
+        vals = _fill(ctx, cfg, rng)[0]
+        x = rng.standard_normal((n, nh, dim)).astype(np.float32)
+        q = torch.from_numpy(x).cuda()
+        out = [torch.zeros(n, nh, dim, device="cuda") for _ in range(6)]
+        row = [torch.zeros(1, nh, dim, device="cuda") for _ in range(6)]
+        pos = torch.tensor([start + n - 1], dtype=torch.int32, device="cuda")
+        want, _ = _chunk_reference(x, vals[0, 0], vals[0, 1], start, start + n, 4)
+        todo.append((ctx, n, nh, start, q, out, row, pos, want, s))
+    torch.cuda.synchronize()
+    for i in range(6):
+        for ctx, n, nh, start, q, out, row, pos, want, s in todo:
+            ctx.uocr_attend_chunk(0, 0, start, n, nh, q.data_ptr(), out[i].data_ptr(), 0)
+            ctx.uocr_attend(0, 1, pos.data_ptr(), nh, q[n - 1].data_ptr(), row[i].data_ptr(), 0)
+    for ctx, n, nh, start, q, out, row, pos, want, s in todo:
+        ctx.uocr_sync()
+        for i in range(6):
+            _close(out[i].double().cpu().numpy(), want, 0)
+            _close(row[i].double().cpu().numpy(), want[-1:], 0)
+        ctx.close()
+
+
 @pytest.mark.parametrize("dim,nh,n,start,group", [(32, 2, 127, 0, 1), (64, 1, 128, 3, 1), (128, 1, 129, 0, 1),
                                                   (64, 2, 40, 30, 5), (128, 2, 37, 0, 7), (32, 3, 86, 11, 3), (128, 1, 16, 200, 8),
                                                   (64, 1, 65, 0, 2), (32, 2, 50, 0, 6), (128, 3, 32, 1, 4)])
