@@ -710,6 +710,41 @@ def test_rows_of_very_different_lengths(cuda, dim, group):
     ctx.close()
 
 
+@pytest.mark.parametrize("dim,nh,group,sink,dtype", [(32, 2, 1, False, 0), (32, 4, 8, True, 1), (64, 1, 3, True, 2), (64, 2, 1, False, 0),
+                                                     (128, 2, 1, True, 1), (128, 1, 8, False, 0), (256, 1, 2, True, 2), (256, 1, 5, False, 0)])
+def test_rows_of_thousands_of_slots(cuda, dim, nh, group, sink, dtype):
+    """Rows whose slots many warps share, with short ones among them and evicted ones; repeated calls agree bit for bit."""
+    torch = cuda
+    rng = np.random.default_rng(dim + group)
+    P, R, rows = 3600, 37, 6
+    cfg = _cfg(head_dim=dim, n_heads=nh, prefix_len=P, ring_len=R, max_rows=rows, use_sink=int(sink), kv_track=1)
+    ctx = binding.Context(cfg, max_rows=rows)
+    nh = cfg.n_heads
+    vals = _fill(ctx, cfg, rng)[0]
+    sinks = rng.standard_normal((1, nh)).astype(np.float32) if sink else None
+    if sink:
+        ctx.uocr_set_sinks(sinks)
+    w = rng.random((rows, nh, P + R)).astype(np.float32)
+    _put_weights(torch, ctx, w)
+    holes = [(0, 0)] * rows
+    for r, keep in ((1, 700), (4, 3)):
+        _evict(torch, ctx, cfg, 0, [r], [r], 3000, keep, 0, vals=False)
+        for h in range(nh):
+            at = oracle.evict_choice(w[r, h, :3000], 3000, keep, 0)
+            vals[r, :, h, :keep] = vals[r][:, h, at]
+        holes[r] = (keep, 3000)
+    pos = [3599, 3400, 0, P + R + 5, 3001, 17]
+    q = rng.standard_normal((rows, nh * group, dim)).astype(np.float32) * 2
+    want, add = oracle.attend_kv4(q, vals[:, 0], vals[:, 1], pos, P, R, holes, sinks=None if sinks is None else sinks[0].astype(np.float64))
+    _put_weights(torch, ctx, np.zeros((rows, nh, P + R)))
+    got = _attend(torch, ctx, cfg, q, pos, dtype=dtype)
+    _close(got, want, dtype)
+    _close(_weights(torch, ctx, cfg), add, 0)
+    assert np.array_equal(_attend(torch, ctx, cfg, q, pos, dtype=dtype), got)
+    _close(_attend(torch, ctx, cfg, q[:1], pos[:1], dtype=dtype), want[:1], dtype)
+    ctx.close()
+
+
 @pytest.mark.parametrize("dim", [32, 128])
 def test_buffers_aligned_to_their_elements_only(cuda, dim):
     """Inputs and outputs one element past a 16-byte boundary give what aligned ones give, bit for bit."""
