@@ -205,6 +205,7 @@ struct Kv4EvictArgs {
   size_t list_cap;             // slots that it holds, a layer's at least
   int wide;                    // set by the launcher: the values are 16-byte aligned
   unsigned char src[kKv4MaxRows], dst[kKv4MaxRows];
+  int cap;                     // set by the launcher: weights that fit into shared memory
 };
 cudaError_t launch_kv4_evict(const Kv4EvictArgs& a, cudaStream_t st, bool pdl);
 cudaError_t init_kv4_attributes();

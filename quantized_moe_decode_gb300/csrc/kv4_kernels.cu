@@ -1438,7 +1438,8 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 // one kernel, so that the two overlap, took 156 to 170 us there and 50 to 64 where
 // the two take 46 (32 rows, one layer).
 constexpr int kEvictThreads = 512;
-constexpr int kEvictKeys = 4096;  // weights kept in shared memory between the passes
+constexpr int kEvictKeys = 49152;  // weights at most that are kept in shared memory between the passes (4 rows of
+                                   // 20000 entries 104 -> 77 us against 4096 of them)
 constexpr int kEvictPer = 8;      // entries of a moving warp
 
 // Four entries in a warp's registers: lane 8 e + i holds dimensions
@@ -1610,7 +1611,7 @@ template <int D, bool MOVE>
 __global__ void __launch_bounds__(kEvictThreads) k_kv4_evict(const Kv4EvictArgs a) {
   constexpr int T = kEvictThreads, NW = T / 32, TB = kv4_tile_bytes(D);
   constexpr int PER = 4, BLOCK = T * PER;  // live entries of a thread and of the CTA at a time
-  __shared__ uint32_t s_key[kEvictKeys];
+  extern __shared__ __align__(16) uint32_t s_key[];
   __shared__ int s_hist[2048];
   __shared__ int s_warp[NW];
   __shared__ int s_kept[MOVE ? BLOCK : 1];
@@ -1628,10 +1629,9 @@ __global__ void __launch_bounds__(kEvictThreads) k_kv4_evict(const Kv4EvictArgs 
   const size_t SLt = (size_t)a.tiles * kKv4Slots;
   const float* ws = a.wts + (((size_t)layer * a.MR + rs) * a.nh + head) * SLt;
   float* wd = a.wts + (((size_t)layer * a.MR + rd) * a.nh + head) * SLt;
-  const bool cached = live <= kEvictKeys;
-  if (cached)
-    for (int i = tid; i < live; i += T) s_key[i] = weight_key(ws[slot_of(i)]);
-  auto key_of = [&](int i) { return cached ? s_key[i] : weight_key(ws[slot_of(i)]); };
+  const int held = min(live, a.cap);
+  for (int i = tid; i < held; i += T) s_key[i] = weight_key(ws[slot_of(i)]);
+  auto key_of = [&](int i) { return i < held ? s_key[i] : weight_key(ws[slot_of(i)]); };
   // the keep - protect largest of the entries behind the protected ones
   if (tid == 0) {
     s_prefix = 0u;
@@ -1795,14 +1795,14 @@ template <int D>
 static cudaError_t launch_evict(Kv4EvictArgs a, bool in_place, cudaStream_t st, bool pdl) {
   const dim3 grid(a.nh, a.rows, a.layers);
   if (in_place) {
-    cudaError_t e = launch_kernel(k_kv4_evict<D, true>, grid, dim3(kEvictThreads), 0, st, pdl, a);
+    cudaError_t e = launch_kernel(k_kv4_evict<D, true>, grid, dim3(kEvictThreads), (size_t)a.cap * 4, st, pdl, a);
     if (e == cudaSuccess) {
       k_kv4_hole<<<a.layers, kKv4MaxRows, 0, st>>>(a);
       e = cudaGetLastError();
     }
     return e;
   }
-  cudaError_t e = launch_kernel(k_kv4_evict<32, false>, grid, dim3(kEvictThreads), 0, st, pdl, a);
+  cudaError_t e = launch_kernel(k_kv4_evict<32, false>, grid, dim3(kEvictThreads), (size_t)a.cap * 4, st, pdl, a);
   const int per = 8 * kEvictPer;
   if (e == cudaSuccess && a.keep)
     e = launch_kernel(k_kv4_move<D>, dim3((a.keep + per - 1) / per, a.rows * a.nh, a.layers), dim3(256), 0, st, true, a);
@@ -1814,6 +1814,7 @@ cudaError_t launch_kv4_evict(const Kv4EvictArgs& args, cudaStream_t st, bool pdl
   bool in_place = false;
   for (int i = 0; i < a.rows; ++i) in_place = in_place || a.src[i] == a.dst[i];
   a.wide = ((uintptr_t)a.k_val | (uintptr_t)a.v_val) % 16 == 0;
+  a.cap = a.n <= 4096 ? 4096 : a.n <= kEvictKeys ? a.n : kEvictKeys;
   // the list holds list_cap slots: as many layers at a time
   const size_t per_layer = (size_t)a.rows * a.nh * (a.keep ? a.keep : 1);
   int group = (int)(a.list_cap / per_layer < (size_t)a.layers ? a.list_cap / per_layer : (size_t)a.layers);
@@ -1844,6 +1845,12 @@ cudaError_t init_kv4_attributes() {
   if (e == cudaSuccess) e = allow_max_dyn_smem(k_kv4_attn<D_, 2>);
   UOCR_A(32) UOCR_A(64) UOCR_A(128) UOCR_A(256)
 #undef UOCR_A
+  // (as many weights as fit, without a preference for shared memory: the move that follows wants the L1)
+#define UOCR_E(D_, MOVE_)                                                                                           \
+  if (e == cudaSuccess)                                                                                             \
+    e = cudaFuncSetAttribute(k_kv4_evict<D_, MOVE_>, cudaFuncAttributeMaxDynamicSharedMemorySize, kEvictKeys * 4);
+  UOCR_E(32, false) UOCR_E(32, true) UOCR_E(64, true) UOCR_E(128, true) UOCR_E(256, true)
+#undef UOCR_E
   if (e == cudaSuccess) e = init_kv4_prompt_attributes();
   return e;
 }

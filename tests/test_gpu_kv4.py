@@ -349,6 +349,28 @@ def test_evict_against_the_oracle(cuda, dim, P, n, keep, protect, in_place):
     ctx.close()
 
 
+@pytest.mark.parametrize("n,keep,protect", [(4097, 1500, 2), (20011, 40, 0), (49153, 30000, 1), (60007, 6001, 7)])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_evict_of_long_rows(cuda, n, keep, protect, in_place):
+    """More entries than shared memory holds weights of; many weights are equal."""
+    torch = cuda
+    rng = np.random.default_rng(n)
+    cfg = _cfg(head_dim=32, n_heads=2, prefix_len=n + 3, ring_len=1, max_rows=2, kv_track=1)
+    ctx = binding.Context(cfg, max_rows=2)
+    vals = _fill(ctx, cfg, rng)[0]
+    w = np.round(rng.random((2, 2, n + 4)) * 500).astype(np.float32)
+    _put_weights(torch, ctx, w)
+    rd = 0 if in_place else 1
+    kept, k, v = _evict(torch, ctx, cfg, 0, [0], [rd], n, keep, protect)
+    for h in range(2):
+        at = oracle.evict_choice(w[0, h, :n], n, keep, protect)
+        assert np.array_equal(kept[0, 0, h], at)
+        assert np.array_equal(k[0, 0, h], vals[0, 0, h, at]) and np.array_equal(v[0, 0, h], vals[0, 1, h, at])
+        assert np.array_equal(_weights(torch, ctx, cfg)[rd, h, :keep], w[0, h, at])
+        assert not np.any(_weights(torch, ctx, cfg)[rd, h, keep:n])
+    ctx.close()
+
+
 def test_attention_skips_what_is_evicted_and_evicts_again(cuda):
     torch = cuda
     rng = np.random.default_rng(8)
