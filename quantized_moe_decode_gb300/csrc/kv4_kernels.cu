@@ -498,7 +498,8 @@ cudaError_t launch_kv4_weights(const Kv4WeightsArgs& a, cudaStream_t st, bool pd
 //
 // What it cannot do without is the read of the entries (64 rows of 2176 slots, ten
 // heads of 128 dimensions: 223 MB, 33 us at the copy bandwidth).  Measured there,
-// device time of back-to-back calls: 48.7 us with an item a CTA, 52.5 with runs, of which
+// device time of back-to-back calls: 48.7 us with an item a CTA (57 with the weights'
+// accumulation, which reads the scores again), 52.5 with runs, of which
 // 6.5 pass before the first tiles are there (they are the first of the stream) and 5
 // from the last tile to the end of the merge; 57% of the issue slots and 59% of DRAM's
 // throughput over the whole launch.  More CTAs on an SM, deeper rings, other orders of
@@ -1433,7 +1434,7 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 // entry never moves up.  Bound by the scattered reads (a slot's values lie in
 // 16-byte pieces of its tile, half of a 32-byte sector each) and the writes: 12
 // layers of 8 rows, 701 of 3000 entries with their values, 10 heads of 128
-// dimensions take 154 us, 34 to select (0.7 of the issue slots) and 118 to move,
+// dimensions take 152 us, 34 to select (0.7 of the issue slots) and 118 to move,
 // whose 340 MB of reads and 401 of writes go at 6.2 TB/s.  Selecting and moving in
 // one kernel, so that the two overlap, took 156 to 170 us there and 50 to 64 where
 // the two take 46 (32 rows, one layer).

@@ -24,12 +24,12 @@
 // partials, which a second kernel merges.
 // What it cannot do without are those products, 4 M N K of them per block and pass:
 // about 1050 cycles of the tensor pipe for a block of 128 dimensions.  Measured, ten
-// heads of 128 dimensions, 2048 tokens from position 0 (18 blocks an SM): 41 us with
-// the merge, 7000 cycles until an item's first scores are there, 6000 to 8000 from one
-// item to the next; eight heads, 8192 tokens (219 blocks an SM): 258 us, 2200 cycles a
-// block.  There the roles wait for one another in turn: the values' warps take 1900 of
-// them, a softmax group 3300 for its two blocks, the issuing warp 1900; what they all
-// share is the SM's issue of instructions.
+// heads of 128 dimensions, 2048 tokens from position 0 (160 items, the longest 32
+// blocks): 40 us, 7000 cycles until an item's first scores are there, 6000 to 8000 from
+// one item to the next; eight heads, 8192 tokens (219 blocks an SM): 246 us, 2200
+// cycles a block.  There the roles wait for one another in turn: the values' warps take
+// 1900 of them, a softmax group 3300 for its two blocks, the issuing warp 1900; what
+// they all share is the SM's issue of instructions.
 #include "kv4_device.cuh"
 #include "launch.h"
 #include "tc_common.cuh"
