@@ -1434,14 +1434,17 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 // entry never moves up.  Bound by the scattered reads (a slot's values lie in
 // 16-byte pieces of its tile, half of a 32-byte sector each) and the writes: 12
 // layers of 8 rows, 701 of 3000 entries with their values, 10 heads of 128
-// dimensions take 152 us, 34 to select (0.7 of the issue slots) and 118 to move,
+// dimensions take 150 us, 34 to select (0.7 of the issue slots) and 116 to move,
 // whose 340 MB of reads and 401 of writes go at 6.2 TB/s.  Selecting and moving in
 // one kernel, so that the two overlap, took 156 to 170 us there and 50 to 64 where
 // the two take 46 (32 rows, one layer).
 constexpr int kEvictThreads = 512;
 constexpr int kEvictKeys = 49152;  // weights at most that are kept in shared memory between the passes (4 rows of
                                    // 20000 entries 104 -> 77 us against 4096 of them)
-constexpr int kEvictPer = 8;      // entries of a moving warp
+// Entries of a moving warp.  Eight and four, in us: 128 dimensions, 32 rows, 512 of 2048
+// entries 44.4 and 42.0, 12 layers of 8 rows, 701 of 3000 152 and 150; 32 dimensions, four
+// layers of 8 rows, 1500 of 3000 40.0 and 47.2; 64 dimensions 50.2 and 51.8.
+constexpr int evict_per(int D) { return D <= 64 ? 8 : 4; }
 
 // Four entries in a warp's registers: lane 8 e + i holds dimensions
 // [i D/8, (i+1) D/8) of entry e (for head_dim 32, keys: eight dimensions in each
@@ -1746,11 +1749,12 @@ __global__ void __launch_bounds__(kEvictThreads) k_kv4_evict(const Kv4EvictArgs 
     a.hole[(size_t)layer * a.MR + rd] = a.keep < a.n ? make_int2(a.keep, a.n) : make_int2(0, 0);
 }
 
-// Move the listed entries between rows: a warp takes kEvictPer of them, four at a
-// time, and has all loads of one round in flight before its stores.
+// Move the listed entries between rows: a warp takes evict_per of them, four at a
+// time, and has all loads of one round in flight before its stores.  Few entries a
+// warp and many warps: the loads are scattered, and latency is what there is to hide.
 template <int D>
-__global__ void __launch_bounds__(256) k_kv4_move(const Kv4EvictArgs a) {
-  constexpr int F = kEvictPer / 4, TB = kv4_tile_bytes(D);
+__global__ void __launch_bounds__(256, D <= 128 ? 8 : 6) k_kv4_move(const Kv4EvictArgs a) {
+  constexpr int PER = evict_per(D), F = PER / 4, TB = kv4_tile_bytes(D);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, e = lane >> 3, i = lane & 7;
   const int head = blockIdx.y % a.nh, r = blockIdx.y / a.nh, l = blockIdx.z, layer = a.layer0 + l;
   const size_t SLt = (size_t)a.tiles * kKv4Slots, out0 = (((size_t)l * a.rows + r) * a.nh + head) * a.keep;
@@ -1758,18 +1762,18 @@ __global__ void __launch_bounds__(256) k_kv4_move(const Kv4EvictArgs a) {
   const size_t row_bytes = (size_t)2 * a.nh * a.tiles * TB, voff = row_bytes / 2;
   const float* ws = a.wts + (((size_t)layer * a.MR + a.src[r]) * a.nh + head) * SLt;
   float* wd = a.wts + (((size_t)layer * a.MR + a.dst[r]) * a.nh + head) * SLt;
-  const int c0 = (blockIdx.x * 8 + warp) * kEvictPer;
+  const int c0 = (blockIdx.x * 8 + warp) * PER;
   pdl_launch_dependents();
   pdl_wait();
   if (c0 >= a.keep) return;
-  const int mine = c0 + lane < a.keep && lane < kEvictPer ? a.list[out0 + c0 + lane] : 0;
+  const int mine = c0 + lane < a.keep && lane < PER ? a.list[out0 + c0 + lane] : 0;
   Kv4Four<D> x[F];
 #pragma unroll
   for (int f = 0; f < F; ++f) {
     const int slot = __shfl_sync(0xffffffffu, mine, 4 * f + e);
     if (c0 + 4 * f + e < a.keep) x[f].load(base + a.src[r] * row_bytes, voff, slot, i);
   }
-  if (lane < kEvictPer && c0 + lane < a.keep) {
+  if (lane < PER && c0 + lane < a.keep) {
     wd[c0 + lane] = ws[mine];
     if (a.kept) a.kept[out0 + c0 + lane] = mine;
   }
@@ -1804,7 +1808,7 @@ static cudaError_t launch_evict(Kv4EvictArgs a, bool in_place, cudaStream_t st, 
     return e;
   }
   cudaError_t e = launch_kernel(k_kv4_evict<32, false>, grid, dim3(kEvictThreads), (size_t)a.cap * 4, st, pdl, a);
-  const int per = 8 * kEvictPer;
+  const int per = 8 * evict_per(D);
   if (e == cudaSuccess && a.keep)
     e = launch_kernel(k_kv4_move<D>, dim3((a.keep + per - 1) / per, a.rows * a.nh, a.layers), dim3(256), 0, st, true, a);
   return e;
