@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
 from array import array
 
 import numpy as np
@@ -53,10 +54,9 @@ class uocr_tensor(C.Structure):
                 ("rows", C.c_int32), ("cols", C.c_int32), ("data", C.c_void_p), ("bytes", C.c_uint64)]
 
 
-class uocr_qkv(C.Structure):
-    _fields_ = [("q", C.c_void_p), ("k", C.c_void_p), ("v", C.c_void_p), ("ld_q", C.c_int64), ("ld_k", C.c_int64),
-                ("ld_v", C.c_int64), ("dtype", C.c_int32), ("q_heads", C.c_int32), ("q_out", C.c_void_p),
-                ("k_val", C.c_void_p), ("v_val", C.c_void_p)]
+# struct uocr_qkv, packed (a ctypes structure takes five times as long to fill):
+# q, k, v, ld_q, ld_k, ld_v, dtype, q_heads, q_out, k_val, v_val
+uocr_qkv = struct.Struct("PPPqqqiiPPP")
 
 
 class uocr_mem_report(C.Structure):
@@ -103,8 +103,8 @@ def load(path: str = LIB_PATH):
         "uocr_project": ([P, I, P, P], I),
         "uocr_kv_write_i4": ([P, I, I, I, I, P, P, P, P, P, P], I),
         "uocr_kv_read_i4": ([P, I, I, I, I, P, P, P, P, P, P], I),
-        "uocr_kv_append": ([P, I, I, P, C.POINTER(uocr_qkv)], I),
-        "uocr_kv_append_chunk": ([P, I, I, I, I, C.POINTER(uocr_qkv)], I),
+        "uocr_kv_append": ([P, I, I, P, C.c_char_p], I),
+        "uocr_kv_append_chunk": ([P, I, I, I, I, C.c_char_p], I),
         "uocr_attend": ([P, I, I, P, I, P, I, P], I),
         "uocr_attend_chunk": ([P, I, I, I, I, I, P, I, P], I),
         "uocr_kv_evict": ([P, I, I, P, P, I, I, I, P, P, P], I),
@@ -258,13 +258,13 @@ class Context:
 
     def uocr_kv_append(self, layer, rows, pos_ptr, q_ptr, k_ptr, v_ptr, *, dtype=DT_F16, q_heads=0, ld_q=0, ld_k=0,
                        ld_v=0, q_out=0, k_val=0, v_val=0):
-        x = uocr_qkv(q_ptr, k_ptr, v_ptr, ld_q, ld_k, ld_v, dtype, q_heads, q_out, k_val, v_val)
-        self._ck(self.lib.uocr_kv_append(self.h, layer, rows, pos_ptr or None, C.byref(x)))
+        x = uocr_qkv.pack(q_ptr or 0, k_ptr or 0, v_ptr or 0, ld_q, ld_k, ld_v, dtype, q_heads, q_out or 0, k_val or 0, v_val or 0)
+        self._ck(self.lib.uocr_kv_append(self.h, layer, rows, pos_ptr or None, x))
 
     def uocr_kv_append_chunk(self, layer, row, start_pos, n, q_ptr, k_ptr, v_ptr, *, dtype=DT_F16, q_heads=0, ld_q=0,
                              ld_k=0, ld_v=0, q_out=0, k_val=0, v_val=0):
-        x = uocr_qkv(q_ptr, k_ptr, v_ptr, ld_q, ld_k, ld_v, dtype, q_heads, q_out, k_val, v_val)
-        self._ck(self.lib.uocr_kv_append_chunk(self.h, layer, row, start_pos, n, C.byref(x)))
+        x = uocr_qkv.pack(q_ptr or 0, k_ptr or 0, v_ptr or 0, ld_q, ld_k, ld_v, dtype, q_heads, q_out or 0, k_val or 0, v_val or 0)
+        self._ck(self.lib.uocr_kv_append_chunk(self.h, layer, row, start_pos, n, x))
 
     def uocr_attend(self, layer, rows, pos_ptr, q_heads, q_ptr, out_ptr, out_dtype=DT_F16):
         self._ck(self.lib.uocr_attend(self.h, layer, rows, pos_ptr or None, q_heads, q_ptr or None, out_dtype,
